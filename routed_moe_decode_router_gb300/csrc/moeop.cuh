@@ -1,0 +1,99 @@
+// moeop.cuh -- what the FP8 layer operators' translation units share:
+// parameter blocks, launchers, the device status word and e4m3 packing.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_ops.h"
+
+namespace moe {
+
+moe_status set_error(moe_status s, const char *msg);  // moe_api.cu
+
+namespace op {
+
+constexpr float kFp8Max = 448.f;   // largest finite e4m3 value
+constexpr float kFp8Tiny = 1e-30f; // least magnitude a scale is made of
+
+struct NormParams {
+    const void *x, *residual, *weight;
+    int64_t x_stride, residual_stride;
+    int rows, hidden, dtype;
+    float eps;
+    void *y, *residual_out;
+    uint8_t *q;
+    float *scales;
+};
+cudaError_t launch_rms_norm(const NormParams &p, bool vec, cudaStream_t st);
+
+struct RouteParams {
+    moeop_route_config c;
+    const void *logits;
+    int64_t stride;
+    const float *bias;
+    int rows;
+    int32_t *ids;
+    float *wts;
+};
+cudaError_t launch_route_topk(const RouteParams &p, cudaStream_t st);
+
+// One FP8 matrix as the products read it: 128-byte columns of whole rows.
+struct Fp8Mat {
+    const uint8_t *p;
+    int64_t rows, k, stride;
+};
+cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b, const float *sb,
+                              void *out, int out_dtype, cudaStream_t st);
+
+// Workspace of moeop_experts_fp8: the pairs (row, slot) in expert order, the
+// tiles of 128 of them, the FP8 rows h and the products y.
+struct ExpertsWs {
+    size_t header, tiles, pair, token, h, h_scales, y, total;
+    int max_tiles;
+    static ExpertsWs make(const moeop_experts_config &c, int rows) {
+        auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+        ExpertsWs w{};
+        const size_t P = (size_t)rows * c.top_k;
+        const size_t full = P / 128 + c.num_experts;
+        w.max_tiles = (int)(P < full ? P : full);
+        size_t o = 0;
+        w.header = o, o += 256;
+        w.tiles = o, o += up((size_t)w.max_tiles * 16);
+        w.pair = o, o += up(P * 4);
+        w.token = o, o += up(P * 4);
+        w.h = o, o += up(P * c.inter);
+        w.h_scales = o, o += up(P * (c.inter / 128) * 4);
+        w.y = o, o += up(P * c.hidden * 2);
+        w.total = o;
+        return w;
+    }
+};
+struct ExpertsArgs {
+    moeop_experts_config c;
+    moeop_experts_weights w;
+    const uint8_t *q;
+    const float *scales;
+    const int32_t *ids;
+    const float *wts;
+    const uint16_t *addend;
+    uint16_t *out;
+    int rows;
+    char *ws;
+};
+cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st);
+
+cudaError_t status_word(uint32_t **p);  // the current device's status word
+
+#ifdef __CUDACC__
+// Four values -> four e4m3 codes, nearest even, beyond +-448 the largest.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+#endif
+
+}  // namespace op
+}  // namespace moe

@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in include/moe_router.h (argument marshalling
-only: every step of the layer runs in the CUDA library).
+"""ctypes binding of the C ABI in include/moe_router.h and include/moe_ops.h
+(argument marshalling only: every step runs in the CUDA library).
 
 The library is loaded from the package's in-tree build folder
 (_build/libmoe_router.so).  If it has not been built, every call raises
@@ -21,6 +21,9 @@ MOE_STATIC_WORKSPACE_BYTES = 10 << 20
 MOE_SCORING_SOFTMAX, MOE_SCORING_SIGMOID = 0, 1
 MOE_ROUTER_BF16, MOE_ROUTER_NVFP4 = 0, 1
 MOE_EXPERT_NVFP4, MOE_EXPERT_FP8, MOE_EXPERT_BF16 = 0, 1, 2
+MOEOP_BLOCK = 128
+MOEOP_BF16, MOEOP_FP16, MOEOP_FP32 = 0, 1, 2
+MOEOP_GROUP_MAX, MOEOP_GROUP_TOP2 = 0, 1
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_STATUS"}
@@ -73,10 +76,32 @@ class UnionTable(C.Structure):
                 ("uslot", (C.c_uint8 * MOE_MAX_ROWS) * MOE_MAX_IDS)]
 
 
+class RouteConfig(C.Structure):
+    _fields_ = [("num_experts", C.c_int), ("top_k", C.c_int), ("scoring", C.c_int),
+                ("groups", C.c_int), ("group_limit", C.c_int), ("group_score", C.c_int),
+                ("norm_topk_prob", C.c_int), ("routed_scaling_factor", C.c_float),
+                ("dtype", C.c_int)]
+
+
+class ExpertsConfig(C.Structure):
+    _fields_ = [("hidden", C.c_int), ("inter", C.c_int), ("num_experts", C.c_int),
+                ("top_k", C.c_int)]
+
+
+class ExpertsWeights(C.Structure):
+    _fields_ = [("gate", C.c_void_p), ("up", C.c_void_p), ("down", C.c_void_p),
+                ("gate_scales", C.c_void_p), ("up_scales", C.c_void_p),
+                ("down_scales", C.c_void_p)]
+
+
 EXPORTS = ("moe_abi_version", "moe_last_error", "moe_check_config",
            "moe_workspace_size", "moe_workspace_init", "moe_route", "moe_union",
            "moe_forward", "moe_forward_timed", "moe_read_routing",
            "moe_read_device_status", "moe_forward_static", "moe_nvfp4_to_t_layout")
+
+OPS_EXPORTS = ("moeop_rms_norm", "moeop_route_topk", "moeop_matmul_fp8",
+               "moeop_experts_workspace_size", "moeop_experts_fp8",
+               "moeop_read_device_status")
 
 _lib = None
 _lock = threading.Lock()
@@ -119,8 +144,17 @@ def lib():
         L.moe_forward_static.argtypes = [C.POINTER(MoeConfig), C.POINTER(MoeWeights),
                                          vp, vp, i, vp]
         L.moe_nvfp4_to_t_layout.argtypes = [vp, vp, i, i, i, vp, vp, vp]
-        for name in EXPORTS[2:]:
-            if name != "moe_workspace_size":
+        i64 = C.c_int64
+        L.moeop_rms_norm.argtypes = [vp, i64, vp, i64, vp, i, i, i, C.c_float, vp, vp, vp, vp, vp]
+        L.moeop_route_topk.argtypes = [C.POINTER(RouteConfig), vp, i64, vp, i, vp, vp, vp]
+        L.moeop_matmul_fp8.argtypes = [vp, i64, vp, vp, i64, vp, i, i, i, vp, i, vp]
+        L.moeop_experts_workspace_size.restype = sz
+        L.moeop_experts_workspace_size.argtypes = [C.POINTER(ExpertsConfig), i]
+        L.moeop_experts_fp8.argtypes = [C.POINTER(ExpertsConfig), C.POINTER(ExpertsWeights), vp,
+                                        vp, vp, vp, vp, vp, i, vp, sz, vp]
+        L.moeop_read_device_status.argtypes = [C.POINTER(C.c_int), vp]
+        for name in EXPORTS[2:] + OPS_EXPORTS:
+            if not name.endswith("workspace_size"):
                 getattr(L, name).restype = i
         _lib = L
         return L
@@ -204,6 +238,50 @@ def moe_nvfp4_to_t_layout(packed: int, scales: int, count: int, n_out: int, k_in
 def moe_read_device_status(ws: int, ws_bytes: int, stream: int = 0) -> int:
     code = C.c_int(0)
     st = lib().moe_read_device_status(ws, ws_bytes, C.byref(code), stream)
+    if st not in (0, 5):
+        _check(st)
+    return code.value
+
+
+# ---------------------------------------------------------------------------
+# The entry points of moe_ops.h, one-to-one
+# ---------------------------------------------------------------------------
+
+def moeop_rms_norm(x: int, x_stride: int, residual: int, residual_stride: int, weight: int,
+                   rows: int, hidden: int, dtype: int, eps: float, y: int, residual_out: int,
+                   q: int, scales: int, stream: int = 0):
+    _check(lib().moeop_rms_norm(x, x_stride, residual, residual_stride, weight, rows, hidden,
+                                dtype, eps, y, residual_out, q, scales, stream))
+
+
+def moeop_route_topk(cfg, logits: int, logits_stride: int, bias: int, rows: int, ids: int,
+                     wts: int, stream: int = 0):
+    _check(lib().moeop_route_topk(C.byref(cfg), logits, logits_stride, bias, rows, ids, wts,
+                                  stream))
+
+
+def moeop_matmul_fp8(a: int, a_stride: int, a_scales: int, b: int, b_stride: int, b_scales: int,
+                     m: int, n: int, k: int, out: int, out_dtype: int, stream: int = 0):
+    _check(lib().moeop_matmul_fp8(a, a_stride, a_scales, b, b_stride, b_scales, m, n, k, out,
+                                  out_dtype, stream))
+
+
+def moeop_experts_workspace_size(cfg: ExpertsConfig, rows: int) -> int:
+    n = lib().moeop_experts_workspace_size(C.byref(cfg), rows)
+    if n == 0:
+        raise MoeError(1, lib().moe_last_error().decode())
+    return n
+
+
+def moeop_experts_fp8(cfg, w, q: int, scales: int, ids: int, wts: int, addend: int, out: int,
+                      rows: int, ws: int, ws_bytes: int, stream: int = 0):
+    _check(lib().moeop_experts_fp8(C.byref(cfg), C.byref(w), q, scales, ids, wts, addend, out,
+                                   rows, ws, ws_bytes, stream))
+
+
+def moeop_read_device_status(stream: int = 0) -> int:
+    code = C.c_int(0)
+    st = lib().moeop_read_device_status(C.byref(code), stream)
     if st not in (0, 5):
         _check(st)
     return code.value
