@@ -8,19 +8,21 @@
 // before the next block is added: an A tile of 128 rows and a B tile of NB x
 // 128 outputs are multiplied block by block into one of two halves of tensor
 // memory (four MMAs of 32 inputs), and while the next block runs into the
-// other half, eight warps read the finished one and add it, scaled, to fp32
-// accumulators in registers (128 per thread for NB = 2).
+// other half, sixteen warps read the finished one and add it, scaled, to fp32
+// accumulators in registers (64 per thread for NB = 2).
 //
-// Roles: warp 8 loads (TMA, 128-byte swizzle, a ring of kStages), warp 9
-// issues the MMAs, warps 0-7 accumulate and store.  Warp w reads lanes
-// 32 (w % 4) .. + 31 (rows) and, of each 128-output block, columns
-// 64 (w / 4) .. + 63, so that in the gate/up form a thread holds a gate value
-// and the up value of the same column.
+// Roles: warps 0-15 accumulate and store, warp 16 loads (TMA, 128-byte
+// swizzle, a ring of 4 or 6 stages) with warps 18 and 19 where rows are
+// gathered, warp 17 issues the MMAs.  Warp w reads lanes 32 (w % 4) .. + 31
+// (rows) and, of each 128-output block, columns 32 (w / 4) .. + 31, so that
+// in the gate/up form a thread holds a gate value and the up value of the
+// same column.
 //
 // Blocks are persistent over the tiles.  Where there are fewer tiles than
-// SMs the inputs are split over a cluster of S blocks, whose partial sums are
-// added through distributed shared memory in rank order: the result does not
-// depend on timing.
+// SMs the inputs are split over a cluster of S blocks.  Each 32 rows belong
+// to one rank, into whose (by then idle) ring the others write their partial
+// sums, and which adds them in rank order: the result does not depend on
+// timing.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,7 +41,11 @@ __device__ uint32_t g_status;
 namespace {
 
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
-constexpr int kThreads = 320;
+constexpr int kColGroups = 4, kCols = 128 / kColGroups;  // of a 128-output block
+constexpr int kAccWarps = 4 * kColGroups, kLoadWarp = kAccWarps, kMmaWarp = kAccWarps + 1;
+constexpr int kThreads = (kAccWarps + 4) * 32;
+constexpr int kBoxRows = 32;      // rows of A in one copy
+constexpr int kMaxSplit = 7;      // six other ranks' sums of 32 rows fill the ring
 constexpr int kTile = 128 * 128;  // bytes of one operand tile
 
 template <int NB>
@@ -77,6 +83,12 @@ __device__ __forceinline__ Tile tile_at(const Params &p, int t) {
     if (MODE == kDense) return {0, mt * 128, min(128, p.rows - mt * 128), nt};
     const int4 d = __ldcg(p.tiles + mt);
     return {d.x, d.y, d.z, nt};
+}
+
+// A scale of the A rows; h's were written by the kernel before.
+template <int MODE>
+__device__ __forceinline__ float ld_scale(const float *p) {
+    return MODE == kDown ? __ldcg(p) : __ldg(p);
 }
 
 // 16 consecutive outputs of one row.
@@ -124,25 +136,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kStage = (1 + NB) * kTile;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[S], empty[S], tm_full[2], tm_empty[2];
-    __shared__ float amax_s[2][128];
+    __shared__ float amax_s[kColGroups][128], sa_s[2][8][128], sb_s[2][8][NB];
     __shared__ uint32_t tm_base;
     __shared__ int abort_s;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&tm_full[i], 1), mbar_init(&tm_empty[i], 8);
+        // a stage is free again when its MMAs are complete and, with three
+        // loading warps, the other two are past it: none can be lapped
+        for (int i = 0; i < S; ++i)
+            mbar_init(&full[i], 1), mbar_init(&empty[i], MODE == kGateUp ? 3 : 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&tm_full[i], 1), mbar_init(&tm_empty[i], kAccWarps);
         abort_s = 0;
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kLoadWarp && elect_one()) {
         tma_prefetch_map(&ma);
         tma_prefetch_map(&mb);
         if (MODE == kGateUp) tma_prefetch_map(&mb2);
     }
-    if (warp == 9) tmem_alloc(&tm_base, 256 * NB);
+    if (warp == kMmaWarp) tmem_alloc(&tm_base, 256 * NB);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -153,76 +168,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int total = tile_count<MODE>(p);
     int syncs = 0;  // of this thread with its cluster: two in every split block
 
-    if (warp == 8) {
-        // ---- loads
+    if (warp >= kLoadWarp && warp != kMmaWarp) {
+        // ---- loads: warp 16 the weights and contiguous rows of A, the
+        // gathered rows split over warps 16, 18 and 19
+        const int part = warp == kLoadWarp ? 0 : warp - kMmaWarp;
         int it = 0;
         bool ok = true;
-        for (int t = first; t < total && ok; t += step) {
+        for (int t = first; t < total && ok && (MODE == kGateUp || part == 0); t += step) {
             const Tile T = tile_at<MODE>(p, t);
+            const int e = uniform(T.e), pos = uniform(T.pos), rows = uniform(T.rows);
+            const int quads = (rows + 3) / 4, boxes = (rows + kBoxRows - 1) / kBoxRows;
             int4 rows4 = make_int4(0, 0, 0, 0);
-            if (MODE != kDense) {
-                // rows 4 lane .. + 3 of the tile; past its end the last row again
+            if (MODE == kGateUp) {
+                // tokens of rows 4 lane .. + 3; past the end the last one again
                 int *r = &rows4.x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = T.pos + min(4 * lane + i, T.rows - 1);
-                    r[i] = MODE == kGateUp ? __ldcg(p.token + pos) : pos;
-                }
+                for (int i = 0; i < 4; ++i)
+                    r[i] = __ldcg(p.token + pos + min(4 * lane + i, rows - 1));
             }
-            const int b0 = (MODE == kGateUp ? T.e * p.n : MODE == kDown ? T.e * p.n : 0) +
-                           T.nt * (MODE == kGateUp ? 128 : 128 * NB);
-            const uint32_t bytes =
-                NB * kTile + (MODE == kDense ? kTile : (T.rows + 3) / 4 * 512);
-            for (int b = kb0; b < kb1 && ok; ++b, ++it) {
+            const int b0 = e * p.n + T.nt * (MODE == kGateUp ? 128 : 128 * NB);
+            const uint32_t bytes = NB * kTile + (MODE == kGateUp ? quads * 512
+                                                                 : boxes * kBoxRows * 128);
+            for (int b = kb0; b < kb1; ++b, ++it) {
                 const int s = it % S;
                 ok = __all_sync(~0u, wait_bar(&empty[s], (it / S & 1) ^ 1, &abort_s));
                 if (!ok) break;
                 const uint32_t dst = ring + s * kStage;
-                if (lane == 0) {
+                if (part == 0 && elect_one()) {
                     mbar_arrive_expect_tx(&full[s], bytes);
-                    if (MODE == kDense) tma_box(dst, &ma, b * 128, T.pos, &full[s]);
                     tma_box(dst + kTile, &mb, b * 128, b0, &full[s]);
                     if (NB == 2)
                         tma_box(dst + 2 * kTile, MODE == kGateUp ? &mb2 : &mb, b * 128,
                                 MODE == kGateUp ? b0 : b0 + 128, &full[s]);
+                    if (MODE != kGateUp)
+                        for (int i = 0; i < boxes; ++i)
+                            tma_box(dst + i * kBoxRows * 128, &ma, b * 128, pos + i * kBoxRows,
+                                    &full[s]);
                 }
                 __syncwarp();
-                if (MODE != kDense && 4 * lane < T.rows)
-                    tma_gather4(dst + lane * 512, &ma, b * 128, rows4, &full[s]);
+                if (MODE == kGateUp)
+                    for (int i = part; i < quads; i += 3) {
+                        const int4 r = make_int4(
+                            __shfl_sync(~0u, rows4.x, i), __shfl_sync(~0u, rows4.y, i),
+                            __shfl_sync(~0u, rows4.z, i), __shfl_sync(~0u, rows4.w, i));
+                        if (elect_one()) tma_gather4(dst + i * 512, &ma, b * 128, r, &full[s]);
+                    }
+                if (part && elect_one()) mbar_arrive(&empty[s]);
             }
         }
-        if (!ok && lane == 0)  // copies in flight end before the block does
+        if (!ok && part == 0)  // copies in flight end before the block does
             for (int i = it > S ? it - S : 0; i < it; ++i)
                 mbar_wait(&full[i % S], i / S & 1);
-    } else if (warp == 9) {
+    } else if (warp == kMmaWarp) {
         // ---- MMAs
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc_idesc(128, 128 * NB);
-            int it = 0;
-            bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                for (int b = kb0; b < kb1; ++b, ++it) {
-                    const int s = it % S, buf = it & 1;
-                    ok = wait_bar(&tm_empty[buf], (it / 2 & 1) ^ 1, &abort_s) &&
-                         wait_bar(&full[s], it / S & 1, &abort_s);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t da = tc_desc(ring + s * kStage);
-                    const uint64_t db = tc_desc(ring + s * kStage + kTile);
+        constexpr uint32_t idesc = tc_idesc(128, 128 * NB);
+        int it = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += step) {
+            for (int b = kb0; b < kb1; ++b, ++it) {
+                const int s = it % S, buf = it & 1;
+                ok = __all_sync(~0u, wait_bar(&tm_empty[buf], (it / 2 & 1) ^ 1, &abort_s) &&
+                                         wait_bar(&full[s], it / S & 1, &abort_s));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t da = tc_desc(ring + s * kStage);
+                const uint64_t db = tc_desc(ring + s * kStage + kTile);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc_mma_e4m3(tm + buf * 128 * NB, da + 2 * k, db + 2 * k, idesc, k > 0);
                     tc_commit(&empty[s]);
                     tc_commit(&tm_full[buf]);
                 }
+                __syncwarp();
             }
         }
-        __syncwarp();
     } else {
         // ---- accumulation and stores
+        // The scales of 8 input blocks at a time go through shared memory: a
+        // row's are contiguous in memory, so a load by rows touches 32 lines.
         const int wg = warp / 4, r = (warp % 4) * 32 + lane;
-        const uint32_t tm_lane = tm + ((uint32_t)(warp % 4) * 32 << 16) + wg * 64;
-        int it = 0;
+        const uint32_t tm_lane = tm + ((uint32_t)(warp % 4) * 32 << 16) + wg * kCols;
+        int it = 0, half = 0;
         bool ok = true;  // false: an earlier wait gave up; nothing is stored any more
         for (int t = first; t < total; t += step) {
             const Tile T = tile_at<MODE>(p, t);
@@ -230,80 +257,112 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int arow = MODE == kGateUp ? (live ? __ldcg(p.token + T.pos + r) : 0)
                                              : T.pos + (live ? r : 0);
             const float *sa = p.sa + (size_t)arow * p.kb;
-            const int nb0 = MODE == kGateUp ? T.nt : T.nt * NB;
-            const int nb1 = MODE == kGateUp ? nb0 : min(nb0 + NB - 1, p.nblocks - 1);
-            const size_t eb = MODE == kDense ? 0 : (size_t)T.e * p.nblocks;
-            const float *sb0 = p.sb + (eb + nb0) * p.kb;
-            const float *sb1 = (MODE == kGateUp ? p.sb2 : p.sb) + (eb + nb1) * p.kb;
-            uint64_t acc[32 * NB];
+            // this thread's part of the B scales: thread (wg 0, r < 8 NB)
+            // fetches block r / 8's, input block r % 8
+            const int nb = MODE == kGateUp ? T.nt : min(T.nt * NB + r / 8, p.nblocks - 1);
+            const float *sb = (MODE == kGateUp && r >= 8 ? p.sb2 : p.sb) +
+                              ((size_t)T.e * p.nblocks + nb) * p.kb;
+            constexpr int kAcc = kCols / 2 * NB;  // pairs of this thread's sums
+            uint64_t acc[kAcc];
 #pragma unroll
-            for (int i = 0; i < 32 * NB; ++i) acc[i] = 0;
-            float a_next = 0.f, b0_next = 0.f, b1_next = 0.f;
-            if (kb0 < kb1 && some) {
-                a_next = MODE == kDown ? __ldcg(sa + kb0) : __ldg(sa + kb0);
-                b0_next = __ldg(sb0 + kb0);
-                if (NB == 2) b1_next = __ldg(sb1 + kb0);
-            }
-            for (int b = kb0; b < kb1; ++b, ++it) {
-                const int buf = it & 1;
-                const float s0 = a_next * b0_next, s1 = a_next * b1_next;
-                if (b + 1 < kb1 && some) {
-                    a_next = MODE == kDown ? __ldcg(sa + b + 1) : __ldg(sa + b + 1);
-                    b0_next = __ldg(sb0 + b + 1);
-                    if (NB == 2) b1_next = __ldg(sb1 + b + 1);
+            for (int i = 0; i < kAcc; ++i) acc[i] = 0;
+            constexpr int kPer = 8 / kColGroups;
+            float as[kPer], bs = 0.f;
+            auto fetch = [&](int b) {  // scales of the 8 input blocks from b on
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int j = b + wg * kPer + i;
+                    as[i] = live && j < kb1 ? ld_scale<MODE>(sa + j) : 0.f;
                 }
+                if (wg == 0 && r < 8 * NB) bs = b + r % 8 < kb1 ? __ldg(sb + b + r % 8) : 0.f;
+            };
+            fetch(kb0);
+            for (int b = kb0; b < kb1; ++b, ++it) {
+                const int buf = it & 1, j = (b - kb0) & 7;
+                if (j == 0) {
+                    // A warp may still read the other half; nobody reads this
+                    // one, for all have met since it was in use.
+                    half ^= 1;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) sa_s[half][wg * kPer + i][r] = as[i];
+                    if (wg == 0 && r < 8 * NB) sb_s[half][r % 8][r / 8] = bs;
+                    named_bar(1, kAccWarps * 32);
+                    if (b + 8 < kb1) fetch(b + 8);
+                }
+                const float a = sa_s[half][j][r];
+                const float s0 = a * sb_s[half][j][0], s1 = a * sb_s[half][j][NB - 1];
                 if (ok) ok = __all_sync(~0u, wait_bar(&tm_full[buf], it / 2 & 1, &abort_s));
                 tc_fence_after();
                 if (some && ok) {
                     const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
+                    // 16 columns at a time, the next ones under way meanwhile
+                    constexpr int kChunks = kCols / 16 * NB;
+                    uint32_t v[2][16];
+                    const uint32_t from = tm_lane + buf * 128 * NB;
+                    tmem_load16(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 2 * NB; ++c) {
-                        uint32_t v[32];
-                        tmem_load32(tm_lane + buf * 128 * NB + (c / 2) * 128 + (c % 2) * 32, v);
+                    for (int c = 0; c < kChunks; ++c) {
+                        tmem_wait16(v[c & 1]);
+                        if (c + 1 < kChunks)
+                            tmem_load16(from + (c + 1) / (kCols / 16) * 128 +
+                                            (c + 1) % (kCols / 16) * 16,
+                                        v[(c + 1) & 1]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            fma2(acc[c * 16 + i], v[2 * i], v[2 * i + 1], c < 2 ? p0 : p1);
+                        for (int i = 0; i < 8; ++i)
+                            fma2(acc[c * 8 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1],
+                                 c < kCols / 16 ? p0 : p1);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tm_empty[buf]);
             }
+            bool mine = live && ok;  // this thread stores its row
             if (p.split > 1) {
-                // Every load and MMA of this block is complete (the last
-                // tm_full), so the ring holds the partial sums now; one tile
-                // per cluster.
-                float *part = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
-                if (rank && some && ok)
-#pragma unroll
-                    for (int i = 0; i < 32 * NB; ++i) {
-                        const float2 f = unpack2(acc[i]);
-                        const int col = (i / 32) * 128 + wg * 64 + (i % 32) * 2;
-                        part[col * 128 + r] = f.x;
-                        part[(col + 1) * 128 + r] = f.y;
-                    }
+                // One tile per cluster.  After the first meeting every load
+                // and MMA of the cluster is complete (each warp has seen its
+                // last tm_full) and the rings are free; buffer q of a ring
+                // holds the sums of the q-th other rank, column by column.
+                const int block = warp % 4, owner = block % p.split;
+                constexpr uint32_t kBuf = 128 * NB * 32 * 4;
+                const uint32_t slot = (block / p.split * (p.split - 1)) * kBuf +
+                                      (wg * kCols * 32 + lane) * 4;
                 cluster_sync();
-                if (rank == 0 && some && ok)
-                    for (int q = 1; q < p.split; ++q) {
-                        const uint32_t remote = map_rank(ring, q) + r * 4;
+                if (rank != owner && some && ok) {
+                    const uint32_t to =
+                        map_rank(ring, owner) + slot + (rank - (rank > owner)) * kBuf;
 #pragma unroll
-                        for (int i = 0; i < 32 * NB; ++i) {
-                            const int col = (i / 32) * 128 + wg * 64 + (i % 32) * 2;
-                            const float2 f = unpack2(acc[i]);
-                            acc[i] = pack2(f.x + ld_cluster(remote + col * 512),
-                                           f.y + ld_cluster(remote + (col + 1) * 512));
-                        }
+                    for (int i = 0; i < kAcc; ++i) {
+                        const float2 f = unpack2(acc[i]);
+                        const uint32_t at =
+                            to + ((i / (kCols / 2)) * 128 + (i % (kCols / 2)) * 2) * 128;
+                        st_cluster(at, f.x);
+                        st_cluster(at + 128, f.y);
                     }
+                }
                 cluster_sync();
                 syncs = 2;
-                if (rank) break;
+                mine = mine && rank == owner;
+                if (rank == owner && some && ok) {
+                    const float *part = reinterpret_cast<const float *>(
+                        smem_raw + (ring - smem_u32(smem_raw)) + slot);
+                    for (int q = 0; q < p.split - 1; ++q, part += kBuf / 4)
+#pragma unroll
+                        for (int i = 0; i < kAcc; ++i) {
+                            const float2 f = unpack2(acc[i]);
+                            const int at =
+                                ((i / (kCols / 2)) * 128 + (i % (kCols / 2)) * 2) * 32;
+                            acc[i] = pack2(f.x + part[at], f.y + part[at + 32]);
+                        }
+                }
             }
             if (MODE == kGateUp) {
                 float amax = 0.f;
                 if (some) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float2 g = unpack2(acc[i]), u = unpack2(acc[i + 32 * (NB - 1)]);
+                    for (int i = 0; i < kCols / 2; ++i) {
+                        const float2 g = unpack2(acc[i]);
+                        const float2 u = unpack2(acc[i + kCols / 2 * (NB - 1)]);
                         const float h0 = __fdividef(g.x, 1.f + __expf(-g.x)) * u.x;
                         const float h1 = __fdividef(g.y, 1.f + __expf(-g.y)) * u.y;
                         acc[i] = pack2(h0, h1);
@@ -311,14 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 amax_s[wg][r] = amax;
-                named_bar(1, 256);
-                amax = fmaxf(fmaxf(amax_s[0][r], amax_s[1][r]), kFp8Tiny);
-                named_bar(1, 256);  // before the next tile writes amax_s
-                if (live && ok) {
-                    const float up = kFp8Max / amax;
-                    const size_t at = (size_t)(T.pos + r) * p.n + T.nt * 128 + wg * 64;
+                named_bar(1, kAccWarps * 32);
+                amax = kFp8Tiny;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kColGroups; ++i) amax = fmaxf(amax, amax_s[i][r]);
+                named_bar(1, kAccWarps * 32);  // before the next tile writes amax_s
+                if (mine) {
+                    const float up = kFp8Max / amax;
+                    const size_t at = (size_t)(T.pos + r) * p.n + T.nt * 128 + wg * kCols;
+#pragma unroll
+                    for (int i = 0; i < kCols / 16; ++i) {
                         uint32_t q[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -332,12 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (wg == 0)
                         p.h_scales[(size_t)(T.pos + r) * (p.n / 128) + T.nt] = amax / kFp8Max;
                 }
-            } else if (live && ok) {
+            } else if (mine) {
                 const size_t orow = MODE == kDown ? (size_t)__ldcg(p.pair + T.pos + r)
                                                   : (size_t)(T.pos + r);
 #pragma unroll
-                for (int c = 0; c < 4 * NB; ++c) {
-                    const int col = (T.nt * NB + c / 4) * 128 + wg * 64 + (c % 4) * 16;
+                for (int c = 0; c < kCols / 16 * NB; ++c) {
+                    const int col = (T.nt * NB + c / (kCols / 16)) * 128 + wg * kCols +
+                                    (c % (kCols / 16)) * 16;
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -357,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; syncs < 2; ++syncs) cluster_sync();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_free(tm, 256 * NB);
+    if (warp == kMmaWarp) tmem_free(tm, 256 * NB);
     if (threadIdx.x == 0 && abort_s) atomicCAS(&g_status, 0u, (uint32_t)MOE_DEV_WAIT_TIMEOUT);
 }
 
@@ -493,8 +555,23 @@ std::mutex g_mu;
 EncodeFn g_encode = nullptr;
 struct Dev {
     int sms = 0;
+    int clusters[kMaxSplit + 1] = {};  // clusters of a size that run at a time
     uint32_t *status = nullptr;
 } g_devs[64];
+
+// A launch of `grid` blocks in clusters of `size`.
+void cluster_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *at, int grid, int size,
+                    int threads, size_t smem, cudaStream_t st) {
+    cfg->gridDim = dim3(grid);
+    cfg->blockDim = dim3(threads);
+    cfg->dynamicSmemBytes = smem;
+    cfg->stream = st;
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = size;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cfg->attrs = at;
+    cfg->numAttrs = 1;
+}
 
 template <int MODE, int NB>
 cudaError_t allow_smem() {
@@ -530,6 +607,14 @@ cudaError_t device(Dev **out) {
             (e = allow_smem<kDown, 2>()) != cudaSuccess ||
             (e = cudaGetSymbolAddress(&sym, g_status)) != cudaSuccess)
             return e;
+        for (int s = 2; s <= kMaxSplit; ++s) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute at[1];
+            cluster_config(&cfg, at, s * v.sms, s, kThreads, ring_bytes<2>() + 1024, nullptr);
+            if ((e = cudaOccupancyMaxActiveClusters(&v.clusters[s], gemm_kernel<kGateUp, 2>,
+                                                    &cfg)) != cudaSuccess)
+                return e;
+        }
         v.status = static_cast<uint32_t *>(sym);
     }
     *out = &v;
@@ -554,28 +639,20 @@ template <int MODE, int NB>
 cudaError_t launch(const TensorMap &ma, const TensorMap &mb, const TensorMap &mb2, const Params &p,
                    int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = ring_bytes<NB>() + 1024;
-    cfg.stream = st;
     cudaLaunchAttribute at[1];
-    if (p.split > 1) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = p.split;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-    }
+    cluster_config(&cfg, at, grid, p.split, kThreads, ring_bytes<NB>() + 1024, st);
+    if (p.split == 1) cfg.numAttrs = 0;
     return cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, NB>, ma, mb, mb2, p);
 }
 
-// Blocks per cluster that share one tile's inputs: as many as fill the SMs
-// (at most 8, the portable cluster), each with two blocks of inputs or more.
-int split_of(int sms, int64_t tiles, int kb) {
-    int64_t s = sms / (tiles > 0 ? tiles : 1);
-    if (s > 8) s = 8;
-    if (s > kb / 2) s = kb / 2;
-    return s < 1 ? 1 : (int)s;
+// Blocks per cluster that share one tile's inputs: as many as still let all
+// tiles run at a time, each with two blocks of inputs or more.  The GPCs do
+// not divide evenly (46 clusters of 3 fit 152 SMs, 28 of 5, 23 of 6): the
+// counts are the driver's.
+int split_of(const Dev &d, int64_t tiles, int kb) {
+    int s = kMaxSplit < kb / 2 ? kMaxSplit : kb / 2;
+    while (s > 1 && d.clusters[s] < tiles) --s;
+    return s < 1 ? 1 : s;
 }
 
 }  // namespace
@@ -609,9 +686,9 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
     const bool wide = 11 * ((t1 + d->sms - 1) / d->sms) >= 20 * ((t2 + d->sms - 1) / d->sms);
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     const int64_t tiles = wide ? t2 : t1;
-    p.split = split_of(d->sms, tiles, p.kb);
+    p.split = split_of(*d, tiles, p.kb);
     TensorMap ma, mb;
-    if ((e = make_map(&ma, a, 128)) != cudaSuccess || (e = make_map(&mb, b, 128)) != cudaSuccess)
+    if ((e = make_map(&ma, a, kBoxRows)) != cudaSuccess || (e = make_map(&mb, b, 128)) != cudaSuccess)
         return e;
     const int grid = p.split > 1 ? (int)tiles * p.split : (int)(tiles < d->sms ? tiles : d->sms);
     return wide ? launch<kDense, 2>(ma, mb, mb, p, grid, st)
@@ -637,7 +714,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     if ((e = make_map(&mq, {a.q, a.rows, H, H}, 1)) != cudaSuccess ||
         (e = make_map(&mg, {a.w.gate, (int64_t)E * I, H, H}, 128)) != cudaSuccess ||
         (e = make_map(&mu, {a.w.up, (int64_t)E * I, H, H}, 128)) != cudaSuccess ||
-        (e = make_map(&mh, {h, P, I, I}, 1)) != cudaSuccess ||
+        (e = make_map(&mh, {h, P, I, I}, kBoxRows)) != cudaSuccess ||
         (e = make_map(&md, {a.w.down, (int64_t)E * H, I, I}, 128)) != cudaSuccess)
         return e;
 
@@ -646,14 +723,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
     const int ranks = P <= 4096 ? 1 : 8;
-    cfg.gridDim = dim3(ranks);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = st;
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ranks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cluster_config(&cfg, at, ranks, ranks, 1024, 0, st);
     if ((e = cudaLaunchKernelEx(&cfg, index_kernel, ip)) != cudaSuccess) return e;
 
     Params p{};
@@ -671,7 +741,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     p.nblocks = p.tiles_n = I / 128;
     // the number of tiles is known on the device only: its upper bound
     int64_t most = (int64_t)w.max_tiles * p.tiles_n;
-    p.split = split_of(d->sms, most, p.kb);
+    p.split = split_of(*d, most, p.kb);
     int grid = p.split > 1 ? (int)most * p.split : (int)(most < d->sms ? most : d->sms);
     if ((e = launch<kGateUp, 2>(mq, mg, mu, p, grid, st)) != cudaSuccess) return e;
 
@@ -685,7 +755,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     const bool wide = (int64_t)w.max_tiles * ((p.nblocks + 1) / 2) >= d->sms;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     most = (int64_t)w.max_tiles * p.tiles_n;
-    p.split = split_of(d->sms, most, p.kb);
+    p.split = split_of(*d, most, p.kb);
     grid = p.split > 1 ? (int)most * p.split : (int)(most < d->sms ? most : d->sms);
     e = wide ? launch<kDown, 2>(mh, md, md, p, grid, st) : launch<kDown, 1>(mh, md, md, p, grid, st);
     if (e != cudaSuccess) return e;

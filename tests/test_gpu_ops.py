@@ -300,6 +300,20 @@ def test_experts_sizes(t, e, k, h, i):
     check_experts(randn(t, h, seed=9), ids, wts, layer(e, h, i))
 
 
+@pytest.mark.parametrize("t", [1, 2, 7, 40])
+def test_experts_few_rows_each_over_and_over(t):
+    """Tiles of one to a few rows with long inputs: the loading warps have
+    unequal shares and must not lose each other."""
+    lay = layer(64, 2048, 128)
+    ids, wts = choice(t, 8, 64, std=0.1)
+    x = randn(t, 2048, seed=9)
+    first = check_experts(x, ids, wts, lay)
+    q, s = R.rows_fp8(x)
+    for _ in range(200):
+        again = ops.experts_fp8(q, s, ids, wts, *lay)
+    assert torch.equal(first, again) and ops.device_status() == 0
+
+
 def test_experts_index_in_a_cluster():
     """More pairs than one block sorts, one expert with most of them."""
     ids, wts = choice(1500, 4, 8, std=3.0)
