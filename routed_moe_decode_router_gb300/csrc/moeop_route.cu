@@ -118,74 +118,74 @@ __device__ __forceinline__ uint32_t take_groups(F score, int groups, int limit, 
 
 __device__ __forceinline__ bool is_dead(float l) { return !(l > -INFINITY); }
 
-// The row again in 64 bits.  sm: E doubles of this warp.
-template <int VPT>
-__device__ __noinline__ void route_row_wide(const RouteParams &p, int row, int lane, double *sm) {
+__device__ __forceinline__ double prob_wide(float l, bool soft, double mx, double sum) {
+    if (is_dead(l)) return 0.0;
+    return soft ? exp((double)l - mx) / sum : 1.0 / (1.0 + exp(-(double)l));
+}
+
+// The row again in 64 bits, its keys in `key` (E doubles of this warp): few
+// rows come here, and registers for them would cost all rows occupancy.
+__device__ __noinline__ void route_row_wide(const RouteParams &p, int row, int lane, double *key) {
     const moeop_route_config &c = p.c;
     const int E = c.num_experts, k = c.top_k;
     const int64_t base = (int64_t)row * p.stride;
-    double prob[VPT], key[VPT];
-    double mx = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int e = j * 32 + lane;
-        const float l = e < E ? load_logit(p.logits, c.dtype, base + e) : -INFINITY;
-        key[j] = is_dead(l) ? -INFINITY : (double)l;
-        mx = fmax(mx, key[j]);
-    }
     const bool soft = c.scoring == MOE_SCORING_SOFTMAX;
-    double sum = 0.0;
+    double mx = -INFINITY, sum = 0.0;
     if (soft) {
+        for (int e = lane; e < E; e += 32) {
+            const float l = load_logit(p.logits, c.dtype, base + e);
+            if (!is_dead(l)) mx = fmax(mx, (double)l);
+        }
         mx = warp_max(mx);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            prob[j] = key[j] > -INFINITY ? exp(key[j] - mx) : 0.0;
-            sum += prob[j];
+        for (int e = lane; e < E; e += 32) {
+            const float l = load_logit(p.logits, c.dtype, base + e);
+            if (!is_dead(l)) sum += exp((double)l - mx);
         }
         sum = warp_sum(sum);
     }
     __syncwarp();
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int e = j * 32 + lane;
-        const bool dead = !(key[j] > -INFINITY);
-        prob[j] = dead ? 0.0 : soft ? prob[j] / sum : 1.0 / (1.0 + exp(-key[j]));
-        const double biased = prob[j] + (p.bias && e < E ? (double)__ldg(p.bias + e) : 0.0);
-        if (p.bias && !dead) key[j] = biased;
-        if (c.groups > 1 && e < E) sm[e] = dead ? -INFINITY : biased;
+    for (int e = lane; e < E; e += 32) {
+        const float l = load_logit(p.logits, c.dtype, base + e);
+        const double biased =
+            prob_wide(l, soft, mx, sum) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+        key[e] = is_dead(l) ? -INFINITY : biased;
     }
     __syncwarp();
+    uint32_t in = ~0u;
+    const int size = E / c.groups;
     if (c.groups > 1) {
         double gap;
         const double s =
-            group_scores<double>(sm, E, c.groups, c.group_score == MOEOP_GROUP_TOP2, lane);
-        const uint32_t in = take_groups<double>(s, c.groups, c.group_limit, lane, &gap);
-        const int size = E / c.groups;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int e = j * 32 + lane;
-            if (e < E && !(in >> (e / size) & 1)) key[j] = -INFINITY;
-        }
+            group_scores<double>(key, E, c.groups, c.group_score == MOEOP_GROUP_TOP2, lane);
+        in = take_groups<double>(s, c.groups, c.group_limit, lane, &gap);
+        __syncwarp();
+    }
+    for (int e = lane; e < E; e += 32) {
+        const float l = load_logit(p.logits, c.dtype, base + e);
+        if (!(in >> (e / size) & 1)) key[e] = -INFINITY;
+        else if (!p.bias) key[e] = is_dead(l) ? -INFINITY : (double)l;
     }
     int my_id[2] = {-1, -1};
     double my_p[2] = {0.0, 0.0};
     for (int s = 0; s < k; ++s) {
-        double best = -INFINITY, bp = 0.0;
+        double best = -INFINITY;
         int be = 1 << 30;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (key[j] > best) { best = key[j]; be = j * 32 + lane; bp = prob[j]; }
+        for (int e = lane; e < E; e += 32)
+            if (key[e] > best) { best = key[e]; be = e; }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            const double ob = __shfl_xor_sync(~0u, best, o), op = __shfl_xor_sync(~0u, bp, o);
+            const double ob = __shfl_xor_sync(~0u, best, o);
             const int oe = __shfl_xor_sync(~0u, be, o);
-            if (ob > best || (ob == best && oe < be)) { best = ob; be = oe; bp = op; }
+            if (ob > best || (ob == best && oe < be)) { best = ob; be = oe; }
         }
         if (!(best > -INFINITY)) break;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (be == j * 32 + lane) key[j] = -INFINITY;
-        if (lane == s % 32) { my_id[s / 32] = be; my_p[s / 32] = bp; }
+        if (lane == be % 32) key[be] = -INFINITY;   // the lane that reads it
+        if (lane == s % 32) {
+            const double bp =
+                prob_wide(load_logit(p.logits, c.dtype, base + be), soft, mx, sum);
+            if (s < 32) { my_id[0] = be; my_p[0] = bp; }
+            else { my_id[1] = be; my_p[1] = bp; }
+        }
     }
     double f = c.routed_scaling_factor;
     if (c.norm_topk_prob) {
@@ -200,6 +200,20 @@ __device__ __noinline__ void route_row_wide(const RouteParams &p, int row, int l
         }
 }
 
+// The largest of this lane's keys, and which: the first among equals.
+template <int VPT>
+__device__ __forceinline__ uint32_t local_best(const uint32_t (&ord)[VPT], int *at) {
+    uint32_t best = ord[0];
+    int j = 0;
+#pragma unroll
+    for (int i = 1; i < VPT; ++i)
+        if (ord[i] > best) { best = ord[i]; j = i; }
+    *at = j;
+    return best;
+}
+
+// VPT: experts per lane.  A round of the selection is one maximum over the
+// lanes' best keys; only the lane that held it looks through its keys again.
 template <int VPT>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) {
     __shared__ double sm_all[kWarps][VPT * 32];
@@ -219,25 +233,29 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
         key[j] = is_dead(l) ? -INFINITY : l;
         mx = fmaxf(mx, key[j]);
     }
-    float sum = 0.f, inv = 1.f;
+    float perr = 8 * kUlp;
     if (soft) {
         mx = warp_max(mx);
+        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             prob[j] = key[j] > -INFINITY ? expf(key[j] - mx) : 0.f;
             sum += prob[j];
         }
         sum = warp_sum(sum);
-        inv = 1.f / sum;  // the largest p of the row
-    }
-    const float perr = soft ? (VPT + 16) * kUlp * inv : 8 * kUlp;
-    bool wide = false;
+        const float inv = 1.f / sum;  // the largest p of the row
+        perr = (VPT + 16) * kUlp * inv;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const bool dead = !(key[j] > -INFINITY);
-        prob[j] = dead ? 0.f : soft ? prob[j] * inv : 1.f / (1.f + expf(-key[j]));
+        for (int j = 0; j < VPT; ++j) prob[j] = key[j] > -INFINITY ? prob[j] * inv : 0.f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            prob[j] = key[j] > -INFINITY ? __fdividef(1.f, 1.f + expf(-key[j])) : 0.f;
     }
+    bool wide = false;
     uint32_t ord[VPT];
+    uint32_t in = ~0u;
+    int size = E;
     if (c.groups > 1) {
         float *sm = reinterpret_cast<float *>(sm_all[warp]);
 #pragma unroll
@@ -252,24 +270,22 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
         float gap;
         const float s =
             group_scores<float>(sm, E, c.groups, c.group_score == MOEOP_GROUP_TOP2, lane);
-        const uint32_t in = take_groups<float>(s, c.groups, c.group_limit, lane, &gap);
+        in = take_groups<float>(s, c.groups, c.group_limit, lane, &gap);
         const float mag = warp_max(lane < c.groups && s > -INFINITY ? fabsf(s) : 0.f);
         wide |= gap <= 4.f * perr + 6.f * kUlp * mag;
-        const int size = E / c.groups;
+        size = E / c.groups;
+    } else if (p.bias) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int e = j * 32 + lane;
-            const bool out = e >= E || !(in >> (e / size) & 1) || !(key[j] > -INFINITY);
-            ord[j] = out ? 0u : order_key(key[j]);
-        }
-    } else {
+        for (int j = 0; j < VPT; ++j)
+            if (key[j] > -INFINITY) key[j] = prob[j] + __ldg(p.bias + j * 32 + lane);
+    }
+    // e / size for e up to 1023, exact: e * (2^20 / size rounded up) >> 20
+    const uint32_t div = ((1u << 20) + size - 1) / size;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int e = j * 32 + lane;
-            const bool dead = !(key[j] > -INFINITY);
-            if (p.bias && !dead) key[j] = prob[j] + __ldg(p.bias + e);
-            ord[j] = dead ? 0u : order_key(key[j]);
-        }
+    for (int j = 0; j < VPT; ++j) {
+        const uint32_t e = j * 32 + lane;
+        const bool out = !(key[j] > -INFINITY) || !(in >> (e * div >> 20) & 1);
+        ord[j] = out ? 0u : order_key(key[j]);
     }
     int my_id[2] = {-1, -1};
     float my_p[2] = {0.f, 0.f};
@@ -277,11 +293,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
     // one round more than top_k with a bias: the last one taken against the
     // first left out.  Without a bias the keys are the logits and exact.
     const int rounds = p.bias ? k + 1 : k;
+    int mine_at;
+    uint32_t mine = local_best<VPT>(ord, &mine_at);
     for (int s = 0; s < rounds; ++s) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) best = max(best, ord[j]);
-        best = __reduce_max_sync(~0u, best);
+        const uint32_t best = __reduce_max_sync(~0u, mine);
         if (best == 0) break;
         if (p.bias) {
             const float v = order_value(best);
@@ -289,16 +304,19 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
             before = v;
             if (s == k) break;
         }
-        int be = 1 << 30;
-#pragma unroll
-        for (int j = VPT - 1; j >= 0; --j)
-            if (ord[j] == best) be = j * 32 + lane;
-        be = __reduce_min_sync(~0u, be);
+        uint32_t who = __ballot_sync(~0u, mine == best);
+        if (who & (who - 1))  // equal keys in several lanes: the lowest expert
+            who = 1u << (__reduce_min_sync(~0u, mine == best ? mine_at * 32 + lane : 1 << 30) & 31);
+        const int from = __ffs(who) - 1;
+        const int be = __shfl_sync(~0u, mine_at * 32 + lane, from);
         float bp = 0.f;
+        if (lane == from) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (be == j * 32 + lane) { ord[j] = 0u; bp = prob[j]; }
-        bp = __shfl_sync(~0u, bp, be % 32);
+            for (int j = 0; j < VPT; ++j)
+                if (j == mine_at) { ord[j] = 0u; bp = prob[j]; }
+            mine = local_best<VPT>(ord, &mine_at);
+        }
+        bp = __shfl_sync(~0u, bp, from);
         if (lane == s % 32) {
             if (s < 32) { my_id[0] = be; my_p[0] = bp; }
             else { my_id[1] = be; my_p[1] = bp; }
@@ -312,7 +330,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
         f = total > 0.f ? f / total : 0.f;
     }
     if (wide) {
-        route_row_wide<VPT>(p, row, lane, sm_all[warp]);
+        route_row_wide(p, row, lane, sm_all[warp]);
         return;
     }
 #pragma unroll
