@@ -16,8 +16,10 @@
 // with u = 2^-24, expf, the divisions and the sum of E terms (E/32 serial, 5
 // in the tree) leave p within (E/32 + 16) u of its value, relative to the
 // largest p of the row; a sigmoid within 8 u; adding the bias rounds by u
-// |key|.  About one row in a hundred takes the second way with N(0, 1.5)
-// logits, 256 experts and a bias.
+// |key|.  About one row in a thousand takes the second way with N(0, 1.5)
+// logits, 256 experts and a bias.  64-bit arithmetic is slow here (an SM does
+// two such operations a cycle): where only the order of the keys is in doubt,
+// as nearly always, just the candidates' keys are computed, one to a lane.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,21 +36,35 @@ namespace {
 constexpr int kWarps = 4;  // rows per block
 constexpr float kUlp = 5.9604645e-8f;
 
-__device__ __forceinline__ float load_logit(const void *p, int dtype, int64_t i) {
-    if (dtype == MOEOP_FP32) return __ldg(static_cast<const float *>(p) + i);
-    if (dtype == MOEOP_BF16)
+// What the kernel needs beside the caller's arguments, worked out once.
+struct Args {
+    RouteParams p;
+    int size;        // experts per group
+    int lane_shift;  // 2^lane_shift lanes score one group (2^lane_shift * groups <= 32)
+    uint32_t div;    // e / size == e * div >> 20 for e up to 1023
+};
+
+template <int DT>
+__device__ __forceinline__ float load_logit(const void *p, int64_t i) {
+    if (DT == MOEOP_FP32) return __ldg(static_cast<const float *>(p) + i);
+    if (DT == MOEOP_BF16)
         return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(p) + i) << 16);
     return __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t *>(p) + i)));
 }
+__device__ __forceinline__ bool is_dead(float l) { return !(l > -INFINITY); }
 
-// Order-preserving map of finite or infinite floats to unsigned; 0 is below
+// Order-preserving maps of finite or infinite floats to unsigned; 0 is below
 // all, and -0 equals 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
     const uint32_t b = __float_as_uint(f + 0.f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float order_value(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+    return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ uint64_t order_key(double f) {
+    const uint64_t b = (uint64_t)__double_as_longlong(f + 0.0);
+    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
 template <typename F>
@@ -56,6 +72,9 @@ __device__ __forceinline__ F warp_max(F v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v = fmax(v, __shfl_xor_sync(~0u, v, o));
     return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+    return order_value(__reduce_max_sync(~0u, order_key(v)));
 }
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -65,58 +84,47 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 
 // Scores of the groups from s[0..E) (dead experts -inf), in lane g for group
-// g; -inf beyond the groups and for groups with nothing left.  `lanes` lanes
-// (a power of two, lanes * groups <= 32) read one group together.
+// g; -inf beyond the groups and for groups with nothing left.
 template <typename F>
-__device__ __forceinline__ F group_scores(const F *s, int E, int groups, int top2, int lane) {
-    const int size = E / groups;
-    int lanes = 1;
-    while (lanes * 2 * groups <= 32) lanes *= 2;
-    const int g = lane / lanes, sub = lane % lanes;
+__device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane) {
+    const int sh = q.lane_shift, lanes = 1 << sh, g = lane >> sh, sub = lane & (lanes - 1);
     const F none = -INFINITY;
     F a = none, b = none;  // the two largest
-    if (g < groups) {
+    if (g < q.p.c.groups) {
         // every lane's list starts at another place, so that the lanes' reads
         // fall into different banks
-        const int n = size > sub ? (size - sub + lanes - 1) / lanes : 0;
-        int i = n ? g % n : 0;
+        const int n = (q.size - sub + lanes - 1) >> sh;
+        const F *from = s + g * q.size + sub;
+        int i = g;
+        while (i >= n && n) i -= n;
+#pragma unroll 4
         for (int t = 0; t < n; ++t) {
-            const F v = s[g * size + sub + i * lanes];
-            if (v > a) { b = a; a = v; }
-            else if (v > b) b = v;
+            const F v = from[i << sh];
+            b = fmax(b, fmin(a, v));
+            a = fmax(a, v);
             if (++i == n) i = 0;
         }
     }
     for (int o = 1; o < lanes; o *= 2) {
         const F oa = __shfl_xor_sync(~0u, a, o), ob = __shfl_xor_sync(~0u, b, o);
-        const F lo = fmin(a, oa);
+        b = fmax(fmin(a, oa), fmax(b, ob));
         a = fmax(a, oa);
-        b = fmax(lo, fmax(b, ob));
     }
-    F score = a;
-    if (top2 && b > none) score += b;
-    const F mine = __shfl_sync(~0u, score, (lane * lanes) & 31);
-    return lane < groups ? mine : none;
+    if (q.p.c.group_score == MOEOP_GROUP_TOP2 && b > none) a += b;
+    const F mine = __shfl_sync(~0u, a, (lane << sh) & 31);
+    return lane < q.p.c.groups ? mine : none;
 }
 
 // Bit g: group g is among the `limit` best (ties: lower index first).
-// *gap: the smallest taken score minus the largest left out.
 template <typename F>
-__device__ __forceinline__ uint32_t take_groups(F score, int groups, int limit, int lane, F *gap) {
+__device__ __forceinline__ uint32_t take_groups(F score, const Args &q, int lane) {
     int rank = 0;
-    for (int g = 0; g < groups; ++g) {
+    for (int g = 0; g < q.p.c.groups; ++g) {
         const F o = __shfl_sync(~0u, score, g);
         rank += o > score || (o == score && g < lane);
     }
-    const bool in = lane < groups && rank < limit;
-    const F none = -INFINITY;
-    const F worst = -warp_max(in ? -score : none);
-    const F best = warp_max(lane < groups && !in ? score : none);
-    *gap = worst - best;  // NaN where both are -inf: then nothing is left in either
-    return __ballot_sync(~0u, in);
+    return __ballot_sync(~0u, lane < q.p.c.groups && rank < q.p.c.group_limit);
 }
-
-__device__ __forceinline__ bool is_dead(float l) { return !(l > -INFINITY); }
 
 __device__ __forceinline__ double prob_wide(float l, bool soft, double mx, double sum) {
     if (is_dead(l)) return 0.0;
@@ -124,69 +132,78 @@ __device__ __forceinline__ double prob_wide(float l, bool soft, double mx, doubl
 }
 
 // The row again in 64 bits, its keys in `key` (E doubles of this warp): few
-// rows come here, and registers for them would cost all rows occupancy.
-__device__ __noinline__ void route_row_wide(const RouteParams &p, int row, int lane, double *key) {
+// rows come here, and registers for them would cost all rows occupancy.  An
+// SM does two 64-bit operations a cycle, so the keys are compared as integers.
+template <int DT>
+__device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, double *key) {
+    const RouteParams &p = q.p;
     const moeop_route_config &c = p.c;
     const int E = c.num_experts, k = c.top_k;
     const int64_t base = (int64_t)row * p.stride;
     const bool soft = c.scoring == MOE_SCORING_SOFTMAX;
     double mx = -INFINITY, sum = 0.0;
     if (soft) {
+        float m = -INFINITY;
         for (int e = lane; e < E; e += 32) {
-            const float l = load_logit(p.logits, c.dtype, base + e);
-            if (!is_dead(l)) mx = fmax(mx, (double)l);
+            const float l = load_logit<DT>(p.logits, base + e);
+            if (!is_dead(l)) m = fmaxf(m, l);
         }
-        mx = warp_max(mx);
+        mx = warp_max(m);
+#pragma unroll 4
         for (int e = lane; e < E; e += 32) {
-            const float l = load_logit(p.logits, c.dtype, base + e);
-            if (!is_dead(l)) sum += exp((double)l - mx);
+            const float l = load_logit<DT>(p.logits, base + e);
+            sum += is_dead(l) ? 0.0 : exp((double)l - mx);
         }
         sum = warp_sum(sum);
     }
     __syncwarp();
-    for (int e = lane; e < E; e += 32) {
-        const float l = load_logit(p.logits, c.dtype, base + e);
-        const double biased =
-            prob_wide(l, soft, mx, sum) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
-        key[e] = is_dead(l) ? -INFINITY : biased;
-    }
-    __syncwarp();
     uint32_t in = ~0u;
-    const int size = E / c.groups;
-    if (c.groups > 1) {
-        double gap;
-        const double s =
-            group_scores<double>(key, E, c.groups, c.group_score == MOEOP_GROUP_TOP2, lane);
-        in = take_groups<double>(s, c.groups, c.group_limit, lane, &gap);
+    if (p.bias || c.groups > 1) {
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) {
+            const float l = load_logit<DT>(p.logits, base + e);
+            const double biased =
+                prob_wide(l, soft, mx, sum) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+            key[e] = is_dead(l) ? -INFINITY : biased;
+        }
+        __syncwarp();
+        if (c.groups > 1) in = take_groups<double>(group_scores<double>(key, q, lane), q, lane);
         __syncwarp();
     }
+    uint64_t *ord = reinterpret_cast<uint64_t *>(key);
+    uint64_t mine = 0;
+    int mine_at = lane;
     for (int e = lane; e < E; e += 32) {
-        const float l = load_logit(p.logits, c.dtype, base + e);
-        if (!(in >> (e / size) & 1)) key[e] = -INFINITY;
-        else if (!p.bias) key[e] = is_dead(l) ? -INFINITY : (double)l;
+        const float l = load_logit<DT>(p.logits, base + e);
+        const bool out = is_dead(l) || !(in >> ((uint32_t)e * q.div >> 20) & 1);
+        const uint64_t o = out ? 0 : order_key(p.bias ? key[e] : (double)l);
+        ord[e] = o;
+        if (o > mine) { mine = o; mine_at = e; }
     }
     int my_id[2] = {-1, -1};
-    double my_p[2] = {0.0, 0.0};
     for (int s = 0; s < k; ++s) {
-        double best = -INFINITY;
-        int be = 1 << 30;
-        for (int e = lane; e < E; e += 32)
-            if (key[e] > best) { best = key[e]; be = e; }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const double ob = __shfl_xor_sync(~0u, best, o);
-            const int oe = __shfl_xor_sync(~0u, be, o);
-            if (ob > best || (ob == best && oe < be)) { best = ob; be = oe; }
+        const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(mine >> 32));
+        if (hi == 0) break;
+        const bool top = (uint32_t)(mine >> 32) == hi;
+        const uint32_t lo = __reduce_max_sync(~0u, top ? (uint32_t)mine : 0u);
+        const int be = __reduce_min_sync(~0u, top && (uint32_t)mine == lo ? mine_at : 1 << 30);
+        if (be == mine_at) {
+            ord[be] = 0;
+            mine = 0;
+            for (int e = lane; e < E; e += 32)
+                if (ord[e] > mine) { mine = ord[e]; mine_at = e; }
         }
-        if (!(best > -INFINITY)) break;
-        if (lane == be % 32) key[be] = -INFINITY;   // the lane that reads it
+        __syncwarp();
         if (lane == s % 32) {
-            const double bp =
-                prob_wide(load_logit(p.logits, c.dtype, base + be), soft, mx, sum);
-            if (s < 32) { my_id[0] = be; my_p[0] = bp; }
-            else { my_id[1] = be; my_p[1] = bp; }
+            if (s < 32) my_id[0] = be;
+            else my_id[1] = be;
         }
     }
+    double my_p[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        my_p[h] = my_id[h] < 0 ? 0.0
+                               : prob_wide(load_logit<DT>(p.logits, base + my_id[h]), soft, mx, sum);
     double f = c.routed_scaling_factor;
     if (c.norm_topk_prob) {
         const double total = warp_sum(my_p[0] + my_p[1]);
@@ -198,6 +215,65 @@ __device__ __noinline__ void route_row_wide(const RouteParams &p, int row, int l
             p.ids[(size_t)row * k + lane + 32 * h] = my_id[h];
             p.wts[(size_t)row * k + lane + 32 * h] = (float)(my_p[h] * f);
         }
+}
+
+// Lane i holds the i-th of n candidates for the top k (-1: none): their
+// order and weights in 64 bits.  The sum of a softmax takes the whole row.
+template <int DT>
+__device__ __noinline__ void route_row_close(const Args &q, int row, int lane, int id, int n) {
+    const RouteParams &p = q.p;
+    const moeop_route_config &c = p.c;
+    const int E = c.num_experts, k = c.top_k;
+    const int64_t base = (int64_t)row * p.stride;
+    const bool soft = c.scoring == MOE_SCORING_SOFTMAX;
+    double mx = 0.0, sum = 0.0;
+    if (soft) {
+        float m = -INFINITY;
+        for (int e = lane; e < E; e += 32) {
+            const float l = load_logit<DT>(p.logits, base + e);
+            if (!is_dead(l)) m = fmaxf(m, l);
+        }
+        mx = warp_max(m);
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) {
+            const float l = load_logit<DT>(p.logits, base + e);
+            sum += is_dead(l) ? 0.0 : exp((double)l - mx);
+        }
+        sum = warp_sum(sum);
+    }
+    double prob = 0.0;
+    uint64_t ord = 0;
+    if (id >= 0) {
+        prob = prob_wide(load_logit<DT>(p.logits, base + id), soft, mx, sum);
+        ord = order_key(prob + (double)__ldg(p.bias + id));
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const uint64_t o = __shfl_sync(~0u, ord, i);
+        const int oid = __shfl_sync(~0u, id, i);
+        rank += o > ord || (o == ord && oid < id);
+    }
+    const bool in = id >= 0 && rank < k;
+    double f = c.routed_scaling_factor;
+    if (c.norm_topk_prob) {
+        const double total = warp_sum(in ? prob : 0.0);
+        f = total > 0.0 ? f / total : 0.0;
+    }
+    if (in) {
+        p.ids[(size_t)row * k + rank] = id;
+        p.wts[(size_t)row * k + rank] = (float)(prob * f);
+    }
+    // slots that no expert is left for
+    const int have = __popc(__ballot_sync(~0u, in));
+    if (lane >= have && lane < k) {
+        p.ids[(size_t)row * k + lane] = -1;
+        p.wts[(size_t)row * k + lane] = 0.f;
+    }
+}
+
+__device__ __forceinline__ float prob_of(float l, bool soft, float mx, float inv) {
+    if (is_dead(l)) return 0.f;
+    return soft ? expf(l - mx) * inv : __fdividef(1.f, 1.f + expf(-l));
 }
 
 // The largest of this lane's keys, and which: the first among equals.
@@ -214,82 +290,73 @@ __device__ __forceinline__ uint32_t local_best(const uint32_t (&ord)[VPT], int *
 
 // VPT: experts per lane.  A round of the selection is one maximum over the
 // lanes' best keys; only the lane that held it looks through its keys again.
-template <int VPT>
-__global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) {
+template <int VPT, int DT>
+__global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
     __shared__ double sm_all[kWarps][VPT * 32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int row = blockIdx.x * kWarps + warp;
+    const RouteParams &p = q.p;
     if (row >= p.rows) return;
     const moeop_route_config &c = p.c;
     const int E = c.num_experts, k = c.top_k;
     const int64_t base = (int64_t)row * p.stride;
     const bool soft = c.scoring == MOE_SCORING_SOFTMAX;
-    float prob[VPT], key[VPT];
-    float mx = -INFINITY;
+    float key[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int e = j * 32 + lane;
-        const float l = e < E ? load_logit(p.logits, c.dtype, base + e) : -INFINITY;
+        const float l = e < E ? load_logit<DT>(p.logits, base + e) : -INFINITY;
         key[j] = is_dead(l) ? -INFINITY : l;
-        mx = fmaxf(mx, key[j]);
     }
-    float perr = 8 * kUlp;
+    float perr = 8 * kUlp, mx = 0.f, inv = 1.f;
     if (soft) {
+        mx = key[0];
+#pragma unroll
+        for (int j = 1; j < VPT; ++j) mx = fmaxf(mx, key[j]);
         mx = warp_max(mx);
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            prob[j] = key[j] > -INFINITY ? expf(key[j] - mx) : 0.f;
-            sum += prob[j];
-        }
+        for (int j = 0; j < VPT; ++j) sum += key[j] > -INFINITY ? expf(key[j] - mx) : 0.f;
         sum = warp_sum(sum);
-        const float inv = 1.f / sum;  // the largest p of the row
+        inv = 1.f / sum;  // the largest p of the row
         perr = (VPT + 16) * kUlp * inv;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) prob[j] = key[j] > -INFINITY ? prob[j] * inv : 0.f;
-    } else {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            prob[j] = key[j] > -INFINITY ? __fdividef(1.f, 1.f + expf(-key[j])) : 0.f;
     }
     bool wide = false;
-    uint32_t ord[VPT];
     uint32_t in = ~0u;
-    int size = E;
-    if (c.groups > 1) {
+    if (p.bias || c.groups > 1) {
         float *sm = reinterpret_cast<float *>(sm_all[warp]);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int e = j * 32 + lane;
             const bool dead = !(key[j] > -INFINITY);
-            const float biased = prob[j] + (p.bias && e < E ? __ldg(p.bias + e) : 0.f);
+            float biased = prob_of(key[j], soft, mx, inv);
+            if (p.bias && e < E) biased += __ldg(p.bias + e);
             if (p.bias && !dead) key[j] = biased;
-            if (e < E) sm[e] = dead ? -INFINITY : biased;
+            if (c.groups > 1 && e < E) sm[e] = dead ? -INFINITY : biased;
         }
-        __syncwarp();
-        float gap;
-        const float s =
-            group_scores<float>(sm, E, c.groups, c.group_score == MOEOP_GROUP_TOP2, lane);
-        in = take_groups<float>(s, c.groups, c.group_limit, lane, &gap);
-        const float mag = warp_max(lane < c.groups && s > -INFINITY ? fabsf(s) : 0.f);
-        wide |= gap <= 4.f * perr + 6.f * kUlp * mag;
-        size = E / c.groups;
-    } else if (p.bias) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (key[j] > -INFINITY) key[j] = prob[j] + __ldg(p.bias + j * 32 + lane);
+        if (c.groups > 1) {
+            __syncwarp();
+            const float s = group_scores<float>(sm, q, lane);
+            in = take_groups<float>(s, q, lane);
+            // the last group taken against the first left out; where nothing
+            // is left in either there is nothing to decide
+            const bool taken = in >> lane & 1, some = lane < c.groups && s > -INFINITY;
+            const float worst = -warp_max(taken ? -s : -INFINITY);
+            const float best = warp_max(!taken && some ? s : -INFINITY);
+            const float mag = warp_max(some ? fabsf(s) : 0.f);
+            wide |= worst - best <= 4.f * perr + 6.f * kUlp * mag;
+        }
     }
-    // e / size for e up to 1023, exact: e * (2^20 / size rounded up) >> 20
-    const uint32_t div = ((1u << 20) + size - 1) / size;
+    uint32_t ord[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const uint32_t e = j * 32 + lane;
-        const bool out = !(key[j] > -INFINITY) || !(in >> (e * div >> 20) & 1);
+        const bool out = !(key[j] > -INFINITY) || !(in >> (e * q.div >> 20) & 1);
         ord[j] = out ? 0u : order_key(key[j]);
     }
     int my_id[2] = {-1, -1};
-    float my_p[2] = {0.f, 0.f};
-    float before = 0.f;
+    float before = 0.f, last = 0.f;
+    bool close = false;
     // one round more than top_k with a bias: the last one taken against the
     // first left out.  Without a bias the keys are the logits and exact.
     const int rounds = p.bias ? k + 1 : k;
@@ -300,37 +367,59 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
         if (best == 0) break;
         if (p.bias) {
             const float v = order_value(best);
-            if (s) wide |= before - v <= 2.f * perr + 4.f * kUlp * fabsf(before);
+            if (s) close |= before - v <= 2.f * perr + 4.f * kUlp * fabsf(before);
             before = v;
             if (s == k) break;
+            last = v;
         }
         uint32_t who = __ballot_sync(~0u, mine == best);
         if (who & (who - 1))  // equal keys in several lanes: the lowest expert
             who = 1u << (__reduce_min_sync(~0u, mine == best ? mine_at * 32 + lane : 1 << 30) & 31);
         const int from = __ffs(who) - 1;
         const int be = __shfl_sync(~0u, mine_at * 32 + lane, from);
-        float bp = 0.f;
         if (lane == from) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
-                if (j == mine_at) { ord[j] = 0u; bp = prob[j]; }
+                if (j == mine_at) ord[j] = 0u;
             mine = local_best<VPT>(ord, &mine_at);
         }
-        bp = __shfl_sync(~0u, bp, from);
         if (lane == s % 32) {
-            if (s < 32) { my_id[0] = be; my_p[0] = bp; }
-            else { my_id[1] = be; my_p[1] = bp; }
+            if (s < 32) my_id[0] = be;
+            else my_id[1] = be;
         }
     }
+    float my_p[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        my_p[h] = my_id[h] < 0 ? 0.f
+                               : prob_of(load_logit<DT>(p.logits, base + my_id[h]), soft, mx, inv);
     float f = c.routed_scaling_factor;
     if (c.norm_topk_prob) {
         const float total = warp_sum(my_p[0] + my_p[1]);
         // under 2^-60 of the row's unit the p that fp32 holds are too small
         wide |= __any_sync(~0u, my_id[0] >= 0) && !(total > 8.7e-19f);
-        f = total > 0.f ? f / total : 0.f;
+        f = total > 0.f ? __fdividef(f, total) : 0.f;
+    }
+    if (close && !wide) {
+        // every expert that may belong to the top k: those taken, and those
+        // left whose keys are as near to the last taken
+        const float from = last - 2.f * perr - 4.f * kUlp * fabsf(last);
+        int id = my_id[0], n = min(k, 32);
+        wide = k > 31;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const uint32_t more = __ballot_sync(~0u, ord[j] && order_value(ord[j]) >= from);
+            for (uint32_t m = more; m; m &= m - 1, ++n)
+                if (lane == n) id = j * 32 + __ffs(m) - 1;
+        }
+        wide |= n > 32;
+        if (!wide) {
+            route_row_close<DT>(q, row, lane, id, n);
+            return;
+        }
     }
     if (wide) {
-        route_row_wide(p, row, lane, sm_all[warp]);
+        route_row_wide<DT>(q, row, lane, sm_all[warp]);
         return;
     }
 #pragma unroll
@@ -341,15 +430,27 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouteParams p) 
         }
 }
 
+template <int DT>
+cudaError_t launch_typed(const Args &q, cudaStream_t st) {
+    const int grid = (q.p.rows + kWarps - 1) / kWarps, E = q.p.c.num_experts;
+    if (E <= 128) route_topk_kernel<4, DT><<<grid, kWarps * 32, 0, st>>>(q);
+    else if (E <= 256) route_topk_kernel<8, DT><<<grid, kWarps * 32, 0, st>>>(q);
+    else if (E <= 512) route_topk_kernel<16, DT><<<grid, kWarps * 32, 0, st>>>(q);
+    else route_topk_kernel<32, DT><<<grid, kWarps * 32, 0, st>>>(q);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_route_topk(const RouteParams &p, cudaStream_t st) {
-    const int grid = (p.rows + kWarps - 1) / kWarps, E = p.c.num_experts;
-    if (E <= 128) route_topk_kernel<4><<<grid, kWarps * 32, 0, st>>>(p);
-    else if (E <= 256) route_topk_kernel<8><<<grid, kWarps * 32, 0, st>>>(p);
-    else if (E <= 512) route_topk_kernel<16><<<grid, kWarps * 32, 0, st>>>(p);
-    else route_topk_kernel<32><<<grid, kWarps * 32, 0, st>>>(p);
-    return cudaGetLastError();
+    Args q{p, p.c.num_experts / p.c.groups, 0, 0};
+    while ((2 << q.lane_shift) * p.c.groups <= 32) ++q.lane_shift;
+    q.div = ((1u << 20) + q.size - 1) / q.size;
+    switch (p.c.dtype) {
+        case MOEOP_BF16: return launch_typed<MOEOP_BF16>(q, st);
+        case MOEOP_FP16: return launch_typed<MOEOP_FP16>(q, st);
+        default: return launch_typed<MOEOP_FP32>(q, st);
+    }
 }
 
 }  // namespace op

@@ -154,6 +154,21 @@ def test_route_decides_close_keys_as_in_64_bits():
     check_route(logits, 8, scoring="softmax", bias=b)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top_k", [1, 8, 31, 32, 40])
+def test_route_pairs_of_keys_a_step_apart(scoring, top_k):
+    """Pairs of experts whose keys differ by about an fp32 step, in and at the
+    end of the selection, more of them than lanes among them."""
+    base = randn(30, 48, std=1.0).repeat_interleave(2, 1)
+    logits = base + randn(30, 96, seed=1) * 1e-7
+    logits[0] = logits[0, 0] + randn(96, seed=2) * 1e-7
+    b = (randn(48, seed=3, std=0.1)).repeat_interleave(2)
+    check_route(logits, top_k, scoring=scoring, bias=b, routed_scaling_factor=2.0)
+    logits[1, 9:] = -math.inf
+    logits[2, 3:] = -math.inf
+    check_route(logits, top_k, scoring=scoring, bias=b, norm_topk_prob=False)
+
+
 @pytest.mark.parametrize("scoring,bias", [("softmax", False), ("softmax", True),
                                           ("sigmoid", False), ("sigmoid", True)])
 @pytest.mark.parametrize("groups,limit", [(1, 1), (8, 2)])
