@@ -48,10 +48,10 @@ constexpr int kBoxRows = 32;      // rows of A in one copy
 constexpr int kMaxSplit = 7;      // six other ranks' sums of 32 rows fill the ring
 constexpr int kTile = 128 * 128;  // bytes of one operand tile
 
+// The ring: 192 KB.
 template <int NB>
 constexpr int stages() { return NB == 2 ? 4 : 6; }
-template <int NB>
-constexpr size_t ring_bytes() { return (size_t)stages<NB>() * (1 + NB) * kTile; }
+constexpr size_t kRing = 12 * kTile;
 
 struct Params {
     int rows, n, kb;          // dense: rows of A; outputs; blocks of 128 inputs
@@ -59,8 +59,10 @@ struct Params {
     int nblocks;              // 128-output blocks of B (per expert)
     int split;                // blocks per cluster
     const float *sa, *sb, *sb2;
+    bool even;                // pairs of scales start on 8-byte boundaries
     void *out;
     int out_dtype;
+    bool vec_out;             // rows of out start on 16-byte boundaries
     // experts
     const int *num_tiles;
     const int4 *tiles;        // expert, first position, rows
@@ -85,46 +87,54 @@ __device__ __forceinline__ Tile tile_at(const Params &p, int t) {
     return {d.x, d.y, d.z, nt};
 }
 
-// A scale of the A rows; h's were written by the kernel before.
-template <int MODE>
-__device__ __forceinline__ float ld_scale(const float *p) {
+// Scales of the A rows; h's were written by the kernel before.
+template <int MODE, typename F>
+__device__ __forceinline__ F ld_scales(const F *p) {
     return MODE == kDown ? __ldcg(p) : __ldg(p);
 }
 
-// 16 consecutive outputs of one row.
-__device__ __forceinline__ void store16(void *out, int dtype, size_t at, const float *v, int left) {
-    if (dtype == MOEOP_FP32) {
-        float *o = static_cast<float *>(out) + at;
-        if (left >= 16 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+__device__ __forceinline__ void store1(void *out, int dtype, size_t at, float v) {
+    if (dtype == MOEOP_FP32) static_cast<float *>(out)[at] = v;
+    else if (dtype == MOEOP_BF16) static_cast<uint16_t *>(out)[at] = f2bf16_rn(v);
+    else static_cast<__half *>(out)[at] = __float2half_rn(v);
+}
+// Two fp32 sums -> two 16-bit outputs.
+__device__ __forceinline__ uint32_t pack16(uint64_t v, int dtype) {
+    const float2 f = unpack2(v);
+    if (dtype != MOEOP_BF16) return pack_f16x2(f.x, f.y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ uint4 shfl_xor4(uint4 v, int m) {
+    return make_uint4(__shfl_xor_sync(~0u, v.x, m), __shfl_xor_sync(~0u, v.y, m),
+                      __shfl_xor_sync(~0u, v.z, m), __shfl_xor_sync(~0u, v.w, m));
+}
+// Among lanes 4q .. 4q + 3: u[j] of lane 4q + i becomes u[i] of lane 4q + j.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
+    const bool hi = lane & 2, odd = lane & 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<float4 *>(o)[i] =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i < left) o[i] = v[i];
-        }
-        return;
+    for (int i = 0; i < 2; ++i) {
+        const uint4 r = shfl_xor4(hi ? u[i] : u[i + 2], 2);
+        if (hi) u[i] = r;
+        else u[i + 2] = r;
     }
-    uint16_t *o = static_cast<uint16_t *>(out) + at;
-    uint32_t u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (dtype == MOEOP_BF16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&b);
-        } else {
-            u[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
-        }
+    for (int i = 0; i < 4; i += 2) {
+        const uint4 r = shfl_xor4(odd ? u[i] : u[i + 1], 1);
+        if (odd) u[i] = r;
+        else u[i + 1] = r;
     }
-    if (left >= 16 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-        reinterpret_cast<uint4 *>(o)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        reinterpret_cast<uint4 *>(o)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-    } else {
+}
+// Transposed units to the outputs from `col` on of rows orow of the lanes;
+// `left`: valid rows from this warp's first on.
+__device__ __forceinline__ void store_rows(const uint4 (&u)[4], char *out, int orow, int n, int col,
+                                           int size, int lane, int left) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < left) o[i] = (uint16_t)(u[i / 2] >> (16 * (i % 2)));
+    for (int j = 0; j < 4; ++j) {
+        const int src = (lane & ~3) + j;
+        const size_t row = __shfl_sync(~0u, orow, src);
+        if (src < left)
+            *reinterpret_cast<uint4 *>(out + (row * n + col) * size + (lane & 3) * 16) = u[j];
     }
 }
 
@@ -136,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kStage = (1 + NB) * kTile;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[S], empty[S], tm_full[2], tm_empty[2];
-    __shared__ float amax_s[kColGroups][128], sa_s[2][8][128], sb_s[2][8][NB];
+    __shared__ float amax_s[kColGroups][128];
     __shared__ uint32_t tm_base;
     __shared__ int abort_s;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -187,8 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r[i] = __ldcg(p.token + pos + min(4 * lane + i, rows - 1));
             }
             const int b0 = e * p.n + T.nt * (MODE == kGateUp ? 128 : 128 * NB);
-            const uint32_t bytes = NB * kTile + (MODE == kGateUp ? quads * 512
-                                                                 : boxes * kBoxRows * 128);
+            const uint32_t bytes =
+                NB * kTile + (MODE == kGateUp ? quads * 512 : boxes * kBoxRows * 128);
             for (int b = kb0; b < kb1; ++b, ++it) {
                 const int s = it % S;
                 ok = __all_sync(~0u, wait_bar(&empty[s], (it / S & 1) ^ 1, &abort_s));
@@ -222,102 +232,134 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         // ---- MMAs
         constexpr uint32_t idesc = tc_idesc(128, 128 * NB);
-        int it = 0;
+        const uint64_t desc0 = tc_desc(ring);
+        int s = 0, buf = 0;
+        uint32_t phase = 0, ring_phase = 0;
         bool ok = true;
         for (int t = first; t < total && ok; t += step) {
-            for (int b = kb0; b < kb1; ++b, ++it) {
-                const int s = it % S, buf = it & 1;
-                ok = __all_sync(~0u, wait_bar(&tm_empty[buf], (it / 2 & 1) ^ 1, &abort_s) &&
-                                         wait_bar(&full[s], it / S & 1, &abort_s));
+            for (int b = kb0; b < kb1; ++b) {
+                const uint64_t da = desc0 + (uint64_t)(s * (kStage >> 4));
+                const uint64_t db = da + (kTile >> 4);
+                const uint32_t d = tm + buf * 128 * NB;
+                ok = __all_sync(~0u, spin_bar(&tm_empty[buf], phase ^ 1, &abort_s) &&
+                                         spin_bar(&full[s], ring_phase, &abort_s));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t da = tc_desc(ring + s * kStage);
-                const uint64_t db = tc_desc(ring + s * kStage + kTile);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tc_mma_e4m3(tm + buf * 128 * NB, da + 2 * k, db + 2 * k, idesc, k > 0);
+                        tc_mma_e4m3(d, da + 2 * k, db + 2 * k, idesc, k > 0);
                     tc_commit(&empty[s]);
                     tc_commit(&tm_full[buf]);
                 }
                 __syncwarp();
+                phase ^= buf;
+                buf ^= 1;
+                if (++s == S) s = 0, ring_phase ^= 1;
             }
         }
     } else {
         // ---- accumulation and stores
-        // The scales of 8 input blocks at a time go through shared memory: a
-        // row's are contiguous in memory, so a load by rows touches 32 lines.
         const int wg = warp / 4, r = (warp % 4) * 32 + lane;
         const uint32_t tm_lane = tm + ((uint32_t)(warp % 4) * 32 << 16) + wg * kCols;
-        int it = 0, half = 0;
+        constexpr int kAcc = kCols / 2 * NB;  // pairs of this thread's sums
+        int arow = 0, brow = 0;               // where its scales are
+        Tile T{};
+        auto take = [&](int t) {
+            T = tile_at<MODE>(p, t);
+            arow = r >= T.rows ? 0 : MODE == kGateUp ? __ldcg(p.token + T.pos + r) : T.pos + r;
+            brow = T.e * p.nblocks + T.nt * (MODE == kGateUp ? 1 : NB);
+        };
+        // The scales of input blocks b and b + 1: this row's, and those of the
+        // tile's output blocks.  They come straight from global memory, two
+        // blocks ahead: a read of shared memory, which is busy with the
+        // operands, takes some 400 cycles and holds up the tensor-memory
+        // loads behind it.
+        float a0 = 0.f, a1 = 0.f, b00 = 0.f, b01 = 0.f, b10 = 0.f, b11 = 0.f;
+        const bool even = p.even && kb0 % 2 == 0;
+        auto fetch = [&](int b) {
+            const float *sa = p.sa + (size_t)arow * p.kb + b;
+            const float *sb0 = p.sb + (size_t)brow * p.kb + b;
+            const float *sb1 = MODE == kGateUp ? p.sb2 + (size_t)brow * p.kb + b
+                                               : sb0 + (T.nt * NB + 1 < p.nblocks ? p.kb : 0);
+            if (even && b + 1 < kb1) {
+                const float2 x = ld_scales<MODE>(reinterpret_cast<const float2 *>(sa));
+                const float2 y = __ldg(reinterpret_cast<const float2 *>(sb0));
+                a0 = x.x, a1 = x.y, b00 = y.x, b01 = y.y;
+                if (NB == 2) {
+                    const float2 z = __ldg(reinterpret_cast<const float2 *>(sb1));
+                    b10 = z.x, b11 = z.y;
+                }
+            } else if (b < kb1) {
+                const int n = b + 1 < kb1;
+                a0 = ld_scales<MODE>(sa), a1 = ld_scales<MODE>(sa + n);
+                b00 = __ldg(sb0), b01 = __ldg(sb0 + n);
+                if (NB == 2) b10 = __ldg(sb1), b11 = __ldg(sb1 + n);
+            }
+        };
+        int it = 0;
         bool ok = true;  // false: an earlier wait gave up; nothing is stored any more
+        if (first < total) {
+            take(first);
+            fetch(kb0);
+        }
         for (int t = first; t < total; t += step) {
-            const Tile T = tile_at<MODE>(p, t);
-            const bool some = (warp % 4) * 32 < T.rows, live = r < T.rows;
-            const int arow = MODE == kGateUp ? (live ? __ldcg(p.token + T.pos + r) : 0)
-                                             : T.pos + (live ? r : 0);
-            const float *sa = p.sa + (size_t)arow * p.kb;
-            // this thread's part of the B scales: thread (wg 0, r < 8 NB)
-            // fetches block r / 8's, input block r % 8
-            const int nb = MODE == kGateUp ? T.nt : min(T.nt * NB + r / 8, p.nblocks - 1);
-            const float *sb = (MODE == kGateUp && r >= 8 ? p.sb2 : p.sb) +
-                              ((size_t)T.e * p.nblocks + nb) * p.kb;
-            constexpr int kAcc = kCols / 2 * NB;  // pairs of this thread's sums
+            const int rows = T.rows;
+            const bool some = (warp % 4) * 32 < rows;
             uint64_t acc[kAcc];
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) acc[i] = 0;
-            constexpr int kPer = 8 / kColGroups;
-            float as[kPer], bs = 0.f;
-            auto fetch = [&](int b) {  // scales of the 8 input blocks from b on
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int j = b + wg * kPer + i;
-                    as[i] = live && j < kb1 ? ld_scale<MODE>(sa + j) : 0.f;
-                }
-                if (wg == 0 && r < 8 * NB) bs = b + r % 8 < kb1 ? __ldg(sb + b + r % 8) : 0.f;
-            };
-            fetch(kb0);
+            float s0 = 0.f, s1 = 0.f, n0 = 0.f, n1 = 0.f;
+            bool hit = bar_done(&tm_full[it & 1], it / 2 & 1);
             for (int b = kb0; b < kb1; ++b, ++it) {
-                const int buf = it & 1, j = (b - kb0) & 7;
-                if (j == 0) {
-                    // A warp may still read the other half; nobody reads this
-                    // one, for all have met since it was in use.
-                    half ^= 1;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) sa_s[half][wg * kPer + i][r] = as[i];
-                    if (wg == 0 && r < 8 * NB) sb_s[half][r % 8][r / 8] = bs;
-                    named_bar(1, kAccWarps * 32);
-                    if (b + 8 < kb1) fetch(b + 8);
+                const int buf = it & 1;
+                if (((b - kb0) & 1) == 0) {
+                    s0 = a0 * b00, s1 = a0 * b10;
+                    n0 = a1 * b01, n1 = a1 * b11;
+                    fetch(b + 2);
+                } else {
+                    s0 = n0, s1 = n1;
                 }
-                const float a = sa_s[half][j][r];
-                const float s0 = a * sb_s[half][j][0], s1 = a * sb_s[half][j][NB - 1];
-                if (ok) ok = __all_sync(~0u, wait_bar(&tm_full[buf], it / 2 & 1, &abort_s));
+                const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
+                if (!__all_sync(~0u, hit) && ok)
+                    ok = __all_sync(~0u, spin_bar(&tm_full[buf], it / 2 & 1, &abort_s));
                 tc_fence_after();
-                if (some && ok) {
-                    const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
-                    // 16 columns at a time, the next ones under way meanwhile
-                    constexpr int kChunks = kCols / 16 * NB;
-                    uint32_t v[2][16];
-                    const uint32_t from = tm_lane + buf * 128 * NB;
-                    tmem_load16(from, v[0]);
+                // 8 columns at a time, the next ones under way meanwhile.
+                // With the last ones in registers the half is given back, and
+                // the next block's barrier is looked up while they are added.
+                constexpr int kPart = kCols / 8, kChunks = kPart * NB;
+                uint32_t v[2][8];
+                const uint32_t from = tm_lane + buf * 128 * NB;
+                if (some && ok) tmem_load8(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        tmem_wait16(v[c & 1]);
+                for (int c = 0; c < kChunks; ++c) {
+                    if (some && ok) {
+                        tmem_wait8(v[c & 1]);
                         if (c + 1 < kChunks)
-                            tmem_load16(from + (c + 1) / (kCols / 16) * 128 +
-                                            (c + 1) % (kCols / 16) * 16,
-                                        v[(c + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            fma2(acc[c * 8 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1],
-                                 c < kCols / 16 ? p0 : p1);
+                            tmem_load8(from + (c + 1) / kPart * 128 + (c + 1) % kPart * 8,
+                                       v[(c + 1) & 1]);
                     }
+                    if (c + 1 == kChunks) {
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive(&tm_empty[buf]);
+                        __syncwarp();
+                        hit = b + 1 < kb1 && bar_done(&tm_full[buf ^ 1], (it + 1) / 2 & 1);
+                    }
+                    if (some && ok)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            fma2(acc[c * 4 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1],
+                                 c < kPart ? p0 : p1);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tm_empty[buf]);
             }
-            bool mine = live && ok;  // this thread stores its row
+            // the next tile's first scales come while this one is stored
+            const Tile done = T;
+            if (t + step < total) {
+                take(t + step);
+                fetch(kb0);
+            }
+            const bool live = r < rows;
+            bool storing = some && ok;  // this warp stores its rows
             if (p.split > 1) {
                 // One tile per cluster.  After the first meeting every load
                 // and MMA of the cluster is complete (each warp has seen its
@@ -342,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 cluster_sync();
                 syncs = 2;
-                mine = mine && rank == owner;
+                storing = storing && rank == owner;
                 if (rank == owner && some && ok) {
                     const float *part = reinterpret_cast<const float *>(
                         smem_raw + (ring - smem_u32(smem_raw)) + slot);
@@ -375,9 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kColGroups; ++i) amax = fmaxf(amax, amax_s[i][r]);
                 named_bar(1, kAccWarps * 32);  // before the next tile writes amax_s
-                if (mine) {
+                if (storing && live) {
                     const float up = kFp8Max / amax;
-                    const size_t at = (size_t)(T.pos + r) * p.n + T.nt * 128 + wg * kCols;
+                    const size_t at = (size_t)(done.pos + r) * p.n + done.nt * 128 + wg * kCols;
 #pragma unroll
                     for (int i = 0; i < kCols / 16; ++i) {
                         uint32_t q[4];
@@ -391,24 +433,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(q[0], q[1], q[2], q[3]);
                     }
                     if (wg == 0)
-                        p.h_scales[(size_t)(T.pos + r) * (p.n / 128) + T.nt] = amax / kFp8Max;
+                        p.h_scales[(size_t)(done.pos + r) * (p.n / 128) + done.nt] = amax / kFp8Max;
                 }
-            } else if (mine) {
-                const size_t orow = MODE == kDown ? (size_t)__ldcg(p.pair + T.pos + r)
-                                                  : (size_t)(T.pos + r);
+            } else if (storing) {
+                // A lane has 32 consecutive outputs of one row; four lanes
+                // exchange them so that a store covers 64 bytes of each of 8
+                // rows (rows apart cost a store one cycle each).
+                const int orow = !live ? 0 : MODE == kDown ? __ldcg(p.pair + done.pos + r)
+                                                           : done.pos + r;
 #pragma unroll
-                for (int c = 0; c < kCols / 16 * NB; ++c) {
-                    const int col = (T.nt * NB + c / (kCols / 16)) * 128 + wg * kCols +
-                                    (c % (kCols / 16)) * 16;
-                    float v[16];
+                for (int c = 0; c < NB; ++c) {
+                    const int col = (done.nt * NB + c) * 128 + wg * kCols;
+                    const bool whole = p.vec_out && col + kCols <= p.n;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = unpack2(acc[c * 8 + i]);
-                        v[2 * i] = f.x;
-                        v[2 * i + 1] = f.y;
+                    for (int h = 0; h < 2; ++h) {
+                        if (p.out_dtype != MOEOP_FP32 && whole) {
+                            if (h) continue;
+                            uint4 u[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint64_t *v = acc + c * 16 + i * 4;
+                                u[i] = make_uint4(pack16(v[0], p.out_dtype), pack16(v[1], p.out_dtype),
+                                                  pack16(v[2], p.out_dtype), pack16(v[3], p.out_dtype));
+                            }
+                            transpose4(u, lane);
+                            store_rows(u, static_cast<char *>(p.out), orow, p.n, col, 2, lane,
+                                       rows - (warp % 4) * 32);
+                        } else if (whole) {
+                            uint4 u[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 x = unpack2(acc[c * 16 + h * 8 + i * 2]);
+                                const float2 y = unpack2(acc[c * 16 + h * 8 + i * 2 + 1]);
+                                u[i] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
+                                                  __float_as_uint(y.x), __float_as_uint(y.y));
+                            }
+                            transpose4(u, lane);
+                            store_rows(u, static_cast<char *>(p.out), orow, p.n, col + h * 16, 4,
+                                       lane, rows - (warp % 4) * 32);
+                        } else if (live) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 f = unpack2(acc[c * 16 + h * 8 + i]);
+                                const int at = col + h * 16 + 2 * i;
+                                if (at < p.n)
+                                    store1(p.out, p.out_dtype, (size_t)orow * p.n + at, f.x);
+                                if (at + 1 < p.n)
+                                    store1(p.out, p.out_dtype, (size_t)orow * p.n + at + 1, f.y);
+                            }
+                        }
                     }
-                    if (col < p.n)
-                        store16(p.out, p.out_dtype, orow * p.n + col, v, p.n - col);
                 }
             }
         }
@@ -575,8 +649,8 @@ void cluster_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *at, int grid, 
 
 template <int MODE, int NB>
 cudaError_t allow_smem() {
-    return cudaFuncSetAttribute(gemm_kernel<MODE, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(ring_bytes<NB>() + 1024));
+    return cudaFuncSetAttribute(gemm_kernel<MODE, NB>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kRing + 1024));
 }
 
 // Looked up once per device: SM count, the kernels' shared-memory limit, the
@@ -610,9 +684,9 @@ cudaError_t device(Dev **out) {
         for (int s = 2; s <= kMaxSplit; ++s) {
             cudaLaunchConfig_t cfg{};
             cudaLaunchAttribute at[1];
-            cluster_config(&cfg, at, s * v.sms, s, kThreads, ring_bytes<2>() + 1024, nullptr);
-            if ((e = cudaOccupancyMaxActiveClusters(&v.clusters[s], gemm_kernel<kGateUp, 2>,
-                                                    &cfg)) != cudaSuccess)
+            cluster_config(&cfg, at, s * v.sms, s, kThreads, kRing + 1024, nullptr);
+            if ((e = cudaOccupancyMaxActiveClusters(
+                     &v.clusters[s], gemm_kernel<kGateUp, 2>, &cfg)) != cudaSuccess)
                 return e;
         }
         v.status = static_cast<uint32_t *>(sym);
@@ -636,11 +710,13 @@ cudaError_t make_map(TensorMap *m, const Fp8Mat &a, uint32_t box_rows) {
 }
 
 template <int MODE, int NB>
-cudaError_t launch(const TensorMap &ma, const TensorMap &mb, const TensorMap &mb2, const Params &p,
+cudaError_t launch(const TensorMap &ma, const TensorMap &mb, const TensorMap &mb2, Params p,
                    int grid, cudaStream_t st) {
+    p.even = p.kb % 2 == 0 && (reinterpret_cast<uintptr_t>(p.sa) | reinterpret_cast<uintptr_t>(p.sb) |
+                               reinterpret_cast<uintptr_t>(p.sb2)) % 8 == 0;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
-    cluster_config(&cfg, at, grid, p.split, kThreads, ring_bytes<NB>() + 1024, st);
+    cluster_config(&cfg, at, grid, p.split, kThreads, kRing + 1024, st);
     if (p.split == 1) cfg.numAttrs = 0;
     return cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, NB>, ma, mb, mb2, p);
 }
@@ -678,9 +754,11 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
     p.sb = p.sb2 = sb;
     p.out = out;
     p.out_dtype = out_dtype;
+    p.vec_out = (size_t)p.n * (out_dtype == MOEOP_FP32 ? 4 : 2) % 16 == 0 &&
+                reinterpret_cast<uintptr_t>(out) % 16 == 0;
     p.tiles_m = (p.rows + 127) / 128;
-    // Tiles of 128 x 256 feed the tensor core with fewer shared-memory reads
-    // per MMA; tiles of 128 x 128 where they need fewer waves of the SMs.
+    // Tiles of 128 x 256 read less from L2 and shared memory per product;
+    // tiles of 128 x 128 where they need fewer waves of the SMs.
     const int64_t t1 = (int64_t)p.tiles_m * p.nblocks;
     const int64_t t2 = (int64_t)p.tiles_m * ((p.nblocks + 1) / 2);
     const bool wide = 11 * ((t1 + d->sms - 1) / d->sms) >= 20 * ((t2 + d->sms - 1) / d->sms);
@@ -752,12 +830,14 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     p.nblocks = H / 128;
     p.out = y;
     p.out_dtype = MOEOP_BF16;
+    p.vec_out = true;
     const bool wide = (int64_t)w.max_tiles * ((p.nblocks + 1) / 2) >= d->sms;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     most = (int64_t)w.max_tiles * p.tiles_n;
     p.split = split_of(*d, most, p.kb);
     grid = p.split > 1 ? (int)most * p.split : (int)(most < d->sms ? most : d->sms);
-    e = wide ? launch<kDown, 2>(mh, md, md, p, grid, st) : launch<kDown, 1>(mh, md, md, p, grid, st);
+    e = wide ? launch<kDown, 2>(mh, md, md, p, grid, st) 
+             : launch<kDown, 1>(mh, md, md, p, grid, st);
     if (e != cudaSuccess) return e;
 
     CombineParams cp{a.ids, a.wts, y, a.addend, a.out, a.rows, H, k, E};
