@@ -67,6 +67,9 @@ struct Params {
     const int *num_tiles;
     const int4 *tiles;        // expert, first position, rows
     const int *pair, *token;
+    int few;                  // pairs of a call without an index, else 0
+    const int32_t *ids;
+    int experts, top_k;
     uint8_t *h;
     float *h_scales;
 };
@@ -75,17 +78,64 @@ struct Tile {
     int e, pos, rows, nt;
 };
 
+// A warp's view of the tiles and of the pairs in their rows.  The experts'
+// lists come from the index kernel; calls of at most 32 pairs do without it:
+// every warp holds all ids, one to a lane, and works the same lists out.
 template <int MODE>
-__device__ __forceinline__ int tile_count(const Params &p) {
-    return MODE == kDense ? p.tiles_m * p.tiles_n : __ldcg(p.num_tiles) * p.tiles_n;
-}
-template <int MODE>
-__device__ __forceinline__ Tile tile_at(const Params &p, int t) {
-    const int mt = t / p.tiles_n, nt = t % p.tiles_n;
-    if (MODE == kDense) return {0, mt * 128, min(128, p.rows - mt * 128), nt};
-    const int4 d = __ldcg(p.tiles + mt);
-    return {d.x, d.y, d.z, nt};
-}
+struct Lists {
+    uint32_t leaders, peers;  // few: the first lanes of an expert; lanes with this lane's
+    int id, start;            // few: this lane's expert; position of its first row
+    int tiles;
+
+    __device__ __forceinline__ Lists(const Params &p, int lane) {
+        leaders = 0;
+        if (MODE == kDense) {
+            tiles = p.tiles_m;
+        } else if (!p.few) {
+            tiles = __ldcg(p.num_tiles);
+        } else {
+            id = lane < p.few ? __ldg(p.ids + lane) : -1;
+            const bool in = (unsigned)id < (unsigned)p.experts;
+            peers = __match_any_sync(~0u, in ? id : -1 - lane);
+            const bool leader = in && __ffs(peers) - 1 == lane;
+            leaders = __ballot_sync(~0u, leader);
+            const int n = leader ? __popc(peers) : 0;
+            start = n;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int v = __shfl_up_sync(~0u, start, o);
+                if (lane >= o) start += v;
+            }
+            start -= n;
+            tiles = __popc(leaders);
+        }
+    }
+    // Of all lanes together.
+    __device__ __forceinline__ Tile at(const Params &p, int t) const {
+        const int mt = t / p.tiles_n, nt = t % p.tiles_n;
+        if (MODE == kDense) return {0, mt * 128, min(128, p.rows - mt * 128), nt};
+        if (p.few) {
+            uint32_t m = leaders;
+            for (int i = 0; i < mt; ++i) m &= m - 1;
+            const int lead = __ffs(m) - 1;
+            return {__shfl_sync(~0u, id, lead), __shfl_sync(~0u, start, lead),
+                    __popc(__shfl_sync(~0u, peers, lead)), nt};
+        }
+        const int4 d = __ldcg(p.tiles + mt);
+        return {d.x, d.y, d.z, nt};
+    }
+    // The pair in row i (valid, any per lane) of tile T.  Of all lanes together.
+    __device__ __forceinline__ int pair(const Params &p, const Tile &T, int i) const {
+        if (!p.few) return __ldcg(p.pair + T.pos + i);
+        const uint32_t mine = __ballot_sync(~0u, id == T.e);
+        uint32_t m = mine;
+        for (int j = 0; j < i; ++j) m &= m - 1;
+        return __ffs(m) - 1;
+    }
+    __device__ __forceinline__ int token(const Params &p, const Tile &T, int i) const {
+        return p.few ? pair(p, T, i) / p.top_k : __ldcg(p.token + T.pos + i);
+    }
+};
 
 // Scales of the A rows; h's were written by the kernel before.
 template <int MODE, typename F>
@@ -138,27 +188,31 @@ __device__ __forceinline__ void store_rows(const uint4 (&u)[4], char *out, int o
     }
 }
 
-template <int MODE, int NB>
+// SPLIT: the inputs are split over a cluster (its own kernel: the code for it
+// costs the others registers that they have no spare of).
+template <int MODE, int NB, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ TensorMap ma, const __grid_constant__ TensorMap mb,
                 const __grid_constant__ TensorMap mb2, const Params p) {
     constexpr int S = stages<NB>();
     constexpr int kStage = (1 + NB) * kTile;
+    constexpr int kBufs = 2;       // halves of tensor memory
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[S], empty[S], tm_full[2], tm_empty[2];
+    __shared__ uint64_t full[S], empty[S], tm_full[kBufs], tm_empty[kBufs];
     __shared__ float amax_s[kColGroups][128];
     __shared__ uint32_t tm_base;
     __shared__ int abort_s;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const int rank = p.split > 1 ? (int)cluster_rank() : 0;
+    const int rank = SPLIT ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         // a stage is free again when its MMAs are complete and, with three
         // loading warps, the other two are past it: none can be lapped
         for (int i = 0; i < S; ++i)
             mbar_init(&full[i], 1), mbar_init(&empty[i], MODE == kGateUp ? 3 : 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&tm_full[i], 1), mbar_init(&tm_empty[i], kAccWarps);
+        for (int i = 0; i < kBufs; ++i)
+            mbar_init(&tm_full[i], 1), mbar_init(&tm_empty[i], kAccWarps);
         abort_s = 0;
         fence_mbar_init();
     }
@@ -173,9 +227,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tm = tm_base;
 
-    const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
-    const int kb0 = rank * p.kb / p.split, kb1 = (rank + 1) * p.kb / p.split;
-    const int total = tile_count<MODE>(p);
+    const int split = SPLIT ? p.split : 1;
+    const int first = blockIdx.x / split, step = gridDim.x / split;
+    const int kb0 = SPLIT ? rank * p.kb / split : 0;
+    const int kb1 = SPLIT ? (rank + 1) * p.kb / split : p.kb;
+    pdl_wait();
+    const Lists<MODE> lists(p, lane);
+    const int total = lists.tiles * p.tiles_n;
     int syncs = 0;  // of this thread with its cluster: two in every split block
 
     if (warp >= kLoadWarp && warp != kMmaWarp) {
@@ -185,16 +243,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         bool ok = true;
         for (int t = first; t < total && ok && (MODE == kGateUp || part == 0); t += step) {
-            const Tile T = tile_at<MODE>(p, t);
+            const Tile T = lists.at(p, t);
             const int e = uniform(T.e), pos = uniform(T.pos), rows = uniform(T.rows);
             const int quads = (rows + 3) / 4, boxes = (rows + kBoxRows - 1) / kBoxRows;
+            // Gathered: the tokens of rows 4 lane .. + 3, past the end the last
+            // one again.
             int4 rows4 = make_int4(0, 0, 0, 0);
             if (MODE == kGateUp) {
-                // tokens of rows 4 lane .. + 3; past the end the last one again
                 int *r = &rows4.x;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    r[i] = __ldcg(p.token + pos + min(4 * lane + i, rows - 1));
+                    r[i] = lists.token(p, T, min(4 * lane + i, rows - 1));
             }
             const int b0 = e * p.n + T.nt * (MODE == kGateUp ? 128 : 128 * NB);
             const uint32_t bytes =
@@ -253,8 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(&tm_full[buf]);
                 }
                 __syncwarp();
-                phase ^= buf;
-                buf ^= 1;
+                if (++buf == kBufs) buf = 0, phase ^= 1;
                 if (++s == S) s = 0, ring_phase ^= 1;
             }
         }
@@ -266,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int arow = 0, brow = 0;               // where its scales are
         Tile T{};
         auto take = [&](int t) {
-            T = tile_at<MODE>(p, t);
-            arow = r >= T.rows ? 0 : MODE == kGateUp ? __ldcg(p.token + T.pos + r) : T.pos + r;
+            T = lists.at(p, t);
+            const int row = min(r, T.rows - 1);  // past the end the last one again
+            arow = MODE == kGateUp ? lists.token(p, T, row) : T.pos + row;
             brow = T.e * p.nblocks + T.nt * (MODE == kGateUp ? 1 : NB);
         };
         // The scales of input blocks b and b + 1: this row's, and those of the
@@ -278,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float a0 = 0.f, a1 = 0.f, b00 = 0.f, b01 = 0.f, b10 = 0.f, b11 = 0.f;
         const bool even = p.even && kb0 % 2 == 0;
         auto fetch = [&](int b) {
+            if ((warp % 4) * 32 >= T.rows) return;
             const float *sa = p.sa + (size_t)arow * p.kb + b;
             const float *sb0 = p.sb + (size_t)brow * p.kb + b;
             const float *sb1 = MODE == kGateUp ? p.sb2 + (size_t)brow * p.kb + b
@@ -310,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) acc[i] = 0;
             float s0 = 0.f, s1 = 0.f, n0 = 0.f, n1 = 0.f;
-            bool hit = bar_done(&tm_full[it & 1], it / 2 & 1);
+            bool hit = bar_done(&tm_full[it % kBufs], it / kBufs & 1);
             for (int b = kb0; b < kb1; ++b, ++it) {
-                const int buf = it & 1;
+                const int buf = it % kBufs;
                 if (((b - kb0) & 1) == 0) {
                     s0 = a0 * b00, s1 = a0 * b10;
                     n0 = a1 * b01, n1 = a1 * b11;
@@ -322,34 +382,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
                 if (!__all_sync(~0u, hit) && ok)
-                    ok = __all_sync(~0u, spin_bar(&tm_full[buf], it / 2 & 1, &abort_s));
+                    ok = __all_sync(~0u, spin_bar(&tm_full[buf], it / kBufs & 1, &abort_s));
                 tc_fence_after();
-                // 8 columns at a time, the next ones under way meanwhile.
-                // With the last ones in registers the half is given back, and
-                // the next block's barrier is looked up while they are added.
+                // 8 columns at a time: registers are what these warps are short
+                // of, and four of them to a scheduler hide each other's loads.
+                // With the last columns in registers the half is given back,
+                // and the next block's barrier is looked up while they are added.
                 constexpr int kPart = kCols / 8, kChunks = kPart * NB;
-                uint32_t v[2][8];
                 const uint32_t from = tm_lane + buf * 128 * NB;
-                if (some && ok) tmem_load8(from, v[0]);
+                uint32_t v[8];
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
-                    if (some && ok) {
-                        tmem_wait8(v[c & 1]);
-                        if (c + 1 < kChunks)
-                            tmem_load8(from + (c + 1) / kPart * 128 + (c + 1) % kPart * 8,
-                                       v[(c + 1) & 1]);
-                    }
+                    if (some && ok) tmem_load8(from + c / kPart * 128 + c % kPart * 8, v);
                     if (c + 1 == kChunks) {
                         tc_fence_before();
                         if (lane == 0) mbar_arrive(&tm_empty[buf]);
                         __syncwarp();
-                        hit = b + 1 < kb1 && bar_done(&tm_full[buf ^ 1], (it + 1) / 2 & 1);
+                        hit = b + 1 < kb1 &&
+                              bar_done(&tm_full[(it + 1) % kBufs], (it + 1) / kBufs & 1);
                     }
                     if (some && ok)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            fma2(acc[c * 4 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1],
-                                 c < kPart ? p0 : p1);
+                            fma2(acc[c * 4 + i], v[2 * i], v[2 * i + 1], c < kPart ? p0 : p1);
                 }
             }
             // the next tile's first scales come while this one is stored
@@ -360,11 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool live = r < rows;
             bool storing = some && ok;  // this warp stores its rows
-            if (p.split > 1) {
+            if (SPLIT) {
                 // One tile per cluster.  After the first meeting every load
                 // and MMA of the cluster is complete (each warp has seen its
                 // last tm_full) and the rings are free; buffer q of a ring
-                // holds the sums of the q-th other rank, column by column.
+                // holds the sums of the q-th other rank, column by column, so
+                // that a warp's store to another block is 128 bytes in a row.
                 const int block = warp % 4, owner = block % p.split;
                 constexpr uint32_t kBuf = 128 * NB * 32 * 4;
                 const uint32_t slot = (block / p.split * (p.split - 1)) * kBuf +
@@ -385,15 +441,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 cluster_sync();
                 syncs = 2;
                 storing = storing && rank == owner;
-                if (rank == owner && some && ok) {
+                if (storing) {
                     const float *part = reinterpret_cast<const float *>(
                         smem_raw + (ring - smem_u32(smem_raw)) + slot);
                     for (int q = 0; q < p.split - 1; ++q, part += kBuf / 4)
 #pragma unroll
                         for (int i = 0; i < kAcc; ++i) {
-                            const float2 f = unpack2(acc[i]);
                             const int at =
                                 ((i / (kCols / 2)) * 128 + (i % (kCols / 2)) * 2) * 32;
+                            const float2 f = unpack2(acc[i]);
                             acc[i] = pack2(f.x + part[at], f.y + part[at + 32]);
                         }
                 }
@@ -439,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // A lane has 32 consecutive outputs of one row; four lanes
                 // exchange them so that a store covers 64 bytes of each of 8
                 // rows (rows apart cost a store one cycle each).
-                const int orow = !live ? 0 : MODE == kDown ? __ldcg(p.pair + done.pos + r)
-                                                           : done.pos + r;
+                const int row = min(r, rows - 1);
+                const int orow = MODE == kDown ? lists.pair(p, done, row) : done.pos + row;
 #pragma unroll
                 for (int c = 0; c < NB; ++c) {
                     const int col = (done.nt * NB + c) * 128 + wg * kCols;
@@ -489,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // The accumulating warps have met their cluster twice; the other warps,
     // and all of a block without a tile, do so here.
-    if (p.split > 1)
+    if (SPLIT)
         for (; syncs < 2; ++syncs) cluster_sync();
     tc_fence_before();
     __syncthreads();
@@ -513,10 +569,12 @@ struct IndexParams {
     int4 *tiles;
 };
 
+template <int RANKS>
 __global__ void __launch_bounds__(1024) index_kernel(IndexParams p) {
     __shared__ int hist[MOEOP_MAX_EXPERTS], cursor[MOEOP_MAX_EXPERTS];
     __shared__ int warp_rows[32], warp_tiles[32];
-    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    pdl_trigger();
+    const int rank = RANKS > 1 ? (int)cluster_rank() : 0, ranks = RANKS;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     hist[tid] = 0;
     __syncthreads();
@@ -524,12 +582,16 @@ __global__ void __launch_bounds__(1024) index_kernel(IndexParams p) {
         const int e = __ldg(p.ids + i);
         if ((unsigned)e < (unsigned)p.experts) atomicAdd(&hist[e], 1);
     }
-    cluster_sync();
-    int rows = 0, lower = 0;
-    for (int q = 0; q < ranks; ++q) {
-        const int v = ld_cluster_i(map_rank(smem_u32(&hist[tid]), q));
-        if (q < rank) lower += v;
-        rows += v;
+    if (RANKS > 1) cluster_sync();
+    else __syncthreads();
+    int counts[RANKS], rows = 0, lower = 0;
+#pragma unroll
+    for (int q = 0; q < RANKS; ++q)
+        counts[q] = RANKS > 1 ? ld_cluster_i(map_rank(smem_u32(&hist[tid]), q)) : hist[tid];
+#pragma unroll
+    for (int q = 0; q < RANKS; ++q) {
+        if (q < rank) lower += counts[q];
+        rows += counts[q];
     }
     // exclusive prefix sums of the rows and of the tiles of 128
     const int tiles = (rows + 127) / 128;
@@ -568,22 +630,27 @@ __global__ void __launch_bounds__(1024) index_kernel(IndexParams p) {
             p.token[at] = (int)(i / p.top_k);
         }
     }
-    cluster_sync();  // the others have read this block's counts
+    if (RANKS > 1) cluster_sync();  // the others have read this block's counts
 }
 
 // ---------------------------------------------------------------------------
 // out[t] = sum_j wts[t][j] y[t * k + j] (+ addend[t]), in slot order
 // ---------------------------------------------------------------------------
-// Bound by memory: k bf16 rows in, one out.  A thread owns 8 outputs.
+// Bound by memory: k rows in, one out.  A thread owns 8 outputs and has the
+// loads of kSlots slots under way at a time.  Y32: y is held in fp32.
 struct CombineParams {
     const int32_t *ids;
     const float *wts;
-    const uint16_t *y, *addend;
+    const void *y;
+    const uint16_t *addend;
     uint16_t *out;
     int rows, hidden, top_k, experts;
 };
 
+template <bool Y32>
 __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
+    constexpr int kSlots = Y32 ? 4 : 8;
+    pdl_wait();
     const int per_row = p.hidden / 8;
     const int64_t n = (int64_t)p.rows * per_row;
     for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
@@ -598,16 +665,34 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[2 * j] = bf16_lo(u[j]), acc[2 * j + 1] = bf16_hi(u[j]);
         }
-        for (int j = 0; j < p.top_k; ++j) {
-            const int64_t pair = t * p.top_k + j;
-            if ((unsigned)__ldg(p.ids + pair) >= (unsigned)p.experts) continue;
-            const float w = __ldg(p.wts + pair);
-            const uint4 v = ld_cg_v4(p.y + pair * p.hidden + col);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
+            // a slot without an expert has no row y: what lies there is read
+            // and not used
+            uint4 v[kSlots][Y32 ? 2 : 1];
+            float w[kSlots];
+            bool in[kSlots];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                acc[2 * c] = fmaf(w, bf16_lo(u[c]), acc[2 * c]);
-                acc[2 * c + 1] = fmaf(w, bf16_hi(u[c]), acc[2 * c + 1]);
+            for (int j = 0; j < kSlots; ++j) {
+                const int64_t pair = t * p.top_k + min(j0 + j, p.top_k - 1);
+                in[j] = j0 + j < p.top_k &&
+                        (unsigned)__ldg(p.ids + pair) < (unsigned)p.experts;
+                w[j] = __ldg(p.wts + pair);
+                const char *y = static_cast<const char *>(p.y) +
+                                (pair * p.hidden + col) * (Y32 ? 4 : 2);
+                v[j][0] = ld_cg_v4(y);
+                if (Y32) v[j][Y32 ? 1 : 0] = ld_cg_v4(y + 16);
+            }
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (!in[j]) continue;
+                const uint4 a = v[j][0], b = v[j][Y32 ? 1 : 0];
+                const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float f = Y32 ? __uint_as_float(u[c])
+                                        : c & 1 ? bf16_hi(u[c / 2]) : bf16_lo(u[c / 2]);
+                    acc[c] = fmaf(w[j], f, acc[c]);
+                }
             }
         }
         uint32_t o[4];
@@ -633,23 +718,34 @@ struct Dev {
     uint32_t *status = nullptr;
 } g_devs[64];
 
-// A launch of `grid` blocks in clusters of `size`.
-void cluster_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *at, int grid, int size,
-                    int threads, size_t smem, cudaStream_t st) {
-    cfg->gridDim = dim3(grid);
-    cfg->blockDim = dim3(threads);
-    cfg->dynamicSmemBytes = smem;
-    cfg->stream = st;
-    at->id = cudaLaunchAttributeClusterDimension;
-    at->val.clusterDim.x = size;
-    at->val.clusterDim.y = at->val.clusterDim.z = 1;
-    cfg->attrs = at;
-    cfg->numAttrs = 1;
-}
+// A launch of `grid` blocks in clusters of `size`; `early`: it may start while
+// the kernel before it still runs (and waits for it before its first read).
+struct Launch {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[2];
+    Launch(int64_t grid, int size, int threads, size_t smem, bool early, cudaStream_t st) {
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = at;
+        if (size > 1) {
+            at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            at[cfg.numAttrs].val.clusterDim.x = size;
+            at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+            ++cfg.numAttrs;
+        }
+        if (early) {
+            at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+            ++cfg.numAttrs;
+        }
+    }
+};
 
-template <int MODE, int NB>
+template <int MODE, int NB, bool SPLIT>
 cudaError_t allow_smem() {
-    return cudaFuncSetAttribute(gemm_kernel<MODE, NB>,
+    return cudaFuncSetAttribute(gemm_kernel<MODE, NB, SPLIT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kRing + 1024));
 }
 
@@ -674,19 +770,20 @@ cudaError_t device(Dev **out) {
         }
         void *sym = nullptr;
         if ((e = cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, d)) != cudaSuccess ||
-            (e = allow_smem<kDense, 1>()) != cudaSuccess ||
-            (e = allow_smem<kDense, 2>()) != cudaSuccess ||
-            (e = allow_smem<kGateUp, 2>()) != cudaSuccess ||
-            (e = allow_smem<kDown, 1>()) != cudaSuccess ||
-            (e = allow_smem<kDown, 2>()) != cudaSuccess ||
+            (e = allow_smem<kDense, 1, false>()) != cudaSuccess ||
+            (e = allow_smem<kDense, 1, true>()) != cudaSuccess ||
+            (e = allow_smem<kDense, 2, false>()) != cudaSuccess ||
+            (e = allow_smem<kGateUp, 2, false>()) != cudaSuccess ||
+            (e = allow_smem<kGateUp, 2, true>()) != cudaSuccess ||
+            (e = allow_smem<kDown, 1, false>()) != cudaSuccess ||
+            (e = allow_smem<kDown, 1, true>()) != cudaSuccess ||
+            (e = allow_smem<kDown, 2, false>()) != cudaSuccess ||
             (e = cudaGetSymbolAddress(&sym, g_status)) != cudaSuccess)
             return e;
         for (int s = 2; s <= kMaxSplit; ++s) {
-            cudaLaunchConfig_t cfg{};
-            cudaLaunchAttribute at[1];
-            cluster_config(&cfg, at, s * v.sms, s, kThreads, kRing + 1024, nullptr);
-            if ((e = cudaOccupancyMaxActiveClusters(
-                     &v.clusters[s], gemm_kernel<kGateUp, 2>, &cfg)) != cudaSuccess)
+            Launch l(s * v.sms, s, kThreads, kRing + 1024, false, nullptr);
+            if ((e = cudaOccupancyMaxActiveClusters(&v.clusters[s],
+                                                    gemm_kernel<kGateUp, 2, true>, &l.cfg)) != cudaSuccess)
                 return e;
         }
         v.status = static_cast<uint32_t *>(sym);
@@ -711,14 +808,16 @@ cudaError_t make_map(TensorMap *m, const Fp8Mat &a, uint32_t box_rows) {
 
 template <int MODE, int NB>
 cudaError_t launch(const TensorMap &ma, const TensorMap &mb, const TensorMap &mb2, Params p,
-                   int grid, cudaStream_t st) {
+                   int64_t grid, bool early, cudaStream_t st) {
     p.even = p.kb % 2 == 0 && (reinterpret_cast<uintptr_t>(p.sa) | reinterpret_cast<uintptr_t>(p.sb) |
                                reinterpret_cast<uintptr_t>(p.sb2)) % 8 == 0;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    cluster_config(&cfg, at, grid, p.split, kThreads, kRing + 1024, st);
-    if (p.split == 1) cfg.numAttrs = 0;
-    return cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, NB>, ma, mb, mb2, p);
+    Launch l(grid, p.split, kThreads, kRing + 1024, early, st);
+    // two blocks of outputs to a tile only come without a split, but for the
+    // gate and up products
+    if (p.split > 1)
+        return cudaLaunchKernelEx(&l.cfg, gemm_kernel<MODE, MODE == kGateUp ? NB : 1, true>, ma, mb,
+                                  mb2, p);
+    return cudaLaunchKernelEx(&l.cfg, gemm_kernel<MODE, NB, false>, ma, mb, mb2, p);
 }
 
 // Blocks per cluster that share one tile's inputs: as many as still let all
@@ -764,13 +863,13 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
     const bool wide = 11 * ((t1 + d->sms - 1) / d->sms) >= 20 * ((t2 + d->sms - 1) / d->sms);
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     const int64_t tiles = wide ? t2 : t1;
-    p.split = split_of(*d, tiles, p.kb);
+    p.split = wide ? 1 : split_of(*d, tiles, p.kb);
     TensorMap ma, mb;
     if ((e = make_map(&ma, a, kBoxRows)) != cudaSuccess || (e = make_map(&mb, b, 128)) != cudaSuccess)
         return e;
-    const int grid = p.split > 1 ? (int)tiles * p.split : (int)(tiles < d->sms ? tiles : d->sms);
-    return wide ? launch<kDense, 2>(ma, mb, mb, p, grid, st)
-                : launch<kDense, 1>(ma, mb, mb, p, grid, st);
+    const int64_t grid = p.split > 1 ? tiles * p.split : tiles < d->sms ? tiles : d->sms;
+    return wide ? launch<kDense, 2>(ma, mb, mb, p, grid, false, st)
+                : launch<kDense, 1>(ma, mb, mb, p, grid, false, st);
 }
 
 cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
@@ -796,19 +895,26 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
         (e = make_map(&md, {a.w.down, (int64_t)E * H, I, I}, 128)) != cudaSuccess)
         return e;
 
-    // one block up to 4096 pairs, else a cluster of 8
-    IndexParams ip{a.ids, (int)P, k, E, num_tiles, pair, token, tiles};
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    const int ranks = P <= 4096 ? 1 : 8;
-    cluster_config(&cfg, at, ranks, ranks, 1024, 0, st);
-    if ((e = cudaLaunchKernelEx(&cfg, index_kernel, ip)) != cudaSuccess) return e;
+    // No index for up to 32 pairs; one block up to 4096, else a cluster of 8.
+    const bool few = P <= 32;
+    if (!few) {
+        const IndexParams ip{a.ids, (int)P, k, E, num_tiles, pair, token, tiles};
+        const int ranks = P <= 4096 ? 1 : 8;
+        Launch l(ranks, ranks, 1024, 0, false, st);
+        e = ranks == 1 ? cudaLaunchKernelEx(&l.cfg, index_kernel<1>, ip)
+                       : cudaLaunchKernelEx(&l.cfg, index_kernel<8>, ip);
+        if (e != cudaSuccess) return e;
+    }
 
     Params p{};
     p.num_tiles = num_tiles;
     p.tiles = tiles;
     p.pair = pair;
     p.token = token;
+    p.few = few ? (int)P : 0;
+    p.ids = a.ids;
+    p.experts = E;
+    p.top_k = k;
     p.h = h;
     p.h_scales = h_scales;
     p.sa = a.scales;
@@ -820,8 +926,8 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     // the number of tiles is known on the device only: its upper bound
     int64_t most = (int64_t)w.max_tiles * p.tiles_n;
     p.split = split_of(*d, most, p.kb);
-    int grid = p.split > 1 ? (int)most * p.split : (int)(most < d->sms ? most : d->sms);
-    if ((e = launch<kGateUp, 2>(mq, mg, mu, p, grid, st)) != cudaSuccess) return e;
+    int64_t grid = p.split > 1 ? most * p.split : most < d->sms ? most : d->sms;
+    if ((e = launch<kGateUp, 2>(mq, mg, mu, p, grid, !few, st)) != cudaSuccess) return e;
 
     p.sa = h_scales;
     p.sb = p.sb2 = a.w.down_scales;
@@ -829,21 +935,22 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     p.kb = I / 128;
     p.nblocks = H / 128;
     p.out = y;
-    p.out_dtype = MOEOP_BF16;
+    p.out_dtype = w.y32 ? MOEOP_FP32 : MOEOP_BF16;
     p.vec_out = true;
     const bool wide = (int64_t)w.max_tiles * ((p.nblocks + 1) / 2) >= d->sms;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     most = (int64_t)w.max_tiles * p.tiles_n;
-    p.split = split_of(*d, most, p.kb);
-    grid = p.split > 1 ? (int)most * p.split : (int)(most < d->sms ? most : d->sms);
-    e = wide ? launch<kDown, 2>(mh, md, md, p, grid, st) 
-             : launch<kDown, 1>(mh, md, md, p, grid, st);
+    p.split = wide ? 1 : split_of(*d, most, p.kb);
+    grid = p.split > 1 ? most * p.split : most < d->sms ? most : d->sms;
+    e = wide ? launch<kDown, 2>(mh, md, md, p, grid, true, st)
+             : launch<kDown, 1>(mh, md, md, p, grid, true, st);
     if (e != cudaSuccess) return e;
 
-    CombineParams cp{a.ids, a.wts, y, a.addend, a.out, a.rows, H, k, E};
+    const CombineParams cp{a.ids, a.wts, y, a.addend, a.out, a.rows, H, k, E};
     const int64_t blocks = ((int64_t)a.rows * (H / 8) + 255) / 256;
-    combine_kernel<<<(int)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(cp);
-    return cudaGetLastError();
+    Launch l(blocks < 65536 ? blocks : 65536, 1, 256, 0, true, st);
+    return w.y32 ? cudaLaunchKernelEx(&l.cfg, combine_kernel<true>, cp)
+                 : cudaLaunchKernelEx(&l.cfg, combine_kernel<false>, cp);
 }
 
 }  // namespace op

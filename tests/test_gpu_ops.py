@@ -309,7 +309,8 @@ def check_experts(x, ids, wts, lay, **kw):
 @pytest.mark.parametrize("t,e,k,h,i", [
     (1, 1, 1, 128, 128), (1, 16, 4, 256, 128), (3, 8, 8, 384, 256), (7, 16, 2, 2048, 768),
     (40, 3, 2, 256, 384), (130, 4, 4, 512, 128), (300, 1, 1, 640, 256), (257, 37, 6, 384, 640),
-    (64, 64, 8, 1024, 256), (1000, 16, 4, 256, 256), (2, 1024, 64, 128, 128)])
+    (64, 64, 8, 1024, 256), (1000, 16, 4, 256, 256), (2, 1024, 64, 128, 128), (4, 40, 8, 512, 384),
+    (33, 5, 1, 256, 256)])
 def test_experts_sizes(t, e, k, h, i):
     ids, wts = choice(t, k, e)
     check_experts(randn(t, h, seed=9), ids, wts, layer(e, h, i))
