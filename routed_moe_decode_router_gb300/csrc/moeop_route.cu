@@ -19,7 +19,9 @@
 // |key|.  About one row in a thousand takes the second way with N(0, 1.5)
 // logits, 256 experts and a bias.  64-bit arithmetic is slow here (an SM does
 // two such operations a cycle): where only the order of the keys is in doubt,
-// as nearly always, just the candidates' keys are computed, one to a lane.
+// as nearly always, just the candidates' keys are computed, one to a lane, and
+// the same for a sigmoid group's place; else the block's threads share the
+// row's experts out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,7 +35,8 @@ namespace op {
 
 namespace {
 
-constexpr int kWarps = 4;  // rows per block
+// Rows per block: 8, at most 48 KB of shared memory for them.
+constexpr int warps_of(int vpt) { return vpt == 32 ? 4 : 8; }
 constexpr float kUlp = 5.9604645e-8f;
 
 // What the kernel needs beside the caller's arguments, worked out once.
@@ -84,9 +87,10 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 
 // Scores of the groups from s[0..E) (dead experts -inf), in lane g for group
-// g; -inf beyond the groups and for groups with nothing left.
+// g; -inf beyond the groups and for groups with nothing left.  *least: the
+// smallest of the values that make the score.
 template <typename F>
-__device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane) {
+__device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane, F *least) {
     const int sh = q.lane_shift, lanes = 1 << sh, g = lane >> sh, sub = lane & (lanes - 1);
     const F none = -INFINITY;
     F a = none, b = none;  // the two largest
@@ -110,8 +114,9 @@ __device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane) {
         b = fmax(fmin(a, oa), fmax(b, ob));
         a = fmax(a, oa);
     }
-    if (q.p.c.group_score == MOEOP_GROUP_TOP2 && b > none) a += b;
-    const F mine = __shfl_sync(~0u, a, (lane << sh) & 31);
+    const bool two = q.p.c.group_score == MOEOP_GROUP_TOP2 && b > none;
+    *least = __shfl_sync(~0u, two ? b : a, (lane << sh) & 31);
+    const F mine = __shfl_sync(~0u, two ? a + b : a, (lane << sh) & 31);
     return lane < q.p.c.groups ? mine : none;
 }
 
@@ -131,45 +136,56 @@ __device__ __forceinline__ double prob_wide(float l, bool soft, double mx, doubl
     return soft ? exp((double)l - mx) / sum : 1.0 / (1.0 + exp(-(double)l));
 }
 
-// The row again in 64 bits, its keys in `key` (E doubles of this warp): few
-// rows come here, and registers for them would cost all rows occupancy.  An
-// SM does two 64-bit operations a cycle, so the keys are compared as integers.
+// A row again in 64 bits, by the whole block: few rows come here, but an SM
+// does two 64-bit operations a cycle and an exp takes a warp a microsecond,
+// so the experts are spread over all threads.  The keys are compared as
+// integers.  key, prob: E doubles each; lane and warp of the calling thread;
+// `owner`: the warp that selects.  The block's threads call it together.
 template <int DT>
-__device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, double *key) {
+__device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, int warp, int owner,
+                                            double *key, double *prob, double *sums) {
     const RouteParams &p = q.p;
     const moeop_route_config &c = p.c;
-    const int E = c.num_experts, k = c.top_k;
+    const int E = c.num_experts, k = c.top_k, threads = blockDim.x;
     const int64_t base = (int64_t)row * p.stride;
     const bool soft = c.scoring == MOE_SCORING_SOFTMAX;
-    double mx = -INFINITY, sum = 0.0;
+    __syncthreads();  // the arrays are free
+    double sum = 1.0;
     if (soft) {
         float m = -INFINITY;
         for (int e = lane; e < E; e += 32) {
             const float l = load_logit<DT>(p.logits, base + e);
             if (!is_dead(l)) m = fmaxf(m, l);
         }
-        mx = warp_max(m);
-#pragma unroll 4
-        for (int e = lane; e < E; e += 32) {
+        const double mx = warp_max(m);
+        sum = 0.0;
+        for (int e = threadIdx.x; e < E; e += threads) {
             const float l = load_logit<DT>(p.logits, base + e);
-            sum += is_dead(l) ? 0.0 : exp((double)l - mx);
+            prob[e] = is_dead(l) ? 0.0 : exp((double)l - mx);
+            sum += prob[e];
         }
         sum = warp_sum(sum);
+        if (lane == 0) sums[warp] = sum;
+        __syncthreads();
+        sum = 0.0;
+        for (int w = 0; w < threads / 32; ++w) sum += sums[w];
+    }
+    for (int e = threadIdx.x; e < E; e += threads) {
+        const float l = load_logit<DT>(p.logits, base + e);
+        const bool dead = is_dead(l);
+        const double v = dead ? 0.0 : soft ? prob[e] / sum : 1.0 / (1.0 + exp(-(double)l));
+        prob[e] = v;
+        key[e] = dead ? -INFINITY : v + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+    }
+    __syncthreads();
+    if (warp != owner) return;
+    uint32_t in = ~0u;
+    if (c.groups > 1) {
+        double least;
+        const double score = group_scores<double>(key, q, lane, &least);
+        in = take_groups<double>(score, q, lane);
     }
     __syncwarp();
-    uint32_t in = ~0u;
-    if (p.bias || c.groups > 1) {
-#pragma unroll 4
-        for (int e = lane; e < E; e += 32) {
-            const float l = load_logit<DT>(p.logits, base + e);
-            const double biased =
-                prob_wide(l, soft, mx, sum) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
-            key[e] = is_dead(l) ? -INFINITY : biased;
-        }
-        __syncwarp();
-        if (c.groups > 1) in = take_groups<double>(group_scores<double>(key, q, lane), q, lane);
-        __syncwarp();
-    }
     uint64_t *ord = reinterpret_cast<uint64_t *>(key);
     uint64_t mine = 0;
     int mine_at = lane;
@@ -201,9 +217,7 @@ __device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, do
     }
     double my_p[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        my_p[h] = my_id[h] < 0 ? 0.0
-                               : prob_wide(load_logit<DT>(p.logits, base + my_id[h]), soft, mx, sum);
+    for (int h = 0; h < 2; ++h) my_p[h] = my_id[h] < 0 ? 0.0 : prob[my_id[h]];
     double f = c.routed_scaling_factor;
     if (c.norm_topk_prob) {
         const double total = warp_sum(my_p[0] + my_p[1]);
@@ -271,6 +285,61 @@ __device__ __noinline__ void route_row_close(const Args &q, int row, int lane, i
     }
 }
 
+// The largest of the lanes' keys and the first lane that has it.
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t v, int *who) {
+    const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(v >> 32));
+    const bool top = (uint32_t)(v >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(~0u, top ? (uint32_t)v : 0u);
+    *who = __ffs(__ballot_sync(~0u, top && (uint32_t)v == lo)) - 1;
+    return (uint64_t)hi << 32 | lo;
+}
+
+// Sigmoid scores: which of the `contested` groups (bits) come in beside the
+// `sure` ones, in 64 bits.  s: the biased fp32 scores; `from` in lane g: the
+// least fp32 value that may be among those that make group g's score.
+// 0 where there are more candidates than lanes.
+template <int VPT, int DT>
+__device__ __noinline__ uint32_t settle_groups(const Args &q, int row, int lane, const float *s,
+                                               uint32_t contested, uint32_t sure, float from) {
+    const RouteParams &p = q.p;
+    const int E = p.c.num_experts;
+    int id = -1, n = 0;
+    for (int j = 0; j < VPT; ++j) {
+        const int e = j * 32 + lane, g = min((int)((uint32_t)e * q.div >> 20), 31);
+        const float low = __shfl_sync(~0u, from, g);
+        const bool may = e < E && (contested >> g & 1) && s[e] >= low;
+        for (uint32_t m = __ballot_sync(~0u, may); m; m &= m - 1, ++n)
+            if (lane == n) id = j * 32 + __ffs(m) - 1;
+    }
+    if (n > 32) return 0;
+    double v = 0.0;
+    if (id >= 0) {
+        v = prob_wide(load_logit<DT>(p.logits, (int64_t)row * p.stride + id), false, 0.0, 1.0);
+        if (p.bias) v += (double)__ldg(p.bias + id);
+    }
+    const int group = id >= 0 ? (int)((uint32_t)id * q.div >> 20) : -1;
+    uint64_t score = 0;
+    for (uint32_t m = contested; m; m &= m - 1) {
+        const int g = __ffs(m) - 1;
+        uint64_t key = group == g ? order_key(v) : 0;
+        int who;
+        warp_max_key(key, &who);
+        double total = __shfl_sync(~0u, v, who);
+        if (lane == who) key = 0;
+        if (p.c.group_score == MOEOP_GROUP_TOP2 && warp_max_key(key, &who))
+            total += __shfl_sync(~0u, v, who);
+        if (lane == g) score = order_key(total);
+    }
+    int rank = 0;
+    for (uint32_t m = contested; m; m &= m - 1) {
+        const int g = __ffs(m) - 1;
+        const uint64_t o = __shfl_sync(~0u, score, g);
+        rank += o > score || (o == score && g < lane);
+    }
+    return sure | __ballot_sync(~0u, (contested >> lane & 1) &&
+                                         rank < p.c.group_limit - __popc(sure));
+}
+
 __device__ __forceinline__ float prob_of(float l, bool soft, float mx, float inv) {
     if (is_dead(l)) return 0.f;
     return soft ? expf(l - mx) * inv : __fdividef(1.f, 1.f + expf(-l));
@@ -288,15 +357,10 @@ __device__ __forceinline__ uint32_t local_best(const uint32_t (&ord)[VPT], int *
     return best;
 }
 
-// VPT: experts per lane.  A round of the selection is one maximum over the
-// lanes' best keys; only the lane that held it looks through its keys again.
+// VPT: experts per lane.  The result: true where the row has to be decided in 64 bits by the block.
 template <int VPT, int DT>
-__global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
-    __shared__ double sm_all[kWarps][VPT * 32];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int row = blockIdx.x * kWarps + warp;
+__device__ __forceinline__ bool route_row(const Args &q, int row, int lane, float *sm) {
     const RouteParams &p = q.p;
-    if (row >= p.rows) return;
     const moeop_route_config &c = p.c;
     const int E = c.num_experts, k = c.top_k;
     const int64_t base = (int64_t)row * p.stride;
@@ -324,7 +388,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
     bool wide = false;
     uint32_t in = ~0u;
     if (p.bias || c.groups > 1) {
-        float *sm = reinterpret_cast<float *>(sm_all[warp]);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int e = j * 32 + lane;
@@ -336,7 +399,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
         }
         if (c.groups > 1) {
             __syncwarp();
-            const float s = group_scores<float>(sm, q, lane);
+            float least;
+            const float s = group_scores<float>(sm, q, lane, &least);
             in = take_groups<float>(s, q, lane);
             // the last group taken against the first left out; where nothing
             // is left in either there is nothing to decide
@@ -344,7 +408,19 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
             const float worst = -warp_max(taken ? -s : -INFINITY);
             const float best = warp_max(!taken && some ? s : -INFINITY);
             const float mag = warp_max(some ? fabsf(s) : 0.f);
-            wide |= worst - best <= 4.f * perr + 6.f * kUlp * mag;
+            const float near = 4.f * perr + 6.f * kUlp * mag;
+            if (worst - best <= near) {
+                uint32_t settled = 0;
+                if (!soft)
+                    settled = settle_groups<VPT, DT>(
+                        q, row, lane, sm,
+                        __ballot_sync(~0u, some && s >= worst - near && s <= best + near),
+                        __ballot_sync(~0u, some && s > best + near),
+                        least - 2.f * perr - 4.f * kUlp * fabsf(least));
+                wide = settled == 0;
+                if (!wide) in = settled;
+            }
+            __syncwarp();
         }
     }
     uint32_t ord[VPT];
@@ -354,12 +430,89 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
         const bool out = !(key[j] > -INFINITY) || !(in >> (e * q.div >> 20) & 1);
         ord[j] = out ? 0u : order_key(key[j]);
     }
-    int my_id[2] = {-1, -1};
-    float before = 0.f, last = 0.f;
-    bool close = false;
-    // one round more than top_k with a bias: the last one taken against the
-    // first left out.  Without a bias the keys are the logits and exact.
+    // At most 32 wanted: the k-th largest of the lanes' best keys bounds the
+    // k-th largest of all from below; the keys from it on (hardly more than
+    // k) go to a list, one to a lane, and are ranked against each other.  One
+    // more than top_k with a bias: the last one taken against the first left
+    // out.  Without a bias the keys are the logits and exact.
     const int rounds = p.bias ? k + 1 : k;
+    uint2 *list = reinterpret_cast<uint2 *>(sm);
+    auto collect = [&](uint32_t from) {  // keys >= from, at most 32; their number
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const bool has = ord[j] >= from;
+            const uint32_t m = __ballot_sync(~0u, has);
+            const int at = n + __popc(m & ((1u << lane) - 1));
+            if (has && at < 32) list[at] = make_uint2(ord[j], j * 32 + lane);
+            n += __popc(m);
+        }
+        __syncwarp();
+        return n;
+    };
+    if (rounds <= 32 && !wide) {
+        uint32_t cur = ord[0], from = 1;
+#pragma unroll
+        for (int j = 1; j < VPT; ++j) cur = max(cur, ord[j]);
+        int s = 0;
+        for (; s < rounds; ++s) {
+            const uint32_t best = __reduce_max_sync(~0u, cur);
+            if (best == 0) break;
+            from = best;
+            if (cur == best) cur = 0;
+        }
+        const int n = collect(s < rounds ? 1u : from);
+        if (n <= 32) {
+            uint2 mine = make_uint2(0, 0);
+            if (lane < n) mine = list[lane];
+            int rank = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint2 o = list[i];
+                rank += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+            }
+            const bool in_k = lane < n && rank < k;
+            if (p.bias) {
+                __syncwarp();
+                if (lane < n) list[rank].x = mine.x;
+                __syncwarp();
+                const float v = order_value(mine.x);
+                const bool next = in_k && rank + 1 < n;
+                if (__any_sync(~0u, next && v - order_value(list[next ? rank + 1 : 0].x) <=
+                                                2.f * perr + 4.f * kUlp * fabsf(v))) {
+                    // every expert that may belong to the top k: those taken,
+                    // and those whose keys are as near to the last taken
+                    const float last = order_value(list[min(n, k) - 1].x);
+                    __syncwarp();
+                    const int m = collect(order_key(last - 2.f * perr - 4.f * kUlp * fabsf(last)));
+                    if (m > 32) return true;
+                    route_row_close<DT>(q, row, lane, lane < m ? (int)list[lane].y : -1, m);
+                    return false;
+                }
+            }
+            const float prob =
+                in_k ? prob_of(load_logit<DT>(p.logits, base + mine.y), soft, mx, inv) : 0.f;
+            float f = c.routed_scaling_factor;
+            if (c.norm_topk_prob) {
+                const float total = warp_sum(prob);
+                // under 2^-60 of the row's unit the p that fp32 holds are too small
+                if (n && !(total > 8.7e-19f)) return true;
+                f = n ? __fdividef(f, total) : 0.f;
+            }
+            if (in_k) {
+                p.ids[(size_t)row * k + rank] = (int)mine.y;
+                p.wts[(size_t)row * k + rank] = prob * f;
+            }
+            if (lane >= n && lane < k) {  // no expert is left for these slots
+                p.ids[(size_t)row * k + lane] = -1;
+                p.wts[(size_t)row * k + lane] = 0.f;
+            }
+            return false;
+        }
+    }
+    // More than 32 wanted, or too many equal keys: one by one.
+    int my_id[2] = {-1, -1};
+    float before = 0.f;
+    bool close = false;
     int mine_at;
     uint32_t mine = local_best<VPT>(ord, &mine_at);
     for (int s = 0; s < rounds; ++s) {
@@ -370,7 +523,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
             if (s) close |= before - v <= 2.f * perr + 4.f * kUlp * fabsf(before);
             before = v;
             if (s == k) break;
-            last = v;
         }
         uint32_t who = __ballot_sync(~0u, mine == best);
         if (who & (who - 1))  // equal keys in several lanes: the lowest expert
@@ -400,43 +552,38 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const Args q) {
         wide |= __any_sync(~0u, my_id[0] >= 0) && !(total > 8.7e-19f);
         f = total > 0.f ? __fdividef(f, total) : 0.f;
     }
-    if (close && !wide) {
-        // every expert that may belong to the top k: those taken, and those
-        // left whose keys are as near to the last taken
-        const float from = last - 2.f * perr - 4.f * kUlp * fabsf(last);
-        int id = my_id[0], n = min(k, 32);
-        wide = k > 31;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const uint32_t more = __ballot_sync(~0u, ord[j] && order_value(ord[j]) >= from);
-            for (uint32_t m = more; m; m &= m - 1, ++n)
-                if (lane == n) id = j * 32 + __ffs(m) - 1;
-        }
-        wide |= n > 32;
-        if (!wide) {
-            route_row_close<DT>(q, row, lane, id, n);
-            return;
-        }
-    }
-    if (wide) {
-        route_row_wide<DT>(q, row, lane, sm_all[warp]);
-        return;
-    }
+    if (wide || close) return true;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         if (lane + 32 * h < k) {
             p.ids[(size_t)row * k + lane + 32 * h] = my_id[h];
             p.wts[(size_t)row * k + lane + 32 * h] = my_p[h] * f;
         }
+    return false;
+}
+
+template <int VPT, int DT>
+__global__ void __launch_bounds__(warps_of(VPT) * 32) route_topk_kernel(const Args q) {
+    constexpr int kWarps = warps_of(VPT);
+    __shared__ float sm[kWarps][VPT * 32];
+    __shared__ double key[VPT * 32], prob[VPT * 32], sums[kWarps];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int row = blockIdx.x * kWarps + warp;
+    const bool wide = row < q.p.rows && route_row<VPT, DT>(q, row, lane, sm[warp]);
+    if (!__syncthreads_or(wide)) return;
+    // by every warp in turn, so that all threads know whose row it is
+    for (int w = 0; w < kWarps; ++w)
+        if (__syncthreads_or(wide && warp == w))
+            route_row_wide<DT>(q, blockIdx.x * kWarps + w, lane, warp, w, key, prob, sums);
 }
 
 template <int DT>
 cudaError_t launch_typed(const Args &q, cudaStream_t st) {
-    const int grid = (q.p.rows + kWarps - 1) / kWarps, E = q.p.c.num_experts;
-    if (E <= 128) route_topk_kernel<4, DT><<<grid, kWarps * 32, 0, st>>>(q);
-    else if (E <= 256) route_topk_kernel<8, DT><<<grid, kWarps * 32, 0, st>>>(q);
-    else if (E <= 512) route_topk_kernel<16, DT><<<grid, kWarps * 32, 0, st>>>(q);
-    else route_topk_kernel<32, DT><<<grid, kWarps * 32, 0, st>>>(q);
+    const int E = q.p.c.num_experts, w = E <= 512 ? 8 : 4, grid = (q.p.rows + w - 1) / w;
+    if (E <= 128) route_topk_kernel<4, DT><<<grid, w * 32, 0, st>>>(q);
+    else if (E <= 256) route_topk_kernel<8, DT><<<grid, w * 32, 0, st>>>(q);
+    else if (E <= 512) route_topk_kernel<16, DT><<<grid, w * 32, 0, st>>>(q);
+    else route_topk_kernel<32, DT><<<grid, w * 32, 0, st>>>(q);
     return cudaGetLastError();
 }
 

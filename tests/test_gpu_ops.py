@@ -169,6 +169,23 @@ def test_route_pairs_of_keys_a_step_apart(scoring, top_k):
     check_route(logits, top_k, scoring=scoring, bias=b, norm_topk_prob=False)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("score", ["max", "top2"])
+@pytest.mark.parametrize("groups,limit", [(4, 1), (8, 3), (12, 11)])
+def test_route_groups_a_step_apart(scoring, score, groups, limit):
+    """Groups whose scores differ by about an fp32 step or not at all, with one
+    to all of their experts behind the score."""
+    size = 96 // groups
+    one = randn(40, size, std=1.0)
+    logits = one.repeat(1, groups) + randn(40, 96, seed=1) * 1e-7
+    logits[10:20] = one[10:20].repeat(1, groups)
+    logits[20:30] = randn(10, 96, seed=2) * 1e-7
+    logits[30, size:] = -math.inf
+    for bias in (None, randn(size, seed=3, std=0.1).repeat(groups)):
+        check_route(logits, min(5, limit * size), scoring=scoring, bias=bias, groups=groups,
+                    group_limit=limit, group_score=score)
+
+
 @pytest.mark.parametrize("scoring,bias", [("softmax", False), ("softmax", True),
                                           ("sigmoid", False), ("sigmoid", True)])
 @pytest.mark.parametrize("groups,limit", [(1, 1), (8, 2)])
