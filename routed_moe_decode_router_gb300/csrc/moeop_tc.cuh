@@ -69,12 +69,12 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const TensorMap *m, int x,
         : "memory");
 }
 // Four rows of a map whose box is one row high.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const TensorMap *m, int x, int4 rows,
-                                            uint64_t *bar) {
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const TensorMap *m, int x,
+                                            const int (&rows)[4], uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(m), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar))
+        "l"(m), "r"(x), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]), "r"(rows[3]), "r"(smem_u32(bar))
         : "memory");
 }
 
