@@ -68,7 +68,7 @@ def _binding_commands():
     tmp = BINDING + ".%d.tmp" % os.getpid()
     link_cmd = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:libmoe_router.so",
                 "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"), "-ltorch_python",
-                "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+                "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"]
     return compile_cmd, link_cmd, tmp
 
 

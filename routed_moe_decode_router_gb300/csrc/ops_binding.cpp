@@ -5,7 +5,7 @@
 // marshalling it through Python and ctypes took 25.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -116,8 +116,9 @@ int small(int64_t n, const char *name) {
     if (n > INT32_MAX || n < INT32_MIN) value_error(std::string(name) + " is out of range");
     return (int)n;
 }
+// From PyTorch's caching allocator, without the dispatcher's round trip.
 Tensor fresh(at::IntArrayRef shape, ScalarType type, const at::Device &dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 void *stream_of(PyObject *o, const at::Device &dev) {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
