@@ -47,6 +47,11 @@ struct Fp8Mat {
 cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b, const float *sb,
                               void *out, int out_dtype, cudaStream_t st);
 
+// Rows up to which a product goes to moeop_few.cu, and pairs (row, slot).
+constexpr int kFewRows = 32, kFewPairs = 32;
+cudaError_t launch_few_dense(const Fp8Mat &a, const float *sa, const Fp8Mat &b, const float *sb,
+                             void *out, int out_dtype, int sms, cudaStream_t st);
+
 // Workspace of moeop_experts_fp8: the pairs (row, slot) in expert order, the
 // tiles of 128 of them, the FP8 rows h and the products y.
 struct ExpertsWs {
@@ -70,7 +75,9 @@ struct ExpertsWs {
         const size_t ny = P * c.hidden;
         w.y32 = ny <= kY32;
         w.y = o, o += up(2 * (ny > 2 * kY32 || w.y32 ? (w.y32 ? 2 : 1) * ny : 2 * kY32));
-        w.total = o;
+        // up to 32 pairs: h in fp32 and nothing else
+        const size_t few = up((P < kFewPairs ? P : (size_t)kFewPairs) * c.inter * 4);
+        w.total = o > few ? o : few;
         return w;
     }
 };
@@ -87,6 +94,7 @@ struct ExpertsArgs {
     char *ws;
 };
 cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st);
+cudaError_t launch_few_experts(const ExpertsArgs &a, float *h, cudaStream_t st);
 
 cudaError_t status_word(uint32_t **p);  // the current device's status word
 

@@ -23,6 +23,8 @@
 // to one rank, into whose (by then idle) ring the others write their partial
 // sums, and which adds them in rank order: the result does not depend on
 // timing.
+//
+// Calls of a few rows go to moeop_few.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -67,9 +69,6 @@ struct Params {
     const int *num_tiles;
     const int4 *tiles;        // expert, first position, rows
     const int *pair, *token;
-    int few;                  // pairs of a call without an index, else 0
-    const int32_t *ids;
-    int experts, top_k;
     uint8_t *h;
     float *h_scales;
 };
@@ -78,64 +77,13 @@ struct Tile {
     int e, pos, rows, nt;
 };
 
-// A warp's view of the tiles and of the pairs in their rows.  The experts'
-// lists come from the index kernel; calls of at most 32 pairs do without it:
-// every warp holds all ids, one to a lane, and works the same lists out.
 template <int MODE>
-struct Lists {
-    uint32_t leaders, peers;  // few: the first lanes of an expert; lanes with this lane's
-    int id, start;            // few: this lane's expert; position of its first row
-    int tiles;
-
-    __device__ __forceinline__ Lists(const Params &p, int lane) {
-        leaders = 0;
-        if (MODE == kDense) {
-            tiles = p.tiles_m;
-        } else if (!p.few) {
-            tiles = __ldcg(p.num_tiles);
-        } else {
-            id = lane < p.few ? __ldg(p.ids + lane) : -1;
-            const bool in = (unsigned)id < (unsigned)p.experts;
-            peers = __match_any_sync(~0u, in ? id : -1 - lane);
-            const bool leader = in && __ffs(peers) - 1 == lane;
-            leaders = __ballot_sync(~0u, leader);
-            const int n = leader ? __popc(peers) : 0;
-            start = n;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int v = __shfl_up_sync(~0u, start, o);
-                if (lane >= o) start += v;
-            }
-            start -= n;
-            tiles = __popc(leaders);
-        }
-    }
-    // Of all lanes together.
-    __device__ __forceinline__ Tile at(const Params &p, int t) const {
-        const int mt = t / p.tiles_n, nt = t % p.tiles_n;
-        if (MODE == kDense) return {0, mt * 128, min(128, p.rows - mt * 128), nt};
-        if (p.few) {
-            uint32_t m = leaders;
-            for (int i = 0; i < mt; ++i) m &= m - 1;
-            const int lead = __ffs(m) - 1;
-            return {__shfl_sync(~0u, id, lead), __shfl_sync(~0u, start, lead),
-                    __popc(__shfl_sync(~0u, peers, lead)), nt};
-        }
-        const int4 d = __ldcg(p.tiles + mt);
-        return {d.x, d.y, d.z, nt};
-    }
-    // The pair in row i (valid, any per lane) of tile T.  Of all lanes together.
-    __device__ __forceinline__ int pair(const Params &p, const Tile &T, int i) const {
-        if (!p.few) return __ldcg(p.pair + T.pos + i);
-        const uint32_t mine = __ballot_sync(~0u, id == T.e);
-        uint32_t m = mine;
-        for (int j = 0; j < i; ++j) m &= m - 1;
-        return __ffs(m) - 1;
-    }
-    __device__ __forceinline__ int token(const Params &p, const Tile &T, int i) const {
-        return p.few ? pair(p, T, i) / p.top_k : __ldcg(p.token + T.pos + i);
-    }
-};
+__device__ __forceinline__ Tile tile_at(const Params &p, int t) {
+    const int mt = t / p.tiles_n, nt = t % p.tiles_n;
+    if (MODE == kDense) return {0, mt * 128, min(128, p.rows - mt * 128), nt};
+    const int4 d = __ldcg(p.tiles + mt);
+    return {d.x, d.y, d.z, nt};
+}
 
 // Scales of the A rows; h's were written by the kernel before.
 template <int MODE, typename F>
@@ -232,8 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb0 = SPLIT ? rank * p.kb / split : 0;
     const int kb1 = SPLIT ? (rank + 1) * p.kb / split : p.kb;
     pdl_wait();
-    const Lists<MODE> lists(p, lane);
-    const int total = lists.tiles * p.tiles_n;
+    const int total = (MODE == kDense ? p.tiles_m : __ldcg(p.num_tiles)) * p.tiles_n;
     int syncs = 0;  // of this thread with its cluster: two in every split block
 
     if (warp >= kLoadWarp && warp != kMmaWarp) {
@@ -243,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         bool ok = true;
         for (int t = first; t < total && ok && (MODE == kGateUp || part == 0); t += step) {
-            const Tile T = lists.at(p, t);
+            const Tile T = tile_at<MODE>(p, t);
             const int e = uniform(T.e), pos = uniform(T.pos), rows = uniform(T.rows);
             const int quads = (rows + 3) / 4, boxes = (rows + kBoxRows - 1) / kBoxRows;
             // Gathered: the tokens of rows 4 lane .. + 3, past the end the last
@@ -257,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (MODE == kGateUp) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    mine[j] = lists.token(p, T, min(4 * lane + j, rows - 1));
+                    mine[j] = __ldcg(p.token + pos + min(4 * lane + j, rows - 1));
             }
             if (kHold) {
 #pragma unroll
@@ -344,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int arow = 0, brow = 0;               // where its scales are
         Tile T{};
         auto take = [&](int t) {
-            T = lists.at(p, t);
+            T = tile_at<MODE>(p, t);
             const int row = min(r, T.rows - 1);  // past the end the last one again
-            arow = MODE == kGateUp ? lists.token(p, T, row) : T.pos + row;
+            arow = MODE == kGateUp ? __ldcg(p.token + T.pos + row) : T.pos + row;
             brow = T.e * p.nblocks + T.nt * (MODE == kGateUp ? 1 : NB);
         };
         // The scales of input blocks b and b + 1: this row's, and those of the
@@ -516,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // exchange them so that a store covers 64 bytes of each of 8
                 // rows (rows apart cost a store one cycle each).
                 const int row = min(r, rows - 1);
-                const int orow = MODE == kDown ? lists.pair(p, done, row) : done.pos + row;
+                const int orow = MODE == kDown ? __ldcg(p.pair + done.pos + row) : done.pos + row;
 #pragma unroll
                 for (int c = 0; c < NB; ++c) {
                     const int col = (done.nt * NB + c) * 128 + wg * kCols;
@@ -864,6 +811,7 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
     Dev *d;
     cudaError_t e = device(&d);
     if (e != cudaSuccess) return e;
+    if (a.rows <= kFewRows) return launch_few_dense(a, sa, b, sb, out, out_dtype, d->sms, st);
     Params p{};
     p.rows = (int)a.rows;
     p.n = (int)b.rows;
@@ -898,6 +846,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int H = a.c.hidden, I = a.c.inter, E = a.c.num_experts, k = a.c.top_k;
     const int64_t P = (int64_t)a.rows * k;
+    if (P <= kFewPairs) return launch_few_experts(a, reinterpret_cast<float *>(a.ws), st);
     const ExpertsWs w = ExpertsWs::make(a.c, a.rows);
     int *num_tiles = reinterpret_cast<int *>(a.ws + w.header);
     int4 *tiles = reinterpret_cast<int4 *>(a.ws + w.tiles);
@@ -915,26 +864,19 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
         (e = make_map(&md, {a.w.down, (int64_t)E * H, I, I}, 128)) != cudaSuccess)
         return e;
 
-    // No index for up to 32 pairs; one block up to 4096, else a cluster of 8.
-    const bool few = P <= 32;
-    if (!few) {
-        const IndexParams ip{a.ids, (int)P, k, E, num_tiles, pair, token, tiles};
-        const int ranks = P <= 4096 ? 1 : 8;
-        Launch l(ranks, ranks, 1024, 0, false, st);
-        e = ranks == 1 ? cudaLaunchKernelEx(&l.cfg, index_kernel<1>, ip)
-                       : cudaLaunchKernelEx(&l.cfg, index_kernel<8>, ip);
-        if (e != cudaSuccess) return e;
-    }
+    // one block up to 4096 pairs, else a cluster of 8
+    const IndexParams ip{a.ids, (int)P, k, E, num_tiles, pair, token, tiles};
+    const int ranks = P <= 4096 ? 1 : 8;
+    Launch li(ranks, ranks, 1024, 0, false, st);
+    e = ranks == 1 ? cudaLaunchKernelEx(&li.cfg, index_kernel<1>, ip)
+                   : cudaLaunchKernelEx(&li.cfg, index_kernel<8>, ip);
+    if (e != cudaSuccess) return e;
 
     Params p{};
     p.num_tiles = num_tiles;
     p.tiles = tiles;
     p.pair = pair;
     p.token = token;
-    p.few = few ? (int)P : 0;
-    p.ids = a.ids;
-    p.experts = E;
-    p.top_k = k;
     p.h = h;
     p.h_scales = h_scales;
     p.sa = a.scales;
@@ -947,7 +889,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     int64_t most = (int64_t)w.max_tiles * p.tiles_n;
     p.split = split_of(*d, most, p.kb);
     int64_t grid = p.split > 1 ? most * p.split : most < d->sms ? most : d->sms;
-    if ((e = launch<kGateUp, 2>(mq, mg, mu, p, grid, !few, st)) != cudaSuccess) return e;
+    if ((e = launch<kGateUp, 2>(mq, mg, mu, p, grid, true, st)) != cudaSuccess) return e;
 
     p.sa = h_scales;
     p.sb = p.sb2 = a.w.down_scales;

@@ -236,7 +236,9 @@ def check_product(a, sa, b, sb, got):
 @pytest.mark.parametrize("m,n,k", [
     (1, 1, 16), (1, 128, 128), (128, 128, 128), (128, 256, 256), (5, 100, 144), (1, 4096, 4096),
     (33, 1000, 2048), (129, 257, 272), (200, 384, 1040), (64, 640, 8192), (127, 129, 128),
-    (1000, 2000, 512), (300, 5000, 1152)])
+    (1000, 2000, 512), (300, 5000, 1152),
+    (8, 1000, 1040), (9, 24, 4096), (16, 4096, 272), (17, 333, 2048), (32, 2048, 7168), (2, 40, 16),
+    (31, 17, 16384)])
 def test_matmul_sizes(m, n, k):
     a, sa, b, sb = operands(m, n, k)
     for t in (torch.float32, torch.bfloat16, torch.float16):
@@ -327,7 +329,8 @@ def check_experts(x, ids, wts, lay, **kw):
     (1, 1, 1, 128, 128), (1, 16, 4, 256, 128), (3, 8, 8, 384, 256), (7, 16, 2, 2048, 768),
     (40, 3, 2, 256, 384), (130, 4, 4, 512, 128), (300, 1, 1, 640, 256), (257, 37, 6, 384, 640),
     (64, 64, 8, 1024, 256), (1000, 16, 4, 256, 256), (2, 1024, 64, 128, 128), (4, 40, 8, 512, 384),
-    (33, 5, 1, 256, 256)])
+    (33, 5, 1, 256, 256), (32, 1, 1, 512, 256), (8, 64, 4, 4096, 1536), (16, 2, 2, 256, 2048),
+    (1, 64, 32, 256, 128), (4, 1000, 8, 128, 4096)])
 def test_experts_sizes(t, e, k, h, i):
     ids, wts = choice(t, k, e)
     check_experts(randn(t, h, seed=9), ids, wts, layer(e, h, i))
@@ -370,6 +373,18 @@ def test_experts_repeated_ids_and_one_expert_for_all():
     lay = layer(4, 256, 128)
     ids = torch.full((150, 3), 2, dtype=torch.int32, device="cuda")
     check_experts(randn(150, 256, seed=9), ids, randn(150, 3).abs(), lay)
+
+
+@pytest.mark.parametrize("t,k", [(1, 1), (4, 8), (10, 3), (32, 1), (40, 2)])
+def test_experts_few_pairs_dropped_and_repeated(t, k):
+    lay = layer(5, 384, 256)
+    g = torch.Generator(device="cuda").manual_seed(t)
+    ids = torch.randint(-2, 7, (t, k), generator=g, device="cuda").to(torch.int32)
+    ids[t // 2] = 3
+    add = randn(t, 384, seed=12).to(torch.bfloat16)
+    check_experts(randn(t, 384, seed=9), ids, randn(t, k, seed=10), lay, addend=add)
+    got = check_experts(randn(t, 384, seed=9), torch.full_like(ids, 5), randn(t, k), lay)
+    assert not got.any()
 
 
 def test_experts_addend_output_and_workspace():
