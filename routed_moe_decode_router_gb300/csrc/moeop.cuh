@@ -48,7 +48,7 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
                               void *out, int out_dtype, cudaStream_t st);
 
 // Rows up to which a product goes to moeop_few.cu, and pairs (row, slot).
-constexpr int kFewRows = 32, kFewPairs = 32;
+constexpr int kFewRows = 16, kFewPairs = 32, kFewSmem = 160 << 10;
 cudaError_t launch_few_dense(const Fp8Mat &a, const float *sa, const Fp8Mat &b, const float *sb,
                              void *out, int out_dtype, int sms, cudaStream_t st);
 
@@ -95,6 +95,8 @@ struct ExpertsArgs {
 };
 cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st);
 cudaError_t launch_few_experts(const ExpertsArgs &a, float *h, cudaStream_t st);
+bool few_experts(int64_t rows, const moeop_experts_config &c);
+cudaError_t allow_few_smem();
 
 cudaError_t status_word(uint32_t **p);  // the current device's status word
 

@@ -1,4 +1,4 @@
-// moeop_few.cu -- the FP8 products for a few rows: moeop_matmul_fp8 up to 32
+// moeop_few.cu -- the FP8 products for a few rows: moeop_matmul_fp8 up to 16
 // rows, and moeop_experts_fp8 up to 32 pairs (row, slot).
 //
 // Few rows leave nothing to compute: the weights' bytes are the bound, and
@@ -53,7 +53,7 @@ struct DenseParams {
 
 // NT: groups of 8 rows of A.  A step is UNROLL blocks of 128 inputs.
 template <int NT>
-__global__ void __launch_bounds__(512) few_dense_kernel(const DenseParams p) {
+__global__ void __launch_bounds__(512, 1) few_dense_kernel(const DenseParams p) {
     constexpr int kUnroll = NT == 1 ? 2 : 1;
     __shared__ float part[16][NT][128];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -160,12 +160,11 @@ struct Groups {
         const int first = __ffs(__ballot_sync(~0u, n > 0 && start <= i && i < start + n)) - 1;
         const int e = __shfl_sync(~0u, id, first);
         const int from = (i - __shfl_sync(~0u, start, first)) * 8;
-        *pair = -1;
+        uint32_t m = __ballot_sync(~0u, id == e && rank >= from && rank < from + 8);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int who = __ffs(__ballot_sync(~0u, id == e && rank == from + c)) - 1;
-            if (lane / 4 == c) *pair = who;
-        }
+        for (int c = 0; c < 7; ++c)
+            if (c < lane / 4) m &= m - 1;
+        *pair = __ffs(m) - 1;
         return e;
     }
 };
@@ -181,14 +180,15 @@ struct ExpertsParams {
     int rows, pairs, top_k, experts, hidden, inter;
 };
 
-// Block (group, 8 columns of h): rows 0-7 of the MMA are gate's, 8-15 up's,
-// so that a lane holds the gate and the up value of the same column and pair.
-__global__ void __launch_bounds__(256) few_gate_up_kernel(const ExpertsParams p) {
+// Block: a group and 8 columns of h.  Rows 0-7 of the MMA are gate's, 8-15
+// up's, so that a lane holds the gate and the up value of the same column and
+// pair.
+__global__ void __launch_bounds__(256, 3) few_gate_up_kernel(const ExpertsParams p) {
     __shared__ float part[8][128];
     pdl_trigger();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int g = lane / 4, t = lane % 4;
-    const int per = p.inter / 8, group = blockIdx.x / per, c0 = (blockIdx.x % per) * 8;
+    const int cols = p.inter / 8, group = blockIdx.x / cols, c = blockIdx.x % cols;
     const Groups groups(p.ids, p.pairs, p.experts, lane);
     if (group >= groups.total) return;
     int pair;
@@ -196,11 +196,11 @@ __global__ void __launch_bounds__(256) few_gate_up_kernel(const ExpertsParams p)
     const int token = pair < 0 ? -1 : pair / p.top_k;
     const int tc[2] = {__shfl_sync(~0u, token, 8 * t), __shfl_sync(~0u, token, 8 * t + 4)};
     const int kb = p.hidden / 128;
-    const size_t row = ((size_t)e * p.inter + c0 + g) * p.hidden + t * 16;
-    const size_t sat = ((size_t)e * (p.inter / 128) + c0 / 128) * kb;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const int b1 = (warp + 1) * kb / warps;
-    constexpr int kUnroll = 4;
+    const size_t row = ((size_t)e * p.inter + c * 8 + g) * p.hidden + t * 16;
+    const size_t sat = ((size_t)e * (p.inter / 128) + c / 16) * kb;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kUnroll = 2;
     for (int b0 = warp * kb / warps; b0 < b1; b0 += kUnroll) {
         uint4 w[kUnroll][2][2], x[kUnroll][2];
         float sw[kUnroll][2], sx[kUnroll][2];
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(256) few_gate_up_kernel(const ExpertsParams p)
             sw[u][0] = in ? __ldg(p.gate_scales + sat + b) : 0.f;
             sw[u][1] = in ? __ldg(p.up_scales + sat + b) : 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                sx[u][c] = in && tc[c] >= 0 ? __ldg(p.scales + (size_t)tc[c] * kb + b) : 0.f;
+            for (int i = 0; i < 2; ++i)
+                sx[u][i] = in && tc[i] >= 0 ? __ldg(p.scales + (size_t)tc[i] * kb + b) : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -230,52 +230,68 @@ __global__ void __launch_bounds__(256) few_gate_up_kernel(const ExpertsParams p)
 #pragma unroll
             for (int h = 0; h < 2; ++h) mma64(d, w[u][0][h], w[u][1][h], x[u][h]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], sx[u][i % 2] * sw[u][i / 2], acc[i]);
+            for (int i = 0; i < 4; ++i)
+                acc[i] = fmaf(d[i], sx[u][i % 2] * sw[u][i / 2], acc[i]);
         }
     }
     // part[..][gate, up][pair of the group][column]
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[warp][i / 2 * 64 + (t * 2 + i % 2) * 8 + g] = acc[i];
     __syncthreads();
-    if (warp < 2 || (warps == 1)) {
+    if (warp < 2)
         for (int i = threadIdx.x; i < 64; i += 32 * min(warps, 2)) {
             const int to = __shfl_sync(~0u, pair, i / 8 * 4);
             float gv = 0.f, uv = 0.f;
             for (int q = 0; q < warps; ++q) gv += part[q][i], uv += part[q][64 + i];
             if (to >= 0)
-                p.h[(size_t)to * p.inter + c0 + i % 8] =
+                p.h[(size_t)to * p.inter + c * 8 + i % 8] =
                     __fdividef(gv, 1.f + __expf(-gv)) * uv;
         }
-    }
 }
 
 // Block: 16 columns of the output, for every pair, and their weighted sums.
-// A unit of work is a group and a share of its inputs; h becomes e4m3 codes
-// on the way in.  The first unit's weights do not depend on h and are on
-// their way before it is there.
+// First h becomes e4m3 codes and scales in shared memory; then a unit of work
+// is a group and a share of its inputs.  The first unit's weights do not
+// depend on h and are on their way before it is there.
 constexpr int kDownWarps = 16;
+// Row of codes: 64 bytes past a multiple of 128, so that the rows of two
+// columns lie in different banks.
+__host__ __device__ __forceinline__ int code_row(int inter) { return inter + 64; }
+__host__ __device__ __forceinline__ size_t few_down_smem(int pairs, int inter) {
+    return (size_t)pairs * (code_row(inter) + inter / 128 * 4);
+}
 
-__global__ void __launch_bounds__(kDownWarps * 32) few_down_kernel(const ExpertsParams p) {
-    __shared__ float part[32][128], y[32][16];
+__global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const ExpertsParams p) {
+    extern __shared__ uint4 smem[];
+    __shared__ float part[32][128], y[32][16], wts[32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int g = lane / 4, t = lane % 4, n0 = blockIdx.x * 16;
+    const int kb = p.inter / 128, pitch = code_row(p.inter);
+    uint8_t *codes = reinterpret_cast<uint8_t *>(smem);
+    float *scales = reinterpret_cast<float *>(codes + (size_t)p.pairs * pitch);
     const Groups groups(p.ids, p.pairs, p.experts, lane);
-    const int kb = p.inter / 128;
+    // a weight of an id that is no expert: not used
+    if (warp == 0) wts[lane] = lane < p.pairs ? __ldg(p.wts + lane) : 0.f;
+    const uint32_t real = __ballot_sync(~0u, (unsigned)groups.id < (unsigned)p.experts);
     // shares: enough to give every warp a unit; at most 31 units, or the groups
     const int shares = groups.total ? min(kb, (kDownWarps + groups.total - 1) / groups.total) : 1;
     const int units = groups.total * shares;
     bool first = true;
-    for (int u = warp; u < units; u += kDownWarps) {
-        int pair;
-        const int e = groups.at(u / shares, lane, &pair);
-        const int share = u % shares, b1 = (share + 1) * kb / shares;
+    for (int u = warp; u < units || first; u += kDownWarps) {
+        const bool work = u < units;
+        int pair = -1, e = 0, b0 = 0, b1 = 0;
+        if (work) {
+            e = groups.at(u / shares, lane, &pair);
+            b0 = u % shares * kb / shares, b1 = (u % shares + 1) * kb / shares;
+        }
         const uint8_t *lo = p.down + ((size_t)e * p.hidden + n0 + g) * p.inter + t * 16;
         const uint8_t *hi = lo + (size_t)8 * p.inter;
         const float *sb = p.down_scales + ((size_t)e * (p.hidden / 128) + n0 / 128) * kb;
-        const float *h = p.h + (size_t)max(pair, 0) * p.inter + t * 16;
+        const int row = max(pair, 0);
+        const int p0 = __shfl_sync(~0u, row, 8 * t), p1 = __shfl_sync(~0u, row, 8 * t + 4);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         constexpr int kUnroll = 4;
-        for (int b0 = share * kb / shares; b0 < b1; b0 += kUnroll) {
+        do {
             uint4 w[kUnroll][2][2];
             float s[kUnroll];
 #pragma unroll
@@ -289,43 +305,59 @@ __global__ void __launch_bounds__(kDownWarps * 32) few_down_kernel(const Experts
                 }
                 s[i] = in ? __ldg(sb + b0 + i) : 0.f;
             }
-            if (first) pdl_wait();
-            first = false;
+            if (first) {
+                first = false;
+                pdl_wait();
+                // eight lanes to a block of 128 inputs
+                for (int i0 = warp * 4; i0 < p.pairs * kb; i0 += 4 * kDownWarps) {
+                    // (rows without an expert are read and not used)
+                    const int i = min(i0 + lane / 8, p.pairs * kb - 1), r = i / kb, b = i % kb;
+                    const int at = b * 128 + lane % 8 * 16;
+                    float4 v[4];
+                    float amax = kFp8Tiny;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = __ldcg(reinterpret_cast<const float4 *>(
+                            p.h + (size_t)r * p.inter + at + j * 4));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)),
+                                                 fmaxf(fabsf(v[j].z), fabsf(v[j].w))));
+#pragma unroll
+                    for (int o = 4; o; o >>= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+                    const float up = kFp8Max / amax;
+                    uint32_t q[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        q[j] = pack_e4m3x4(v[j].x * up, v[j].y * up, v[j].z * up, v[j].w * up);
+                    *reinterpret_cast<uint4 *>(codes + r * pitch + at) =
+                        make_uint4(q[0], q[1], q[2], q[3]);
+                    if (lane % 8 == 0) scales[r * kb + b] = amax / kFp8Max;
+                }
+                __syncthreads();
+            }
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 if (b0 + i >= b1) break;
-                // this lane's 32 of the 128 inputs
-                float4 v[8];
-                float amax = 0.f;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    v[c] = pair >= 0 ? __ldcg(reinterpret_cast<const float4 *>(
-                                           h + (size_t)(b0 + i) * 128 + c / 4 * 64 + c % 4 * 4))
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[c].x), fabsf(v[c].y)),
-                                             fmaxf(fabsf(v[c].z), fabsf(v[c].w))));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-                amax = fmaxf(fmaxf(amax, __shfl_xor_sync(~0u, amax, 2)), kFp8Tiny);
-                const float up = kFp8Max / amax;
-                uint32_t q[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    q[c] = pack_e4m3x4(v[c].x * up, v[c].y * up, v[c].z * up, v[c].w * up);
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma64(d, w[i][0][0], w[i][1][0], make_uint4(q[0], q[1], q[2], q[3]));
-                mma64(d, w[i][0][1], w[i][1][1], make_uint4(q[4], q[5], q[6], q[7]));
-                const float mine = amax / kFp8Max;
-                const float s0 = __shfl_sync(~0u, mine, 8 * t) * s[i];
-                const float s1 = __shfl_sync(~0u, mine, 8 * t + 4) * s[i];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    mma64(d, w[i][0][c], w[i][1][c],
+                          *reinterpret_cast<const uint4 *>(codes + row * pitch +
+                                                           (b0 + i) * 128 + c * 64 + t * 16));
+                const float s0 = scales[p0 * kb + b0 + i] * s[i];
+                const float s1 = scales[p1 * kb + b0 + i] * s[i];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[c] = fmaf(d[c], c % 2 ? s1 : s0, acc[c]);
             }
-        }
+            b0 += kUnroll;
+        } while (b0 < b1);
+        // (columns without a pair hold another's sums: nobody reads them)
+        if (work)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) part[u][(t * 2 + c % 2) * 16 + g + c / 2 * 8] = acc[c];
+            for (int c = 0; c < 4; ++c) part[u][(t * 2 + c % 2) * 16 + g + c / 2 * 8] = acc[c];
     }
-    if (first) pdl_wait();
     __syncthreads();
     for (int i = warp; i < groups.total; i += kDownWarps) {
         int pair;
@@ -345,8 +377,7 @@ __global__ void __launch_bounds__(kDownWarps * 32) few_down_kernel(const Experts
     float v = p.addend ? bf16_lo(p.addend[at]) : 0.f;
     for (int j = 0; j < p.top_k; ++j) {
         const int pair = row * p.top_k + j;
-        if ((unsigned)__ldg(p.ids + pair) < (unsigned)p.experts)
-            v = fmaf(__ldg(p.wts + pair), y[pair][col], v);
+        if (real >> pair & 1) v = fmaf(wts[pair], y[pair][col], v);
     }
     p.out[at] = f2bf16_rn(v);
 }
@@ -364,9 +395,17 @@ cudaError_t launch_few_dense(const Fp8Mat &a, const float *sa, const Fp8Mat &b, 
     while (warps < p.kb && (int64_t)tiles * warps < 8 * sms) ++warps;
     if (warps > 16) warps = 16;
     if (p.m <= 8) few_dense_kernel<1><<<tiles, warps * 32, 0, st>>>(p);
-    else if (p.m <= 16) few_dense_kernel<2><<<tiles, warps * 32, 0, st>>>(p);
-    else few_dense_kernel<4><<<tiles, warps * 32, 0, st>>>(p);
+    else few_dense_kernel<2><<<tiles, warps * 32, 0, st>>>(p);
     return cudaGetLastError();
+}
+
+bool few_experts(int64_t rows, const moeop_experts_config &c) {
+    const int64_t pairs = rows * c.top_k;
+    return pairs <= kFewPairs && few_down_smem((int)pairs, c.inter) <= kFewSmem;
+}
+cudaError_t allow_few_smem() {
+    return cudaFuncSetAttribute(few_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kFewSmem);
 }
 
 cudaError_t launch_few_experts(const ExpertsArgs &a, float *h, cudaStream_t st) {
@@ -384,6 +423,7 @@ cudaError_t launch_few_experts(const ExpertsArgs &a, float *h, cudaStream_t st) 
     cudaLaunchAttribute at[1];
     cfg.gridDim = dim3(a.c.hidden / 16);
     cfg.blockDim = dim3(kDownWarps * 32);
+    cfg.dynamicSmemBytes = few_down_smem(pairs, a.c.inter);
     cfg.stream = st;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

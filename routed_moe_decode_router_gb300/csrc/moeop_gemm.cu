@@ -745,6 +745,7 @@ cudaError_t device(Dev **out) {
             (e = allow_smem<kDown, 1, false>()) != cudaSuccess ||
             (e = allow_smem<kDown, 1, true>()) != cudaSuccess ||
             (e = allow_smem<kDown, 2, false>()) != cudaSuccess ||
+            (e = allow_few_smem()) != cudaSuccess ||
             (e = cudaGetSymbolAddress(&sym, g_status)) != cudaSuccess)
             return e;
         for (int s = 2; s <= kMaxSplit; ++s) {
@@ -846,7 +847,8 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int H = a.c.hidden, I = a.c.inter, E = a.c.num_experts, k = a.c.top_k;
     const int64_t P = (int64_t)a.rows * k;
-    if (P <= kFewPairs) return launch_few_experts(a, reinterpret_cast<float *>(a.ws), st);
+    if (few_experts(a.rows, a.c))
+        return launch_few_experts(a, reinterpret_cast<float *>(a.ws), st);
     const ExpertsWs w = ExpertsWs::make(a.c, a.rows);
     int *num_tiles = reinterpret_cast<int *>(a.ws + w.header);
     int4 *tiles = reinterpret_cast<int4 *>(a.ws + w.tiles);
