@@ -6,7 +6,8 @@
  * conventions: device pointers, the caller's memory and stream, every check
  * on the host before the first launch, moe_status with moe_last_error(), no
  * allocation and no synchronisation (moeop_read_device_status excepted), and
- * capture into CUDA graphs.
+ * capture into CUDA graphs.  The first product on a device looks up what the
+ * library keeps per device: make that call before a capture.
  *
  * FP8 rows [T][K]: e4m3 (bias 7, no infinity) codes, row-major, and fp32
  * scales [T][ceil(K/128)]; value = code * scale of its 128 inputs.
@@ -58,7 +59,7 @@ MOE_API moe_status moeop_rms_norm(const void *x, int64_t x_stride, const void *r
  * wts: p of the chosen (never the bias), divided by their sum with
  * norm_topk_prob, times routed_scaling_factor.
  * A logit of -inf or NaN takes its expert out of the row; it counts for no
- * group.  Slots for which no expert is left get id -1 and weight 0. */
+ * group.  (+inf is no logit: a softmax of it has NaN weights.)  Slots for which no expert is left get id -1 and weight 0. */
 typedef struct moeop_route_config {
     int num_experts;             /* 1..1024 */
     int top_k;                   /* 1..min(64, group_limit * num_experts / groups) */
@@ -88,8 +89,10 @@ MOE_API moe_status moeop_matmul_fp8(const uint8_t *a, int64_t a_stride, const fl
  *   g, u = q . gate[e]^T, q . up[e]^T;  h = silu(g) * u, held as FP8 rows;
  *   out[t] = sum_j wts[t][j] * (h . down[e]^T)  (+ addend[t]), e = ids[t][j]
  * in slot order.  An id outside [0, num_experts) contributes nothing.  The
- * products of the down projection are held in bf16 until they are weighted
- * and added in fp32.  addend (bf16, may be NULL) and out (bf16) are
+ * products of the down projection are held in fp32, those of larger calls
+ * (more than 2^20 of them) in bf16, until they are weighted and added in fp32:
+ * they are the call's largest traffic, and rounding them once is as large an
+ * error as rounding the output.  addend (bf16, may be NULL) and out (bf16) are
  * contiguous; out may be addend.  All weights of a kind are one stack:
  * gate, up [E][inter][hidden], down [E][hidden][inter], each with its scales
  * [E][..][..].  A dense FP8 MLP is the case num_experts = top_k = 1. */

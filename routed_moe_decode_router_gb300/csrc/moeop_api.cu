@@ -79,7 +79,8 @@ moe_status moeop_rms_norm(const void *x, int64_t x_stride, const void *residual,
                           float *scales, void *stream) {
     moe_status s;
     if ((s = check_dtype(dtype, "dtype")) != MOE_OK) return s;
-    if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows=%d: must not be negative", rows);
+    if (rows < 0 || rows > (1 << 30))
+        return fail(MOE_ERR_INVALID_ARG, "rows=%d: must be in [0, 2^30]", rows);
     if (hidden < 1 || hidden > MOEOP_MAX_NORM_HIDDEN)
         return fail(MOE_ERR_INVALID_ARG, "hidden=%d: must be in [1, %d]", hidden,
                     MOEOP_MAX_NORM_HIDDEN);
@@ -150,7 +151,8 @@ moe_status moeop_route_topk(const moeop_route_config *cfg, const void *logits,
     if (c.norm_topk_prob & ~1) return fail(MOE_ERR_INVALID_ARG, "norm_topk_prob must be 0 or 1");
     if (!std::isfinite(c.routed_scaling_factor))
         return fail(MOE_ERR_INVALID_ARG, "routed_scaling_factor is not finite");
-    if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows=%d: must not be negative", rows);
+    if (rows < 0 || rows > (1 << 30))
+        return fail(MOE_ERR_INVALID_ARG, "rows=%d: must be in [0, 2^30]", rows);
     if (rows == 0) return ok();
     if (bad(logits, type_size(c.dtype)) || !aligned(bias, 4) || bad(ids, 4) || bad(wts, 4))
         return fail(MOE_ERR_INVALID_ARG, "a pointer is NULL or not aligned to its type");

@@ -5,7 +5,9 @@ the routed experts, for any number of token rows.
 Like layer.py it only marshals: tensors are checked by their attributes
 before any pointer reaches the library, every step runs in the CUDA library
 on the given (or current) stream, and every call can be captured into a CUDA
-graph.  The checks and the output tensors are made in the extension
+graph (after a first call outside of one, which looks up what the library
+keeps per device).  Outputs made by a call belong to the stream it runs on.
+The checks and the output tensors are made in the extension
 csrc/ops_binding.cpp.  FP8 rows are float8_e4m3fn [T, K] with float32 scales
 [T, ceil(K / 128)]; FP8 weights float8_e4m3fn [N, K] with float32 scales
 [ceil(N / 128), ceil(K / 128)] (experts: one more leading dimension).
@@ -65,9 +67,11 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     strided), with the residual added first if there is one, and the sum
     returned.  quantize: also as FP8 rows; keep=False: only as FP8 rows.
     residual_out: where the sum goes (x or residual itself for in place)."""
-    return NormOut(*(_ext or _load()).rms_norm(
-        x, weight, eps, residual, bool(quantize), bool(keep), residual_out,
-        None if stream is None else stream.cuda_stream))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm(x, weight, eps, residual, quantize, keep, residual_out)
+    return NormOut(*(_ext or _load()).rms_norm(x, weight, eps, residual, bool(quantize),
+                                               bool(keep), residual_out, None))
 
 
 def route_topk(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
@@ -79,6 +83,10 @@ def route_topk(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
     key.  scoring: "softmax" or "sigmoid"; bias [E] float32 is added for the
     selection only; group_score: "max" or "top2".  Experts whose logit is
     -inf or NaN are not taken: id -1, weight 0 where none is left."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_topk(logits, top_k, scoring, bias, groups, group_limit, group_score,
+                              norm_topk_prob, routed_scaling_factor)
     try:
         scoring_code, score_code = _SCORING[scoring], _GROUP_SCORE[group_score]
     except KeyError:
@@ -86,8 +94,7 @@ def route_topk(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                          "not %r and %r" % (scoring, group_score)) from None
     return (_ext or _load()).route_topk(
         logits, top_k, scoring_code, bias, groups, group_limit, score_code,
-        bool(norm_topk_prob), routed_scaling_factor,
-        None if stream is None else stream.cuda_stream)
+        bool(norm_topk_prob), routed_scaling_factor, None)
 
 
 def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -96,11 +103,13 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     """a [M, K] (FP8 rows) times the transpose of b [N, K] (FP8 weights):
     [M, N] in out_dtype (bf16, fp16 or fp32).  K and the row strides of a and
     b are multiples of 16."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return matmul_fp8(a, a_scales, b, b_scales, out_dtype, out)
     code = _DTYPES.get(out_dtype if out is None else out.dtype)
     if code is None:
         raise ValueError("out_dtype is %s, expected bfloat16, float16 or float32" % out_dtype)
-    return (_ext or _load()).matmul_fp8(a, a_scales, b, b_scales, code, out,
-                                        None if stream is None else stream.cuda_stream)
+    return (_ext or _load()).matmul_fp8(a, a_scales, b, b_scales, code, out, None)
 
 
 class ExpertsWorkspace:
@@ -127,14 +136,14 @@ def experts_fp8(q: torch.Tensor, scales: torch.Tensor, ids: torch.Tensor, wts: t
     weighted sum over each row's experts in slot order (+ addend).  gate, up
     [E, I, H] and down [E, H, I] are FP8 weights, ids / wts [T, k] as
     route_topk gives them (ids outside [0, E) contribute nothing).  Without
-    `ws` the scratch comes from PyTorch's allocator for the call, which then
-    has to run on the current stream."""
-    if ws is None and stream is not None and stream != torch.cuda.current_stream():
-        raise ValueError("a call on another stream than the current one needs a workspace")
+    `ws` the scratch comes from PyTorch's allocator for the call."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return experts_fp8(q, scales, ids, wts, gate, gate_scales, up, up_scales, down,
+                               down_scales, ws, addend, out)
     return (_ext or _load()).experts_fp8(
         q, scales, ids, wts, gate, gate_scales, up, up_scales, down, down_scales,
-        None if ws is None else ws.buf, addend, out,
-        None if stream is None else stream.cuda_stream)
+        None if ws is None else ws.buf, addend, out, None)
 
 
 def device_status(stream=None) -> int:

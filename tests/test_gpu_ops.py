@@ -429,8 +429,11 @@ def test_all_on_another_stream_and_in_a_graph():
         n = ops.rms_norm(x, w, residual=r, quantize=True, stream=stream)
         logits = ops.matmul_fp8(n.q, n.scales, *proj, out_dtype=torch.float32, stream=stream)
         ids, wts = ops.route_topk(logits, 2, stream=stream)
-        return ops.experts_fp8(n.q, n.scales, ids, wts, *lay, ws=ws, addend=n.residual,
-                               stream=stream)
+        out = ops.experts_fp8(n.q, n.scales, ids, wts, *lay, ws=ws, addend=n.residual,
+                              stream=stream)
+        if stream is not None:
+            stream.synchronize()
+        return out
     want = path().clone()
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
@@ -438,6 +441,13 @@ def test_all_on_another_stream_and_in_a_graph():
     with torch.cuda.stream(side):
         assert torch.equal(path(), want)
     torch.cuda.synchronize()
+    assert torch.equal(path(stream=side), want)
+    n = ops.rms_norm(x, w, quantize=True, stream=side)
+    ids = torch.zeros(9, 1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    got = ops.experts_fp8(n.q, n.scales, ids, ids.float() + 1, *lay, stream=side)
+    side.synchronize()
+    assert torch.equal(got, ops.experts_fp8(n.q, n.scales, ids, ids.float() + 1, *lay))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = path()
@@ -465,8 +475,7 @@ def test_refusals_with_device_tensors():
             (lambda: ops.rms_norm(sa, sa[0], residual_out=sa), "without residual"),
             (lambda: ops.rms_norm(sa, sa[0], keep=False), "no output"),
             (lambda: ops.experts_fp8(a, sa, ids.long(), wts, *lay), "dtype"),
-            (lambda: ops.experts_fp8(a, sa, ids, wts.t(), *lay), "shape"),
-            (lambda: ops.experts_fp8(a, sa, ids, wts, *lay, stream=torch.cuda.Stream()), "workspace")):
+            (lambda: ops.experts_fp8(a, sa, ids, wts.t(), *lay), "shape")):
         with pytest.raises(ValueError, match=text):
             call()
     from routed_moe_decode_router_gb300 import native as N
@@ -474,3 +483,46 @@ def test_refusals_with_device_tensors():
         ops.route_topk(sa, 3)
     with pytest.raises(N.MoeError, match="needs"):
         ops.experts_fp8(a, sa, ids, wts, *lay, ws=ops.ExpertsWorkspace(1, 2, 256, 128, 8))
+
+
+@pytest.mark.parametrize("rows", [1, 5, 70])
+@pytest.mark.parametrize("scoring,groups,limit", [("softmax", 1, 1), ("sigmoid", 4, 2)])
+def test_layer_of_all_operators(rows, scoring, groups, limit):
+    """The layer's steps against the definitions, each on what the step before
+    it gave, and its output byte for byte."""
+    from routed_moe_decode_router_gb300 import fp8_layer
+    lay = fp8_layer.random_layer(512, 16, 256, 4, seed=3, shared_inter=384, scoring=scoring,
+                                 groups=groups, group_limit=limit, group_score="top2")
+    x, r = randn(rows, 512).to(torch.bfloat16), randn(rows, 512, seed=1).to(torch.bfloat16)
+    out, res = lay.forward(x, r)
+    n = ops.rms_norm(x, lay.norm, residual=r, quantize=True)
+    check_norm(x, lay.norm, n, r)
+    assert torch.equal(res, n.residual)
+    logits = ops.matmul_fp8(n.q, n.scales, *lay.router, out_dtype=torch.float32)
+    check_product(n.q, n.scales, *lay.router, logits)
+    kw = dict(scoring=scoring, bias=lay.bias, groups=groups, group_limit=limit,
+              group_score="top2")
+    check_route(logits[:, :16].contiguous(), 4, **kw)
+    ids, wts = ops.route_topk(logits[:, :16], 4, **kw)
+    gate = torch.sigmoid(logits[:, 16:].double())
+    shared, sb = R.experts(n.q, n.scales, torch.zeros_like(ids[:, :1]), gate, *lay.shared)
+    want, bound = R.experts(n.q, n.scales, ids, wts, *lay.routed)
+    # the shared output is rounded once more on its way; the gate within 8 U
+    total = bound + sb + shared.abs() * (R.half_step(torch.bfloat16) + 8 * R.U)
+    total = total + (want + shared).abs() * R.half_step(torch.bfloat16)
+    within(out, want + shared, total)
+    again, _ = lay.forward(x, r)
+    assert torch.equal(again, out)
+    first, res = lay.forward(x)
+    assert res is x and first.shape == x.shape
+
+
+def test_layer_weights_quantised_by_blocks():
+    from routed_moe_decode_router_gb300 import fp8_layer
+    w = randn(2, 200, 300) * torch.exp(randn(2, 200, 1, seed=1))
+    q = fp8_layer.quantize_weights(w)
+    for i in range(2):
+        c, s = R.weights_fp8(w[i])
+        assert torch.equal(s, q.scales[i])
+        assert (R.wide_weights(q.codes[i], q.scales[i]) - w[i].double()).abs().max() <= \
+            2.0 ** -4 * w[i].abs().max()

@@ -62,7 +62,8 @@ def norm_args(**kw):
 
 
 @pytest.mark.parametrize("kw,text", [
-    (dict(dtype=3), "dtype"), (dict(rows=-1), "rows"), (dict(hidden=0), "hidden"),
+    (dict(dtype=3), "dtype"), (dict(rows=-1), "rows"), (dict(rows=(1 << 30) + 1), "rows"),
+    (dict(hidden=0), "hidden"),
     (dict(hidden=32769, xs=40000), "hidden"), (dict(eps=-1.0), "eps"),
     (dict(eps=float("nan")), "eps"), (dict(y=0), "required"), (dict(q=4 * P), "together"),
     (dict(sc=4 * P), "together"), (dict(x=0), "NULL"), (dict(x=P + 1), "aligned"),
