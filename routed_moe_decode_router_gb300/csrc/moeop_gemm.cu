@@ -336,18 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t acc[kAcc];
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) acc[i] = 0;
-            float s0 = 0.f, s1 = 0.f, n0 = 0.f, n1 = 0.f;
             bool hit = bar_done(&tm_full[it % kBufs], it / kBufs & 1);
             for (int b = kb0; b < kb1; ++b, ++it) {
                 const int buf = it % kBufs;
-                if (((b - kb0) & 1) == 0) {
-                    s0 = a0 * b00, s1 = a0 * b10;
-                    n0 = a1 * b01, n1 = a1 * b11;
-                    fetch(b + 2);
-                } else {
-                    s0 = n0, s1 = n1;
-                }
+                const bool second = (b - kb0) & 1;
+                const float s0 = second ? a1 * b01 : a0 * b00;
+                const float s1 = second ? a1 * b11 : a0 * b10;
                 const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
+                if (second) fetch(b + 1);
                 if (!__all_sync(~0u, hit) && ok)
                     ok = __all_sync(~0u, spin_bar(&tm_full[buf], it / kBufs & 1, &abort_s));
                 tc_fence_after();
