@@ -64,7 +64,7 @@ struct Params {
     bool even;                // pairs of scales start on 8-byte boundaries
     void *out;
     int out_dtype;
-    bool vec_out;             // rows of out start on 16-byte boundaries
+    int out_align;            // 16 or 8 where rows of out start on such boundaries
     // experts
     const int *num_tiles;
     const int4 *tiles;        // expert, first position, rows
@@ -91,11 +91,6 @@ __device__ __forceinline__ F ld_scales(const F *p) {
     return MODE == kDown ? __ldcg(p) : __ldg(p);
 }
 
-__device__ __forceinline__ void store1(void *out, int dtype, size_t at, float v) {
-    if (dtype == MOEOP_FP32) static_cast<float *>(out)[at] = v;
-    else if (dtype == MOEOP_BF16) static_cast<uint16_t *>(out)[at] = f2bf16_rn(v);
-    else static_cast<__half *>(out)[at] = __float2half_rn(v);
-}
 // Two fp32 sums -> two 16-bit outputs.
 __device__ __forceinline__ uint32_t pack16(uint64_t v, int dtype) {
     const float2 f = unpack2(v);
@@ -123,16 +118,58 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
         else u[i + 1] = r;
     }
 }
-// Transposed units to the outputs from `col` on of rows orow of the lanes;
-// `left`: valid rows from this warp's first on.
-__device__ __forceinline__ void store_rows(const uint4 (&u)[4], char *out, int orow, int n, int col,
-                                           int size, int lane, int left) {
+// Transposed units (16 bytes of outputs of SIZE bytes each) to the outputs
+// from `col` on of rows orow of the lanes; `left`: valid rows from this warp's
+// first on.  align: 16 or 8 where all rows start on such boundaries and all
+// columns exist.  Else, all rows in one way (a warp would go all ways): 4-byte
+// words, those of a row that starts on an odd 16-bit output shifted by one,
+// the last output of the lane before in front.
+template <int SIZE>
+__device__ __forceinline__ void store_rows(const uint4 (&u)[4], void *out, int orow, int n, int col,
+                                           int lane, int left, int align) {
+    const int c = col + (lane & 3) * (16 / SIZE), have = n - c;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int src = (lane & ~3) + j;
         const size_t row = __shfl_sync(~0u, orow, src);
-        if (src < left)
-            *reinterpret_cast<uint4 *>(out + (row * n + col) * size + (lane & 3) * 16) = u[j];
+        char *to = static_cast<char *>(out) + (row * n + c) * SIZE;
+        const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+        if (align == 16) {
+            if (src < left) *reinterpret_cast<uint4 *>(to) = u[j];
+            continue;
+        }
+        if (align == 8) {
+            if (src < left) {
+                reinterpret_cast<uint2 *>(to)[0] = make_uint2(w[0], w[1]);
+                reinterpret_cast<uint2 *>(to)[1] = make_uint2(w[2], w[3]);
+            }
+            continue;
+        }
+        if (SIZE == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (src < left && i < have) reinterpret_cast<uint32_t *>(to)[i] = w[i];
+            continue;
+        }
+        const uint32_t before = __shfl_up_sync(~0u, w[3] >> 16, 1, 4);
+        const int odd = reinterpret_cast<uintptr_t>(to) / 2 & 1;
+        to -= odd * 2;
+        int single = odd && (lane & 3) == 3 && have > 7 ? 8 : -1;  // of the word's halves
+        uint32_t value = w[3] >> 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = i ? w[i - 1] >> 16 : before;
+            const uint32_t word = odd ? lo | w[i] << 16 : w[i];
+            // the word's outputs are 2 i - odd and the next
+            const bool first = 2 * i - odd < have && have >= 0 && (i || !odd || (lane & 3));
+            const bool second = 2 * i - odd + 1 < have;
+            if (src < left && first && second) reinterpret_cast<uint32_t *>(to)[i] = word;
+            else if (first) single = 2 * i, value = word & 0xFFFFu;
+            else if (second && !i && src < left)
+                reinterpret_cast<uint16_t *>(to)[1] = (uint16_t)(word >> 16);
+        }
+        if (src < left && single >= 0)
+            reinterpret_cast<uint16_t *>(to)[single] = (uint16_t)value;
     }
 }
 
@@ -463,44 +500,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < NB; ++c) {
                     const int col = (done.nt * NB + c) * 128 + wg * kCols;
-                    const bool whole = p.vec_out && col + kCols <= p.n;
+                    if (col >= p.n) continue;
+                    const int align = MODE == kDown ? 16 : col + kCols <= p.n ? p.out_align : 0;
+                    const int left = rows - (warp % 4) * 32;
+                    uint4 u[4];
+                    if (p.out_dtype != MOEOP_FP32) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t *v = acc + c * 16 + i * 4;
+                            u[i] = make_uint4(pack16(v[0], p.out_dtype), pack16(v[1], p.out_dtype),
+                                              pack16(v[2], p.out_dtype), pack16(v[3], p.out_dtype));
+                        }
+                        transpose4(u, lane);
+                        store_rows<2>(u, p.out, orow, p.n, col, lane, left, align);
+                        continue;
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (p.out_dtype != MOEOP_FP32 && whole) {
-                            if (h) continue;
-                            uint4 u[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint64_t *v = acc + c * 16 + i * 4;
-                                u[i] = make_uint4(pack16(v[0], p.out_dtype), pack16(v[1], p.out_dtype),
-                                                  pack16(v[2], p.out_dtype), pack16(v[3], p.out_dtype));
-                            }
-                            transpose4(u, lane);
-                            store_rows(u, static_cast<char *>(p.out), orow, p.n, col, 2, lane,
-                                       rows - (warp % 4) * 32);
-                        } else if (whole) {
-                            uint4 u[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 x = unpack2(acc[c * 16 + h * 8 + i * 2]);
-                                const float2 y = unpack2(acc[c * 16 + h * 8 + i * 2 + 1]);
-                                u[i] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
-                                                  __float_as_uint(y.x), __float_as_uint(y.y));
-                            }
-                            transpose4(u, lane);
-                            store_rows(u, static_cast<char *>(p.out), orow, p.n, col + h * 16, 4,
-                                       lane, rows - (warp % 4) * 32);
-                        } else if (live) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 f = unpack2(acc[c * 16 + h * 8 + i]);
-                                const int at = col + h * 16 + 2 * i;
-                                if (at < p.n)
-                                    store1(p.out, p.out_dtype, (size_t)orow * p.n + at, f.x);
-                                if (at + 1 < p.n)
-                                    store1(p.out, p.out_dtype, (size_t)orow * p.n + at + 1, f.y);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 x = unpack2(acc[c * 16 + h * 8 + i * 2]);
+                            const float2 y = unpack2(acc[c * 16 + h * 8 + i * 2 + 1]);
+                            u[i] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
+                                              __float_as_uint(y.x), __float_as_uint(y.y));
                         }
+                        transpose4(u, lane);
+                        store_rows<4>(u, p.out, orow, p.n, col + h * 16, lane, left, align);
                     }
                 }
             }
@@ -818,8 +843,9 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
     p.sb = p.sb2 = sb;
     p.out = out;
     p.out_dtype = out_dtype;
-    p.vec_out = (size_t)p.n * (out_dtype == MOEOP_FP32 ? 4 : 2) % 16 == 0 &&
-                reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(out) |
+                             (uintptr_t)p.n * (out_dtype == MOEOP_FP32 ? 4 : 2);
+    p.out_align = starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : 0;
     p.tiles_m = (p.rows + 127) / 128;
     // Tiles of 128 x 256 read less from L2 and shared memory per product;
     // tiles of 128 x 128 where they need fewer waves of the SMs.
@@ -896,7 +922,6 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     p.nblocks = H / 128;
     p.out = y;
     p.out_dtype = w.y32 ? MOEOP_FP32 : MOEOP_BF16;
-    p.vec_out = true;
     const bool wide = (int64_t)w.max_tiles * ((p.nblocks + 1) / 2) >= d->sms;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     most = (int64_t)w.max_tiles * p.tiles_n;

@@ -265,6 +265,18 @@ def test_matmul_all_codes_and_wide_accumulation():
     assert not out.any()
 
 
+@pytest.mark.parametrize("n", [130, 131, 133, 260, 257, 271, 383, 388, 519])
+@pytest.mark.parametrize("offset", [0, 1, 2, 4])
+def test_matmul_rows_of_outputs_at_every_alignment(n, offset):
+    a, sa, b, sb = operands(150, n, 256)
+    for t in (torch.bfloat16, torch.float32):
+        flat = torch.full((150 * n + 16,), 77.0, dtype=t, device="cuda")
+        out = flat[offset:offset + 150 * n].view(150, n)
+        ops.matmul_fp8(a, sa, b, sb, out=out)
+        check_product(a, sa, b, sb, out)
+        assert (flat[:offset] == 77).all() and (flat[offset + 150 * n:] == 77).all()
+
+
 def test_matmul_strided_operands_and_given_output():
     a, sa, b, sb = operands(70, 200, 640)
     wa = torch.zeros(70, 1024, dtype=torch.uint8, device="cuda").view(ops.F8)
