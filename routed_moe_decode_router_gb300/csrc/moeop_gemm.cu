@@ -847,14 +847,22 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
                              (uintptr_t)p.n * (out_dtype == MOEOP_FP32 ? 4 : 2);
     p.out_align = starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : 0;
     p.tiles_m = (p.rows + 127) / 128;
-    // Tiles of 128 x 256 read less from L2 and shared memory per product;
-    // tiles of 128 x 128 where they need fewer waves of the SMs.
+    // Tiles of 128 x 256 read less per product, tiles of 128 x 128 fill the SMs
+    // better.  By the cycles that a tile takes, measured: 1080 per 128 inputs
+    // and 4500 besides, or 700 and 3500, and 5000 to join a split.  At 8192 x
+    // 4096 x 4096 they take 126 and 176 us, at 2000 x 5000 x 1024 22 and 25
+    // (3 waves, 5 waves), at 700 x 1500 x 3600 25 and 14 (36 tiles, 72 split
+    // in two).
     const int64_t t1 = (int64_t)p.tiles_m * p.nblocks;
     const int64_t t2 = (int64_t)p.tiles_m * ((p.nblocks + 1) / 2);
-    const bool wide = 11 * ((t1 + d->sms - 1) / d->sms) >= 20 * ((t2 + d->sms - 1) / d->sms);
+    const int split = split_of(*d, t1, p.kb);
+    const int64_t c1 = split > 1 ? (p.kb + split - 1) / split * 700 + 8500
+                                 : (t1 + d->sms - 1) / d->sms * ((int64_t)p.kb * 700 + 3500);
+    const int64_t c2 = (t2 + d->sms - 1) / d->sms * ((int64_t)p.kb * 1080 + 4500);
+    const bool wide = c2 < c1;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     const int64_t tiles = wide ? t2 : t1;
-    p.split = wide ? 1 : split_of(*d, tiles, p.kb);
+    p.split = wide ? 1 : split;
     TensorMap ma, mb;
     if ((e = make_map(&ma, a, kBoxRows)) != cudaSuccess || (e = make_map(&mb, b, 128)) != cudaSuccess)
         return e;
