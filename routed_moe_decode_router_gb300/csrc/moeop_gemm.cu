@@ -810,11 +810,12 @@ cudaError_t launch(const TensorMap &ma, const TensorMap &mb, const TensorMap &mb
 }
 
 // Blocks per cluster that share one tile's inputs: as many as still let all
-// tiles run at a time, each with two blocks of inputs or more.  The GPCs do
+// tiles run at a time, each with four blocks of inputs or more (250 x 2048 x
+// 512 takes 7.0 us whole and 8.4 split in two).  The GPCs do
 // not divide evenly (46 clusters of 3 fit 152 SMs, 28 of 5, 23 of 6): the
 // counts are the driver's.
 int split_of(const Dev &d, int64_t tiles, int kb) {
-    int s = kMaxSplit < kb / 2 ? kMaxSplit : kb / 2;
+    int s = kMaxSplit < kb / 4 ? kMaxSplit : kb / 4;
     while (s > 1 && d.clusters[s] < tiles) --s;
     return s < 1 ? 1 : s;
 }
