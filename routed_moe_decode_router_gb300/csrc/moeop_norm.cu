@@ -79,11 +79,18 @@ __device__ __forceinline__ void store8(T *p, int col, int n, const float (&v)[8]
 // blockDim.x threads (a multiple of 32) per row, blockDim.y rows per block.
 // A block loads, waits, computes and stores: what keeps the memory busy is
 // the number of blocks on an SM, so up to 4096 elements the registers are
-// held to 32 (8 blocks of 256).  8192 rows of 4096 bf16 with everything: 51 us
-// (5.9 TB/s) against 66 us with 512 threads of one vector and 3 blocks.
-constexpr int threads_of(int vpt) { return vpt == 8 ? 512 : 256; }
-template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(threads_of(VPT), VPT <= 2 ? 8 : VPT == 4 ? 4 : 1)
+// held to 32 (8 blocks of 256).  8192 rows of 4096 bf16 with everything: 49 us
+// (6.2 TB/s) against 66 us with 512 threads of one vector and 3 blocks.
+// WIDE, where there is an SM for every row: one vector per thread, and the
+// weights are asked for together with the row (one row of 4096: 2.3 us
+// against 3.0).
+constexpr int kSms = 152;
+constexpr int threads_of(int vpt, bool wide) { return wide ? 1024 : vpt == 8 ? 512 : 256; }
+template <typename T, int VPT, bool VEC, bool WIDE>
+__global__ void __launch_bounds__(threads_of(VPT, WIDE), WIDE       ? 1
+                                                         : VPT <= 2 ? 8
+                                                         : VPT == 4 ? 4
+                                                                    : 1)
     rms_norm_kernel(NormParams p) {
     __shared__ float part[32];
     const int H = p.hidden, tpr = blockDim.x;
@@ -96,12 +103,13 @@ __global__ void __launch_bounds__(threads_of(VPT), VPT <= 2 ? 8 : VPT == 4 ? 4 :
     const T *res =
         p.residual ? static_cast<const T *>(p.residual) + (size_t)row * p.residual_stride : nullptr;
     const T *w = static_cast<const T *>(p.weight);
-    float v[VPT][8];
+    float v[VPT][8], g[8];
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int col = (j * tpr + threadIdx.x) * 8;
         if (col < H) {
+            if (WIDE) load8<T, VEC>(w, col, H, g);
             load8<T, VEC>(x, col, H, v[j]);
             if (res) {
                 float r[8];
@@ -134,11 +142,10 @@ __global__ void __launch_bounds__(threads_of(VPT), VPT <= 2 ? 8 : VPT == 4 ? 4 :
     for (int j = 0; j < VPT; ++j) {
         const int col = (j * tpr + threadIdx.x) * 8;
         const bool in = live && col < H;
-        float g[8];
         if (col < H) {
             if (p.residual_out && in)
                 store8<T, VEC>(static_cast<T *>(p.residual_out) + base, col, H, v[j]);
-            load8<T, VEC>(w, col, H, g);
+            if (!WIDE) load8<T, VEC>(w, col, H, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = v[j][i] * inv * g[i];
             if (p.y && in) store8<T, VEC>(static_cast<T *>(p.y) + base, col, H, g);
@@ -180,10 +187,11 @@ __global__ void __launch_bounds__(threads_of(VPT), VPT <= 2 ? 8 : VPT == 4 ? 4 :
 template <typename T, bool VEC>
 cudaError_t launch_vpt(const NormParams &p, int vpt, dim3 grid, dim3 block, cudaStream_t st) {
     switch (vpt) {
-        case 1: rms_norm_kernel<T, 1, VEC><<<grid, block, 0, st>>>(p); break;
-        case 2: rms_norm_kernel<T, 2, VEC><<<grid, block, 0, st>>>(p); break;
-        case 4: rms_norm_kernel<T, 4, VEC><<<grid, block, 0, st>>>(p); break;
-        default: rms_norm_kernel<T, 8, VEC><<<grid, block, 0, st>>>(p); break;
+        case 0: rms_norm_kernel<T, 1, VEC, true><<<grid, block, 0, st>>>(p); break;
+        case 1: rms_norm_kernel<T, 1, VEC, false><<<grid, block, 0, st>>>(p); break;
+        case 2: rms_norm_kernel<T, 2, VEC, false><<<grid, block, 0, st>>>(p); break;
+        case 4: rms_norm_kernel<T, 4, VEC, false><<<grid, block, 0, st>>>(p); break;
+        default: rms_norm_kernel<T, 8, VEC, false><<<grid, block, 0, st>>>(p); break;
     }
     return cudaGetLastError();
 }
@@ -192,11 +200,14 @@ cudaError_t launch_vpt(const NormParams &p, int vpt, dim3 grid, dim3 block, cuda
 
 cudaError_t launch_rms_norm(const NormParams &p, bool vec, cudaStream_t st) {
     // Up to 256 threads of 1, 2 or 4 vectors of 8 elements, then 512 of 8;
-    // short rows share a block.
+    // short rows share a block.  Rows of at most 1024 vectors that have an SM
+    // each: a thread per vector.
     const int nvec = (p.hidden + 7) / 8;
     int vpt = 1;
-    while (nvec > threads_of(vpt) * vpt) vpt *= 2;
-    const int tpr = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
+    while (nvec > threads_of(vpt, false) * vpt) vpt *= 2;
+    if (p.rows <= kSms && nvec <= threads_of(1, true)) vpt = 0;  // WIDE
+    const int per = vpt ? vpt : 1;
+    const int tpr = ((nvec + per - 1) / per + 31) / 32 * 32;
     const int ry = tpr >= 256 || p.rows < 2 ? 1 : 256 / tpr;
     const dim3 block(tpr, ry), grid((p.rows + ry - 1) / ry);
     switch (p.dtype) {
