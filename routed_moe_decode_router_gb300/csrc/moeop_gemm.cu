@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t da = desc0 + (uint64_t)(s * (kStage >> 4));
                 const uint64_t db = da + (kTile >> 4);
                 const uint32_t d = tm + buf * 128 * NB;
-                ok = __all_sync(~0u, spin_bar(&tm_empty[buf], phase ^ 1, &abort_s) &&
-                                         spin_bar(&full[s], ring_phase, &abort_s));
+                ok = __all_sync(~0u, wait_bar(&tm_empty[buf], phase ^ 1, &abort_s) &&
+                                         wait_bar(&full[s], ring_phase, &abort_s));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) acc[i] = 0;
             bool hit = bar_done(&tm_full[it % kBufs], it / kBufs & 1);
+            // (unrolled, the other forms spill registers: 4096 rows 286 -> 430 us)
+#pragma unroll(MODE == kDense ? 2 : 1)
             for (int b = kb0; b < kb1; ++b, ++it) {
                 const int buf = it % kBufs;
                 const bool second = (b - kb0) & 1;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
                 if (second) fetch(b + 1);
                 if (!__all_sync(~0u, hit) && ok)
-                    ok = __all_sync(~0u, spin_bar(&tm_full[buf], it / kBufs & 1, &abort_s));
+                    ok = __all_sync(~0u, wait_bar(&tm_full[buf], it / kBufs & 1, &abort_s));
                 tc_fence_after();
                 // 8 columns at a time: registers are what these warps are short
                 // of, and four of them to a scheduler hide each other's loads.

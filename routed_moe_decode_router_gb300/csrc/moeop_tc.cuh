@@ -37,8 +37,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
 
-// The same wait without suspending the thread: it goes on sooner after the
-// barrier's phase ends, and takes issue slots meanwhile.
+// One look at a barrier, without waiting.
 __device__ __forceinline__ bool bar_done(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -49,11 +48,6 @@ __device__ __forceinline__ bool bar_done(uint64_t *bar, uint32_t parity) {
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
-}
-__device__ __forceinline__ bool spin_bar(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    for (int i = 0; i < 64; ++i)
-        if (bar_done(bar, parity)) return true;
-    return wait_bar(bar, parity, abort);
 }
 
 __device__ __forceinline__ void tma_prefetch_map(const TensorMap *m) {
