@@ -365,12 +365,13 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
     const int E = c.num_experts, k = c.top_k;
     const int64_t base = (int64_t)row * p.stride;
     const bool soft = c.scoring == MOE_SCORING_SOFTMAX;
-    float key[VPT];
+    float key[VPT], bias[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int e = j * 32 + lane;
         const float l = e < E ? load_logit<DT>(p.logits, base + e) : -INFINITY;
         key[j] = is_dead(l) ? -INFINITY : l;
+        bias[j] = p.bias && e < E ? __ldg(p.bias + e) : 0.f;
     }
     float perr = 8 * kUlp, mx = 0.f, inv = 1.f;
     if (soft) {
@@ -392,8 +393,7 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
         for (int j = 0; j < VPT; ++j) {
             const int e = j * 32 + lane;
             const bool dead = !(key[j] > -INFINITY);
-            float biased = prob_of(key[j], soft, mx, inv);
-            if (p.bias && e < E) biased += __ldg(p.bias + e);
+            const float biased = prob_of(key[j], soft, mx, inv) + bias[j];
             if (p.bias && !dead) key[j] = biased;
             if (c.groups > 1 && e < E) sm[e] = dead ? -INFINITY : biased;
         }
