@@ -11,6 +11,10 @@
 // depend on it.  Each block of 128 inputs is summed by itself, then scaled
 // and added in fp32; the warps of a block split the inputs and add up in
 // shared memory, in order.
+//
+// One GB300, in a CUDA graph: 1 x 4096 x 4096 4.5 us (3.7 TB/s with the launch),
+// experts (hidden 2048, 128 x 768, top 8) of one row 14.0 us, against 8.5 and
+// 24.2 us through tensor memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -24,6 +24,14 @@
 // sums, and which adds them in rank order: the result does not depend on
 // timing.
 //
+// Bound by the way out of tensor memory: 128 inputs of a 128 x 256 tile are
+// 512 cycles of MMAs, but some 165 instructions in each of the 16 warps, four
+// to a scheduler, and 96 KB through shared memory (768 cycles); they take 900.
+// One GB300: 8192 x 4096 x 4096 118 us (2.3 PFLOP/s, tensor pipe 52% active),
+// 333 x 1000 x 2048 8.1 us; experts (hidden 2048, 128 x 768, top 8), 4096
+// rows: gate/up 158 us, down 95, the weighted sum 30, lists 10; experts
+// (hidden 4096, 160 x 1536, top 8), 61 rows 413 us, 7.0 TB/s of weights.
+//
 // Calls of a few rows go to moeop_few.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -851,17 +859,17 @@ cudaError_t launch_matmul_fp8(const Fp8Mat &a, const float *sa, const Fp8Mat &b,
     p.out_align = starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : 0;
     p.tiles_m = (p.rows + 127) / 128;
     // Tiles of 128 x 256 read less per product, tiles of 128 x 128 fill the SMs
-    // better.  By the cycles that a tile takes, measured: 1080 per 128 inputs
-    // and 4500 besides, or 700 and 3500, and 5000 to join a split.  At 8192 x
-    // 4096 x 4096 they take 126 and 176 us, at 2000 x 5000 x 1024 22 and 25
-    // (3 waves, 5 waves), at 700 x 1500 x 3600 25 and 14 (36 tiles, 72 split
+    // better.  By the cycles that a tile takes, measured: 900 per 128 inputs
+    // and 4500 besides, or 620 and 3500, and 5000 to join a split.  At 8192 x
+    // 4096 x 4096 they take 121 and 170 us, at 2000 x 5000 x 1024 21 and 25
+    // (3 waves, 5 waves), at 700 x 1500 x 3600 23 and 14 (36 tiles, 72 split
     // in two).
     const int64_t t1 = (int64_t)p.tiles_m * p.nblocks;
     const int64_t t2 = (int64_t)p.tiles_m * ((p.nblocks + 1) / 2);
     const int split = split_of(*d, t1, p.kb);
-    const int64_t c1 = split > 1 ? (p.kb + split - 1) / split * 700 + 8500
-                                 : (t1 + d->sms - 1) / d->sms * ((int64_t)p.kb * 700 + 3500);
-    const int64_t c2 = (t2 + d->sms - 1) / d->sms * ((int64_t)p.kb * 1080 + 4500);
+    const int64_t c1 = split > 1 ? (p.kb + split - 1) / split * 620 + 8500
+                                 : (t1 + d->sms - 1) / d->sms * ((int64_t)p.kb * 620 + 3500);
+    const int64_t c2 = (t2 + d->sms - 1) / d->sms * ((int64_t)p.kb * 900 + 4500);
     const bool wide = c2 < c1;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     const int64_t tiles = wide ? t2 : t1;

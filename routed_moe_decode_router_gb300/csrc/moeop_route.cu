@@ -22,6 +22,11 @@
 // as nearly always, just the candidates' keys are computed, one to a lane, and
 // the same for a sigmoid group's place; else the block's threads share the
 // row's experts out.
+//
+// Bound by instructions: with 256 experts, sigmoid, bias and 8 groups some
+// 1260 a row, five in eight issue slots taken.  One GB300: 16384 rows 23.8 us,
+// 1 row 3.9 us (5.2 where the biases are asked for after the scores), 777 rows
+// of 160 experts by softmax 3.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
