@@ -67,6 +67,17 @@ def test_norm_sizes(dtype, rows, hidden):
     check_norm(x, w, out)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("hidden", [264, 2048, 4096, 4100, 8192, 8200])
+@pytest.mark.parametrize("rows", [152, 153])
+def test_norm_at_a_row_for_every_sm_and_one_more(dtype, rows, hidden):
+    x, r = randn(rows, hidden).to(dtype), randn(rows, hidden, seed=1, std=3.0).to(dtype)
+    w = (1 + randn(hidden, seed=2, std=0.1)).to(dtype)
+    check_norm(x, w, ops.rms_norm(x, w, residual=r, quantize=True), r)
+    own = r.clone()
+    check_norm(x, w, ops.rms_norm(x, w, residual=own, residual_out=own), r)
+
+
 @pytest.mark.parametrize("offset", [0, 1, 8])
 def test_norm_strided_rows_and_in_place(offset):
     big = randn(17, 600).to(torch.bfloat16)
