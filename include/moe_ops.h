@@ -89,13 +89,11 @@ MOE_API moe_status moeop_matmul_fp8(const uint8_t *a, int64_t a_stride, const fl
  *   g, u = q . gate[e]^T, q . up[e]^T;  h = silu(g) * u, held as FP8 rows;
  *   out[t] = sum_j wts[t][j] * (h . down[e]^T)  (+ addend[t]), e = ids[t][j]
  * in slot order.  An id outside [0, num_experts) contributes nothing.  The
- * products of the down projection are held in fp32, those of larger calls
- * (more than 2^20 of them) in bf16, until they are weighted and added in fp32:
- * they are the call's largest traffic, and rounding them once is as large an
- * error as rounding the output.  addend (bf16, may be NULL) and out (bf16) are
- * contiguous; out may be addend.  All weights of a kind are one stack:
- * gate, up [E][inter][hidden], down [E][hidden][inter], each with its scales
- * [E][..][..].  A dense FP8 MLP is the case num_experts = top_k = 1. */
+ * products of the down projection are held in fp32 until they are weighted and
+ * added, in fp32; out is rounded once.  addend (bf16, may be NULL) and out
+ * (bf16) are contiguous; out may be addend.  All weights of a kind are one
+ * stack: gate, up [E][inter][hidden], down [E][hidden][inter], each with its
+ * scales [E][..][..].  A dense FP8 MLP is the case num_experts = top_k = 1. */
 typedef struct moeop_experts_config {
     int hidden;                  /* multiple of 128, 128..32768 */
     int inter;                   /* multiple of 128, 128..32768 */

@@ -53,12 +53,10 @@ cudaError_t launch_few_dense(const Fp8Mat &a, const float *sa, const Fp8Mat &b, 
                              void *out, int out_dtype, int sms, cudaStream_t st);
 
 // Workspace of moeop_experts_fp8: the pairs (row, slot) in expert order, the
-// tiles of 128 of them, the FP8 rows h and the products y.
+// tiles of 128 of them, the FP8 rows h and the products y in fp32.
 struct ExpertsWs {
-    static constexpr size_t kY32 = (size_t)1 << 20;  // products y held in fp32, at most
     size_t header, tiles, pair, token, h, h_scales, y, total;
     int max_tiles;
-    bool y32;  // y in fp32: while it stays in L2 that costs nothing
     static ExpertsWs make(const moeop_experts_config &c, int rows) {
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
         ExpertsWs w{};
@@ -72,9 +70,7 @@ struct ExpertsWs {
         w.token = o, o += up(P * 4);
         w.h = o, o += up(P * c.inter);
         w.h_scales = o, o += up(P * (c.inter / 128) * 4);
-        const size_t ny = P * c.hidden;
-        w.y32 = ny <= kY32;
-        w.y = o, o += up(2 * (ny > 2 * kY32 || w.y32 ? (w.y32 ? 2 : 1) * ny : 2 * kY32));
+        w.y = o, o += up(P * c.hidden * 4);
         // up to 32 pairs: h in fp32 and nothing else
         const size_t few = up((P < kFewPairs ? P : (size_t)kFewPairs) * c.inter * 4);
         w.total = o > few ? o : few;

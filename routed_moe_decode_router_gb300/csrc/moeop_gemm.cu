@@ -29,8 +29,11 @@
 // to a scheduler, and 96 KB through shared memory (768 cycles); they take 900.
 // One GB300: 8192 x 4096 x 4096 118 us (2.3 PFLOP/s, tensor pipe 52% active),
 // 333 x 1000 x 2048 8.1 us; experts (hidden 2048, 128 x 768, top 8), 4096
-// rows: gate/up 158 us, down 95, the weighted sum 30, lists 10; experts
-// (hidden 4096, 160 x 1536, top 8), 61 rows 413 us, 7.0 TB/s of weights.
+// rows 320 us: gate/up 161, down 113, the weighted sum 47 (6.1 TB/s), lists
+// 10; experts (hidden 4096, 160 x 1536, top 8), 61 rows 417 us.  The products y
+// are fp32: rounded to bf16 on their way they would take 37 us less of the
+// 4096 rows and 5 of the 61, and leave an error of 2^-9 of each product where
+// slots cancel.
 //
 // Calls of a few rows go to moeop_few.cu.
 #include <cuda.h>
@@ -514,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int align = MODE == kDown ? 16 : col + kCols <= p.n ? p.out_align : 0;
                     const int left = rows - (warp % 4) * 32;
                     uint4 u[4];
-                    if (p.out_dtype != MOEOP_FP32) {
+                    if (MODE == kDense && p.out_dtype != MOEOP_FP32) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint64_t *v = acc + c * 16 + i * 4;
@@ -634,20 +637,19 @@ __global__ void __launch_bounds__(1024) index_kernel(IndexParams p) {
 // ---------------------------------------------------------------------------
 // out[t] = sum_j wts[t][j] y[t * k + j] (+ addend[t]), in slot order
 // ---------------------------------------------------------------------------
-// Bound by memory: k rows in, one out.  A thread owns 8 outputs and has the
-// loads of kSlots slots under way at a time.  Y32: y is held in fp32.
+// Bound by memory: k rows of fp32 in, one of bf16 out.  A thread owns 8 outputs
+// and has the loads of kSlots slots under way at a time.
 struct CombineParams {
     const int32_t *ids;
     const float *wts;
-    const void *y;
+    const float *y;
     const uint16_t *addend;
     uint16_t *out;
     int rows, hidden, top_k, experts;
 };
 
-template <bool Y32>
 __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
-    constexpr int kSlots = Y32 ? 4 : 8;
+    constexpr int kSlots = 4;
     pdl_wait();
     const int per_row = p.hidden / 8;
     const int64_t n = (int64_t)p.rows * per_row;
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
         for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
             // a slot without an expert has no row y: what lies there is read
             // and not used
-            uint4 v[kSlots][Y32 ? 2 : 1];
+            uint4 v[kSlots][2];
             float w[kSlots];
             bool in[kSlots];
 #pragma unroll
@@ -675,22 +677,17 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
                 in[j] = j0 + j < p.top_k &&
                         (unsigned)__ldg(p.ids + pair) < (unsigned)p.experts;
                 w[j] = __ldg(p.wts + pair);
-                const char *y = static_cast<const char *>(p.y) +
-                                (pair * p.hidden + col) * (Y32 ? 4 : 2);
+                const float *y = p.y + pair * p.hidden + col;
                 v[j][0] = ld_cg_v4(y);
-                if (Y32) v[j][Y32 ? 1 : 0] = ld_cg_v4(y + 16);
+                v[j][1] = ld_cg_v4(y + 4);
             }
 #pragma unroll
             for (int j = 0; j < kSlots; ++j) {
                 if (!in[j]) continue;
-                const uint4 a = v[j][0], b = v[j][Y32 ? 1 : 0];
+                const uint4 a = v[j][0], b = v[j][1];
                 const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float f = Y32 ? __uint_as_float(u[c])
-                                        : c & 1 ? bf16_hi(u[c / 2]) : bf16_lo(u[c / 2]);
-                    acc[c] = fmaf(w[j], f, acc[c]);
-                }
+                for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[j], __uint_as_float(u[c]), acc[c]);
             }
         }
         uint32_t o[4];
@@ -897,7 +894,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     int *token = reinterpret_cast<int *>(a.ws + w.token);
     uint8_t *h = reinterpret_cast<uint8_t *>(a.ws + w.h);
     float *h_scales = reinterpret_cast<float *>(a.ws + w.h_scales);
-    uint16_t *y = reinterpret_cast<uint16_t *>(a.ws + w.y);
+    float *y = reinterpret_cast<float *>(a.ws + w.y);
 
     TensorMap mq, mg, mu, mh, md;
     if ((e = make_map(&mq, {a.q, a.rows, H, H}, 1)) != cudaSuccess ||
@@ -940,7 +937,6 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     p.kb = I / 128;
     p.nblocks = H / 128;
     p.out = y;
-    p.out_dtype = w.y32 ? MOEOP_FP32 : MOEOP_BF16;
     const bool wide = (int64_t)w.max_tiles * ((p.nblocks + 1) / 2) >= d->sms;
     p.tiles_n = wide ? (p.nblocks + 1) / 2 : p.nblocks;
     most = (int64_t)w.max_tiles * p.tiles_n;
@@ -953,8 +949,7 @@ cudaError_t launch_experts_fp8(const ExpertsArgs &a, cudaStream_t st) {
     const CombineParams cp{a.ids, a.wts, y, a.addend, a.out, a.rows, H, k, E};
     const int64_t blocks = ((int64_t)a.rows * (H / 8) + 255) / 256;
     Launch l(blocks < 65536 ? blocks : 65536, 1, 256, 0, true, st);
-    return w.y32 ? cudaLaunchKernelEx(&l.cfg, combine_kernel<true>, cp)
-                 : cudaLaunchKernelEx(&l.cfg, combine_kernel<false>, cp);
+    return cudaLaunchKernelEx(&l.cfg, combine_kernel, cp);
 }
 
 }  // namespace op
