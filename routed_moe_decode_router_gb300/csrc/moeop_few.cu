@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Expe
                     const int i = min(i0 + lane / 8, p.pairs * kb - 1), r = i / kb, b = i % kb;
                     const int at = b * 128 + lane % 8 * 16;
                     float4 v[4];
-                    float amax = kFp8Tiny;
+                    float amax = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         v[j] = __ldcg(reinterpret_cast<const float4 *>(
@@ -330,14 +330,14 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Expe
 #pragma unroll
                     for (int o = 4; o; o >>= 1)
                         amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-                    const float up = kFp8Max / amax;
+                    const Fp8Scale scale(amax);
                     uint32_t q[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        q[j] = pack_e4m3x4(v[j].x * up, v[j].y * up, v[j].z * up, v[j].w * up);
+                        q[j] = scale.codes(v[j].x, v[j].y, v[j].z, v[j].w);
                     *reinterpret_cast<uint4 *>(codes + r * pitch + at) =
                         make_uint4(q[0], q[1], q[2], q[3]);
-                    if (lane % 8 == 0) scales[r * kb + b] = amax / kFp8Max;
+                    if (lane % 8 == 0) scales[r * kb + b] = scale.scale;
                 }
                 __syncthreads();
             }

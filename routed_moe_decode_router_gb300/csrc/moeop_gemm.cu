@@ -29,8 +29,8 @@
 // to a scheduler, and 96 KB through shared memory (768 cycles); they take 900.
 // One GB300: 8192 x 4096 x 4096 118 us (2.3 PFLOP/s, tensor pipe 52% active),
 // 333 x 1000 x 2048 8.1 us; experts (hidden 2048, 128 x 768, top 8), 4096
-// rows 320 us: gate/up 161, down 113, the weighted sum 47 (6.1 TB/s), lists
-// 10; experts (hidden 4096, 160 x 1536, top 8), 61 rows 417 us.  The products y
+// rows 322 us: gate/up 162, down 113, the weighted sum 47 (6.1 TB/s), lists
+// 10; experts (hidden 4096, 160 x 1536, top 8), 61 rows 419 us.  The products y
 // are fp32: rounded to bf16 on their way they would take 37 us less of the
 // 4096 rows and 5 of the 61, and leave an error of 2^-9 of each product where
 // slots cancel.
@@ -482,12 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 amax_s[wg][r] = amax;
                 named_bar(1, kAccWarps * 32);
-                amax = kFp8Tiny;
 #pragma unroll
                 for (int i = 0; i < kColGroups; ++i) amax = fmaxf(amax, amax_s[i][r]);
                 named_bar(1, kAccWarps * 32);  // before the next tile writes amax_s
                 if (storing && live) {
-                    const float up = kFp8Max / amax;
+                    const Fp8Scale scale(amax);
                     const size_t at = (size_t)(done.pos + r) * p.n + done.nt * 128 + wg * kCols;
 #pragma unroll
                     for (int i = 0; i < kCols / 16; ++i) {
@@ -496,13 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 4; ++j) {
                             const float2 x = unpack2(acc[i * 8 + j * 2]);
                             const float2 y = unpack2(acc[i * 8 + j * 2 + 1]);
-                            q[j] = pack_e4m3x4(x.x * up, x.y * up, y.x * up, y.y * up);
+                            q[j] = scale.codes(x.x, x.y, y.x, y.y);
                         }
                         *reinterpret_cast<uint4 *>(p.h + at + i * 16) =
                             make_uint4(q[0], q[1], q[2], q[3]);
                     }
                     if (wg == 0)
-                        p.h_scales[(size_t)(done.pos + r) * (p.n / 128) + done.nt] = amax / kFp8Max;
+                        p.h_scales[(size_t)(done.pos + r) * (p.n / 128) + done.nt] = scale.scale;
                 }
             } else if (storing) {
                 // A lane has 32 consecutive outputs of one row; four lanes

@@ -79,8 +79,9 @@ __device__ __forceinline__ void store8(T *p, int col, int n, const float (&v)[8]
 // blockDim.x threads (a multiple of 32) per row, blockDim.y rows per block.
 // A block loads, waits, computes and stores: what keeps the memory busy is
 // the number of blocks on an SM, so up to 4096 elements the registers are
-// held to 32 (8 blocks of 256).  8192 rows of 4096 bf16 with everything: 49 us
-// (6.2 TB/s) against 66 us with 512 threads of one vector and 3 blocks.
+// held to 32 (8 blocks of 256).  8192 rows of 4096 bf16 with everything: 51 us
+// (5.9 TB/s; 49 with codes by the reciprocal alone) against 66 us with 512
+// threads of one vector and 3 blocks.
 // WIDE, where there is an SM for every row: one vector per thread, and the
 // weights are asked for together with the row (one row of 4096: 2.3 us
 // against 3.0).
@@ -159,17 +160,12 @@ __global__ void __launch_bounds__(threads_of(VPT, WIDE), WIDE       ? 1
             for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(g[i]));
 #pragma unroll
             for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-            amax = fmaxf(amax, kFp8Tiny);
             if (in) {
-                // the code is the nearest e4m3 to y / scale; the reciprocal
-                // changes a code only where y / scale is within 2^-22 of the
-                // middle between two
-                const float up = kFp8Max / amax;
+                const Fp8Scale s(amax);
                 uint32_t c[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    c[i] = pack_e4m3x4(g[4 * i] * up, g[4 * i + 1] * up, g[4 * i + 2] * up,
-                                       g[4 * i + 3] * up);
+                    c[i] = s.codes(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
                 if (VEC) {
                     *reinterpret_cast<uint2 *>(p.q + base + col) = make_uint2(c[0], c[1]);
                 } else {
@@ -178,7 +174,7 @@ __global__ void __launch_bounds__(threads_of(VPT, WIDE), WIDE       ? 1
                         if (col + i < H) p.q[base + col + i] = (uint8_t)(c[i / 4] >> (8 * (i % 4)));
                 }
                 if (threadIdx.x % 16 == 0)
-                    p.scales[(size_t)row * groups + col / 128] = amax / kFp8Max;
+                    p.scales[(size_t)row * groups + col / 128] = s.scale;
             }
         }
     }
