@@ -412,7 +412,7 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
             const bool taken = in >> lane & 1, some = lane < c.groups && s > -INFINITY;
             const float worst = -warp_max(taken ? -s : -INFINITY);
             const float best = warp_max(!taken && some ? s : -INFINITY);
-            const float mag = warp_max(some ? fabsf(s) : 0.f);
+            const float mag = warp_max(some && s < INFINITY ? fabsf(s) : 0.f);
             const float near = 4.f * perr + 6.f * kUlp * mag;
             if (worst - best <= near) {
                 uint32_t settled = 0;
@@ -482,8 +482,10 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
                 __syncwarp();
                 const float v = order_value(mine.x);
                 const bool next = in_k && rank + 1 < n;
-                if (__any_sync(~0u, next && v - order_value(list[next ? rank + 1 : 0].x) <=
-                                                2.f * perr + 4.f * kUlp * fabsf(v))) {
+                // (beside an infinite key nothing is in doubt)
+                if (__any_sync(~0u, next && v < INFINITY &&
+                                        v - order_value(list[next ? rank + 1 : 0].x) <=
+                                            2.f * perr + 4.f * kUlp * fabsf(v))) {
                     // every expert that may belong to the top k: those taken,
                     // and those whose keys are as near to the last taken
                     const float last = order_value(list[min(n, k) - 1].x);
@@ -525,7 +527,8 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
         if (best == 0) break;
         if (p.bias) {
             const float v = order_value(best);
-            if (s) close |= before - v <= 2.f * perr + 4.f * kUlp * fabsf(before);
+            if (s)
+                close |= before < INFINITY && before - v <= 2.f * perr + 4.f * kUlp * fabsf(before);
             before = v;
             if (s == k) break;
         }

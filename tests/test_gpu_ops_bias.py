@@ -1,0 +1,92 @@
+"""GPU tests of the routing with biases that force an expert or take it out,
+on every way a row can be decided: the list of candidates, the near ties
+among them, one expert after another, and the whole row in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from routed_moe_decode_router_gb300 import ops
+from tests import ops_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def randn(*shape, seed=0, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(3000 + seed)
+    return torch.randn(*shape, generator=g, device="cuda") * std
+
+
+def want(logits, top_k, bias, scoring, groups, group_limit, group_score):
+    """(ids, weights) by the definition, in 64 bits: an expert whose logit or
+    biased score is -inf or NaN is out."""
+    x = logits.double()
+    t, e = x.shape
+    dead = ~(x > -math.inf)
+    if scoring == "softmax":
+        p = torch.softmax(x.masked_fill(dead, -math.inf), 1)
+    else:
+        p = 1.0 / (1.0 + torch.exp(-x))
+    p = p.masked_fill(dead, 0.0)
+    key = p + bias.double()
+    key = key.masked_fill(dead | ~(key > -math.inf), -math.inf)
+    best = key.unflatten(1, (groups, -1)).sort(dim=2, descending=True).values
+    score = best[:, :, 0]
+    if group_score == "top2" and best.shape[2] > 1:
+        score = score + best[:, :, 1].masked_fill(best[:, :, 1] == -math.inf, 0.0)
+    rank = score.sort(dim=1, descending=True, stable=True).indices.argsort(1)
+    key = key.masked_fill((rank >= group_limit).repeat_interleave(e // groups, 1), -math.inf)
+    key, ids = key.sort(dim=1, descending=True, stable=True)
+    key, ids = key[:, :top_k], ids[:, :top_k]
+    w = p.gather(1, ids).masked_fill(key == -math.inf, 0.0)
+    total = w.sum(1, keepdim=True)
+    w = torch.where(total > 0, w / total, 0.0)
+    return ids.masked_fill(key == -math.inf, -1).to(torch.int32), w
+
+
+def check(logits, top_k, bias, scoring, groups=1, group_limit=1, group_score="max"):
+    kw = dict(scoring=scoring, groups=groups, group_limit=group_limit, group_score=group_score)
+    ids, w = want(logits, top_k, bias, **kw)
+    got, wts = ops.route_topk(logits, top_k, bias=bias, **kw)
+    assert torch.equal(got, ids), "%d rows differ" % int((got != ids).any(1).sum())
+    # p: expf of a difference up to 100, the sum and the division, under 2^7 U;
+    # the total and its division the same again
+    assert ((wts.double() - w).abs() <= w * 2.0 ** 8 * R.U + 1e-38).all()
+
+
+SCORINGS = pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+
+
+@SCORINGS
+@pytest.mark.parametrize("experts", [40, 128, 256])
+@pytest.mark.parametrize("top_k,forced", [(1, 1), (1, 3), (4, 2), (4, 4), (4, 6), (8, 1), (31, 31),
+                                          (32, 5), (40, 40)])
+def test_forced_experts(scoring, experts, top_k, forced):
+    bias = randn(experts, seed=1, std=0.1)
+    bias[torch.randperm(experts, generator=torch.Generator().manual_seed(2))[:forced]] = math.inf
+    check(randn(50, experts), top_k, bias, scoring)
+    # beside near and exact ties
+    check(randn(50, experts).round(), top_k, bias.round(), scoring)
+    check(torch.zeros(3, experts, device="cuda"), top_k, bias, scoring)
+
+
+@SCORINGS
+@pytest.mark.parametrize("score", ["max", "top2"])
+@pytest.mark.parametrize("limit", [1, 2, 3])
+def test_forced_experts_in_groups(scoring, score, limit):
+    for forced in ([17], [17, 18], [1, 17], [3, 17, 30], range(0, 32, 8)):
+        bias = randn(32, seed=1, std=0.1)
+        bias[list(forced)] = math.inf
+        kw = dict(groups=4, group_limit=limit, group_score=score)
+        check(randn(50, 32), 4, bias, scoring, **kw)
+        # the other groups tie
+        bias = torch.where(bias == math.inf, bias, 0.25)
+        check(torch.zeros(3, 32, device="cuda"), 4, bias, scoring, **kw)
+        check(randn(50, 8).repeat(1, 4), 4, bias, scoring, **kw)
