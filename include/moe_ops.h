@@ -58,10 +58,12 @@ MOE_API moe_status moeop_rms_norm(const void *x, int64_t x_stride, const void *r
  * everything were computed in 64 bits.
  * wts: p of the chosen (never the bias), divided by their sum with
  * norm_topk_prob, times routed_scaling_factor.
- * A logit of -inf or NaN takes its expert out of the row; it counts for no
- * group.  (+inf is no logit: a softmax of it has NaN weights.)  A bias of +inf
- * puts its expert, and its group, before all others; its weight is p as ever.
- * Slots for which no expert is left get id -1 and weight 0. */
+ * A logit of -inf or NaN takes its expert out of the row, a bias of -inf or
+ * NaN out of all rows: it is not taken and counts for no group.  (The softmax
+ * goes over all logits that are not -inf or NaN, whatever the biases; +inf is
+ * no logit, its softmax has NaN weights.)  A bias of +inf puts its expert, and
+ * its group, before all others; its weight is p as ever.  Slots for which no
+ * expert is left get id -1 and weight 0. */
 typedef struct moeop_route_config {
     int num_experts;             /* 1..1024 */
     int top_k;                   /* 1..min(64, group_limit * num_experts / groups) */

@@ -59,6 +59,7 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
         return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(p) + i) << 16);
     return __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t *>(p) + i)));
 }
+// A logit or bias that takes its expert out: -inf or NaN.
 __device__ __forceinline__ bool is_dead(float l) { return !(l > -INFINITY); }
 
 // Order-preserving maps of finite or infinite floats to unsigned; 0 is below
@@ -177,10 +178,11 @@ __device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, in
     }
     for (int e = threadIdx.x; e < E; e += threads) {
         const float l = load_logit<DT>(p.logits, base + e);
+        const float b = p.bias ? __ldg(p.bias + e) : 0.f;
         const bool dead = is_dead(l);
         const double v = dead ? 0.0 : soft ? prob[e] / sum : 1.0 / (1.0 + exp(-(double)l));
         prob[e] = v;
-        key[e] = dead ? -INFINITY : v + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+        key[e] = dead || is_dead(b) ? -INFINITY : v + (double)b;
     }
     __syncthreads();
     if (warp != owner) return;
@@ -196,7 +198,7 @@ __device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, in
     int mine_at = lane;
     for (int e = lane; e < E; e += 32) {
         const float l = load_logit<DT>(p.logits, base + e);
-        const bool out = is_dead(l) || !(in >> ((uint32_t)e * q.div >> 20) & 1);
+        const bool out = key[e] == -INFINITY || !(in >> ((uint32_t)e * q.div >> 20) & 1);
         const uint64_t o = out ? 0 : order_key(p.bias ? key[e] : (double)l);
         ord[e] = o;
         if (o > mine) { mine = o; mine_at = e; }
@@ -397,9 +399,9 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int e = j * 32 + lane;
-            const bool dead = !(key[j] > -INFINITY);
+            const bool dead = is_dead(key[j]) || is_dead(bias[j]);
             const float biased = prob_of(key[j], soft, mx, inv) + bias[j];
-            if (p.bias && !dead) key[j] = biased;
+            if (p.bias) key[j] = dead ? -INFINITY : biased;
             if (c.groups > 1 && e < E) sm[e] = dead ? -INFINITY : biased;
         }
         if (c.groups > 1) {

@@ -81,8 +81,9 @@ def route_topk(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
     """(ids [T, top_k] int32, wts [T, top_k] float32) of logits [T, E] (fp32,
     bf16 or fp16; rows may be strided), in descending order of the selection
     key.  scoring: "softmax" or "sigmoid"; bias [E] float32 is added for the
-    selection only; group_score: "max" or "top2".  Experts whose logit is
-    -inf or NaN are not taken: id -1, weight 0 where none is left."""
+    selection only; group_score: "max" or "top2".  Experts whose logit or bias
+    is -inf or NaN are not taken: id -1, weight 0 where none is left.  A bias
+    of +inf puts its expert first."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return route_topk(logits, top_k, scoring, bias, groups, group_limit, group_score,

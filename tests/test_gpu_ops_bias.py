@@ -90,3 +90,51 @@ def test_forced_experts_in_groups(scoring, score, limit):
         bias = torch.where(bias == math.inf, bias, 0.25)
         check(torch.zeros(3, 32, device="cuda"), 4, bias, scoring, **kw)
         check(randn(50, 8).repeat(1, 4), 4, bias, scoring, **kw)
+
+
+NANS = [math.nan, -math.nan]
+
+
+def test_nans_of_both_signs():
+    signs = torch.tensor(NANS, device="cuda").view(torch.int32) < 0
+    assert signs.tolist() == [False, True]
+
+
+@SCORINGS
+@pytest.mark.parametrize("value", [-math.inf] + NANS, ids=["-inf", "nan", "-nan"])
+@pytest.mark.parametrize("top_k,live", [(1, 0), (4, 2), (4, 9), (8, 3), (31, 20), (32, 20), (40, 7)])
+def test_experts_taken_out_by_their_bias(scoring, value, top_k, live):
+    bias = randn(64, seed=1, std=0.1)
+    off = torch.randperm(64, generator=torch.Generator().manual_seed(3))[live:]
+    bias[off] = value
+    check(randn(50, 64), top_k, bias, scoring)
+    # near and exact ties: the candidates, or the row, again in 64 bits
+    check(randn(50, 64).round(), top_k, bias.round(), scoring)
+    check(torch.zeros(3, 64, device="cuda"), top_k, bias, scoring)
+    # weights too small for fp32: the row in 64 bits
+    far = randn(50, 64, seed=4) - 200.0
+    far[:, off[0]] = 0.0
+    check(far, top_k, bias, scoring)
+    # with a logit that takes its expert out too, and one forced expert
+    gone = randn(50, 64, seed=5)
+    gone[::2, 7] = -math.inf
+    bias[9] = math.inf
+    check(gone, top_k, bias, scoring)
+
+
+@SCORINGS
+@pytest.mark.parametrize("value", [-math.inf] + NANS, ids=["-inf", "nan", "-nan"])
+@pytest.mark.parametrize("score", ["max", "top2"])
+@pytest.mark.parametrize("limit", [1, 2, 3])
+def test_experts_and_groups_taken_out_by_their_bias(scoring, value, score, limit):
+    for off in ([3], [0, 1, 2, 3, 4, 5, 7], list(range(8, 16)), list(range(1, 32)), list(range(32)),
+                [8, 9, 10, 11, 12, 13, 14, 24, 25, 26, 27, 28, 29, 30]):
+        bias = randn(32, seed=1, std=0.1)
+        bias[off] = value
+        kw = dict(groups=4, group_limit=limit, group_score=score)
+        check(randn(50, 32), 8, bias, scoring, **kw)
+        bias = torch.where(bias == bias.clamp(-9, 9), 0.25, bias)
+        # groups that tie
+        check(torch.zeros(3, 32, device="cuda"), 8, bias, scoring, **kw)
+        check(randn(50, 8).repeat(1, 4), 8, bias, scoring, **kw)
+        check(randn(50, 32) - 200.0, 8, bias, scoring, **kw)
