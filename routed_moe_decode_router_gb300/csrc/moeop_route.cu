@@ -94,9 +94,10 @@ __device__ __forceinline__ F warp_sum(F v) {
 
 // Scores of the groups from s[0..E) (dead experts -inf), in lane g for group
 // g; -inf beyond the groups and for groups with nothing left.  *least: the
-// smallest of the values that make the score.
+// smallest of the values that make the score; *size: the sum of their
+// magnitudes, 0 where one is infinite (the score is exact then).
 template <typename F>
-__device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane, F *least) {
+__device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane, F *least, F *size) {
     const int sh = q.lane_shift, lanes = 1 << sh, g = lane >> sh, sub = lane & (lanes - 1);
     const F none = -INFINITY;
     F a = none, b = none;  // the two largest
@@ -122,6 +123,8 @@ __device__ __forceinline__ F group_scores(const F *s, const Args &q, int lane, F
     }
     const bool two = q.p.c.group_score == MOEOP_GROUP_TOP2 && b > none;
     *least = __shfl_sync(~0u, two ? b : a, (lane << sh) & 31);
+    const F sum = a < INFINITY ? fabs(a) + (two ? fabs(b) : F(0)) : F(0);
+    *size = __shfl_sync(~0u, sum, (lane << sh) & 31);
     const F mine = __shfl_sync(~0u, two ? a + b : a, (lane << sh) & 31);
     return lane < q.p.c.groups ? mine : none;
 }
@@ -188,8 +191,8 @@ __device__ __noinline__ void route_row_wide(const Args &q, int row, int lane, in
     if (warp != owner) return;
     uint32_t in = ~0u;
     if (c.groups > 1) {
-        double least;
-        const double score = group_scores<double>(key, q, lane, &least);
+        double least, size;
+        const double score = group_scores<double>(key, q, lane, &least, &size);
         in = take_groups<double>(score, q, lane);
     }
     __syncwarp();
@@ -406,19 +409,22 @@ __device__ __forceinline__ bool route_row(const Args &q, int row, int lane, floa
         }
         if (c.groups > 1) {
             __syncwarp();
-            float least;
-            const float s = group_scores<float>(sm, q, lane, &least);
+            float least, size;
+            const float s = group_scores<float>(sm, q, lane, &least, &size);
             in = take_groups<float>(s, q, lane);
             // the last group taken against the first left out; where nothing
             // is left in either there is nothing to decide
-            const bool taken = in >> lane & 1, some = lane < c.groups && s > -INFINITY;
+            const bool taken = in >> lane & 1, some = lane < c.groups && least > -INFINITY;
             const float worst = -warp_max(taken ? -s : -INFINITY);
             const float best = warp_max(!taken && some ? s : -INFINITY);
-            const float mag = warp_max(some && s < INFINITY ? fabsf(s) : 0.f);
-            const float near = 4.f * perr + 6.f * kUlp * mag;
-            if (worst - best <= near) {
+            // each term of a score is off by perr and u of its magnitude, the
+            // sum by u of theirs; of two large terms that cancel the score
+            // itself says nothing.  Finite terms may sum to more than fp32 holds.
+            const float most = warp_max(some ? size : 0.f);
+            const float near = 4.f * perr + 6.f * kUlp * most;
+            if (worst - best <= near || most == INFINITY) {
                 uint32_t settled = 0;
-                if (!soft)
+                if (!soft && most < INFINITY)
                     settled = settle_groups<VPT, DT>(
                         q, row, lane, sm,
                         __ballot_sync(~0u, some && s >= worst - near && s <= best + near),

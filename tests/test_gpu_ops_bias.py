@@ -138,3 +138,29 @@ def test_experts_and_groups_taken_out_by_their_bias(scoring, value, score, limit
         check(torch.zeros(3, 32, device="cuda"), 8, bias, scoring, **kw)
         check(randn(50, 8).repeat(1, 4), 8, bias, scoring, **kw)
         check(randn(50, 32) - 200.0, 8, bias, scoring, **kw)
+
+
+@SCORINGS
+@pytest.mark.parametrize("limit", [1, 3, 8, 31])
+@pytest.mark.parametrize("big", [0.5, 8.0, 64.0, 256.0, 1000.0, 1e6])
+def test_groups_whose_two_best_cancel(scoring, limit, big):
+    """The score of a group is what is left of two large biased scores."""
+    bias = torch.tensor([big, -big] * 32, device="cuda")
+    kw = dict(groups=32, group_limit=limit, group_score="top2")
+    check(randn(4096, 64), 2, bias, scoring, **kw)
+    # all groups near each other: logits some steps of fp32 apart
+    steps = torch.randint(-8, 9, (500, 64), generator=torch.Generator().manual_seed(6)).cuda()
+    check(randn(500, 2, seed=7).repeat(1, 32) * (1 + steps * 2.0 ** -21), 2, bias, scoring, **kw)
+    few = dict(groups=4, group_limit=min(limit, 3), group_score="top2")
+    bias = torch.cat([randn(28, seed=8, std=0.1), bias[:4]]).view(2, 16).t().reshape(32)
+    check(randn(500, 8, seed=7).repeat(1, 4) * (1 + steps[:, :32] * 2.0 ** -21), 4, bias, scoring,
+          **few)
+
+
+@SCORINGS
+def test_group_scores_beyond_fp32(scoring):
+    pairs = [(2e38, 3.3e38), (3e38, 1e38), (1.0, 2.0), (-3e38, -3e38), (-2e38, -3.3e38),
+             (-math.inf, -3e38), (-math.inf, -math.inf), (3.4e38, -3.4e38)]
+    bias = torch.tensor(pairs, device="cuda").flatten()
+    for limit in range(1, 9):
+        check(randn(20, 16), 2, bias, scoring, groups=8, group_limit=limit, group_score="top2")
