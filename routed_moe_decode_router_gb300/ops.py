@@ -50,6 +50,10 @@ def _load():
             raise RuntimeError("extension %s is missing: build it first "
                                "(python -c 'import __graft_entry__ as g; g.build()')"
                                % _build.BINDING)
+        if _build.built_for() != _build.target():
+            raise RuntimeError("extension %s was built for %s, this is %s: build it again"
+                               % (_build.BINDING, _build.built_for() or "another PyTorch",
+                                  _build.target()))
         loader = importlib.machinery.ExtensionFileLoader("_moe_ops", _build.BINDING)
         mod = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_moe_ops", loader))
