@@ -40,33 +40,47 @@ def quantize_weights(w: torch.Tensor) -> Fp8Weights:
 class Fp8MoeLayer:
     """The layer's weights on a CUDA device, and its forward call.
 
-    norm [H] (bf16); router [E, H] and, with a shared expert, its gate vector
-    [H], which become one FP8 matrix (the gate as its last row); gate, up
+    norm [H] (bf16); router [E, H] and, with a gated shared expert, its gate
+    vector [H], which become one matrix (the gate as its last row); gate, up
     [E, I, H] and down [E, H, I]; shared: the same three matrices
     [1, Is, H] / [1, H, Is] or None.  The routing arguments are those of
-    ops.route_topk."""
+    ops.route_topk.
+
+    router_fp8: the router's matrix as FP8 weights, the logits from the FP8
+    rows that the experts read, in one of the package's products; which of two
+    experts with near logits is taken then depends on the rounding to e4m3.
+    False, for a router trained in bf16 or fp32: its matrix in fp32, the logits
+    an fp32 matrix product with the normed rows in bf16."""
 
     def __init__(self, norm: torch.Tensor, router: torch.Tensor, gate: Fp8Weights,
                  up: Fp8Weights, down: Fp8Weights, top_k: int, *,
                  shared: Optional[tuple] = None, shared_gate: Optional[torch.Tensor] = None,
-                 eps: float = 1e-6, bias: Optional[torch.Tensor] = None, **routing):
+                 router_fp8: bool = True, eps: float = 1e-6,
+                 bias: Optional[torch.Tensor] = None, **routing):
         if (shared is None) != (shared_gate is None):
             raise ValueError("shared and shared_gate come together")
         self.norm, self.eps, self.top_k = norm, eps, top_k
         self.experts = router.shape[0]
         if shared_gate is not None:
             router = torch.cat([router, shared_gate[None].to(router.dtype)])
-        self.router = quantize_weights(router)
+        self.router = quantize_weights(router) if router_fp8 else router.float()
+        self.router_fp8 = router_fp8
         self.routed = (*gate, *up, *down)
         self.shared = None if shared is None else tuple(t for w in shared for t in w)
         self.bias, self.routing = bias, routing
+
+    def logits(self, n: ops.NormOut) -> torch.Tensor:
+        """[T, E] (and the shared gate's column) in fp32 of the normed rows."""
+        if self.router_fp8:
+            return ops.matmul_fp8(n.q, n.scales, *self.router, out_dtype=torch.float32)
+        return torch.mm(n.y.float(), self.router.t())
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
         """(out, residual) [T, H] bf16 of x and the running residual: out is
         what the next layer's norm adds to the returned residual."""
         n = ops.rms_norm(x, self.norm, eps=self.eps, residual=residual, quantize=True,
-                         keep=False)
-        logits = ops.matmul_fp8(n.q, n.scales, *self.router, out_dtype=torch.float32)
+                         keep=not self.router_fp8)
+        logits = self.logits(n)
         ids, wts = ops.route_topk(logits[:, :self.experts], self.top_k, bias=self.bias,
                                   **self.routing)
         out = None
@@ -81,7 +95,8 @@ class Fp8MoeLayer:
 
 
 def random_layer(hidden: int, experts: int, inter: int, top_k: int, seed: int = 0,
-                 device="cuda", shared_inter: int = 0, **routing) -> Fp8MoeLayer:
+                 device="cuda", shared_inter: int = 0, router_fp8: bool = True,
+                 **routing) -> Fp8MoeLayer:
     """A layer with weights N(0, 0.02), as the package's synthetic layers."""
     g = torch.Generator(device=device).manual_seed(seed)
 
@@ -102,7 +117,7 @@ def random_layer(hidden: int, experts: int, inter: int, top_k: int, seed: int = 
     return Fp8MoeLayer((1 + normal(hidden)).to(torch.bfloat16), normal(experts, hidden),
                        stack(experts, inter, hidden), stack(experts, inter, hidden),
                        stack(experts, hidden, inter), top_k, shared=shared, shared_gate=gate,
-                       bias=bias, **routing)
+                       router_fp8=router_fp8, bias=bias, **routing)
 
 
 def main():
