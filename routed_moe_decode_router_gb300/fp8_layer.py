@@ -43,8 +43,8 @@ class Fp8MoeLayer:
     norm [H] (bf16); router [E, H] and, with a gated shared expert, its gate
     vector [H], which become one matrix (the gate as its last row); gate, up
     [E, I, H] and down [E, H, I]; shared: the same three matrices
-    [1, Is, H] / [1, H, Is] or None.  The routing arguments are those of
-    ops.route_topk.
+    [1, Is, H] / [1, H, Is] or None, its output added as it is without a gate
+    vector.  The routing arguments are those of ops.route_topk.
 
     router_fp8: the router's matrix as FP8 weights, the logits from the FP8
     rows that the experts read, in one of the package's products; which of two
@@ -57,8 +57,8 @@ class Fp8MoeLayer:
                  shared: Optional[tuple] = None, shared_gate: Optional[torch.Tensor] = None,
                  router_fp8: bool = True, eps: float = 1e-6,
                  bias: Optional[torch.Tensor] = None, **routing):
-        if (shared is None) != (shared_gate is None):
-            raise ValueError("shared and shared_gate come together")
+        if shared is None and shared_gate is not None:
+            raise ValueError("shared_gate is given without shared")
         self.norm, self.eps, self.top_k = norm, eps, top_k
         self.experts = router.shape[0]
         if shared_gate is not None:
@@ -67,6 +67,7 @@ class Fp8MoeLayer:
         self.router_fp8 = router_fp8
         self.routed = (*gate, *up, *down)
         self.shared = None if shared is None else tuple(t for w in shared for t in w)
+        self.shared_gated = shared_gate is not None
         self.bias, self.routing = bias, routing
 
     def logits(self, n: ops.NormOut) -> torch.Tensor:
@@ -86,17 +87,20 @@ class Fp8MoeLayer:
         out = None
         if self.shared is not None:
             # the shared expert is one expert that every row chooses, its
-            # weight the sigmoid of the gate row's logit
-            one, gate = ops.route_topk(logits[:, self.experts:], 1, scoring="sigmoid",
-                                       norm_topk_prob=False)
+            # weight 1 or the sigmoid of the gate row's logit
+            if self.shared_gated:
+                one, gate = ops.route_topk(logits[:, self.experts:], 1, scoring="sigmoid",
+                                           norm_topk_prob=False)
+            else:
+                one, gate = torch.zeros_like(ids[:, :1]), torch.ones_like(wts[:, :1])
             out = ops.experts_fp8(n.q, n.scales, one, gate, *self.shared)
         out = ops.experts_fp8(n.q, n.scales, ids, wts, *self.routed, addend=out, out=out)
         return out, x if residual is None else n.residual
 
 
 def random_layer(hidden: int, experts: int, inter: int, top_k: int, seed: int = 0,
-                 device="cuda", shared_inter: int = 0, router_fp8: bool = True,
-                 **routing) -> Fp8MoeLayer:
+                 device="cuda", shared_inter: int = 0, shared_gated: bool = True,
+                 router_fp8: bool = True, **routing) -> Fp8MoeLayer:
     """A layer with weights N(0, 0.02), as the package's synthetic layers."""
     g = torch.Generator(device=device).manual_seed(seed)
 
@@ -110,7 +114,7 @@ def random_layer(hidden: int, experts: int, inter: int, top_k: int, seed: int = 
     if shared_inter:
         shared = (stack(1, shared_inter, hidden), stack(1, shared_inter, hidden),
                   stack(1, hidden, shared_inter))
-        gate = normal(hidden)
+        gate = normal(hidden) if shared_gated else None
     bias = None
     if routing.get("scoring") == "sigmoid":
         bias = torch.rand(experts, generator=g, device=device) * 0.2 - 0.1

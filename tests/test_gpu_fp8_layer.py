@@ -1,4 +1,5 @@
-"""GPU tests of the FP8 layer's forms: a router in fp32."""
+"""GPU tests of the FP8 layer's forms: a router in fp32, a shared expert without
+a gate."""
 import pytest
 import torch
 
@@ -55,3 +56,39 @@ def test_router_in_fp32(rows, shared):
     # the same experts' weights behind the router in FP8: its logits differ
     eight = fp8_layer.random_layer(512, 16, 256, 4, seed=3, shared_inter=shared)
     assert (eight.logits(n).double() - y @ w.T).abs().max() > 1e-3
+
+
+@pytest.mark.parametrize("rows", [1, 5, 70])
+@pytest.mark.parametrize("router_fp8", [True, False])
+def test_shared_expert_without_a_gate(rows, router_fp8):
+    lay = fp8_layer.random_layer(512, 16, 256, 4, seed=3, shared_inter=384, shared_gated=False,
+                                 router_fp8=router_fp8, scoring="sigmoid", groups=4, group_limit=2,
+                                 group_score="top2")
+    x = randn(rows, 512).to(torch.bfloat16)
+    n = ops.rms_norm(x, lay.norm, quantize=True)
+    logits = lay.logits(n)
+    assert logits.shape == (rows, 16)
+    ids, wts = ops.route_topk(logits, 4, bias=lay.bias, **lay.routing)
+    one = torch.zeros_like(ids[:, :1])
+    shared, sb = R.experts(n.q, n.scales, one, torch.ones_like(wts[:, :1]), *lay.shared)
+    want, bound = R.experts(n.q, n.scales, ids, wts, *lay.routed)
+    # the shared output is rounded once more on its way, the sum once
+    total = bound + sb + shared.abs() * R.half_step(torch.bfloat16)
+    total = total + (want + shared).abs() * R.half_step(torch.bfloat16)
+    out, res = lay.forward(x)
+    assert res is x
+    within(out, want + shared, total)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again, _ = lay.forward(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+
+
+def test_gate_without_a_shared_expert_is_refused():
+    lay = fp8_layer.random_layer(256, 8, 128, 2)
+    w = fp8_layer.Fp8Weights
+    parts = [w(*lay.routed[i:i + 2]) for i in (0, 2, 4)]
+    with pytest.raises(ValueError, match="without shared"):
+        fp8_layer.Fp8MoeLayer(lay.norm, randn(8, 256), *parts, 2, shared_gate=randn(256))
