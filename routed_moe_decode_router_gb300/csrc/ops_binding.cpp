@@ -1,6 +1,6 @@
 // ops_binding.cpp -- the calls of ops.py as a CPython extension: it checks
 // the tensors' attributes, allocates the outputs through PyTorch and calls
-// the C ABI of include/moe_ops.h on the caller's stream.  It exists for the
+// the C ABI of include/moe_ops.h on the current stream.  It exists for the
 // host's time: a call for one token is a few microseconds of GPU work, and
 // marshalling it through Python and ctypes took 25.
 #include <Python.h>
@@ -120,9 +120,8 @@ int small(int64_t n, const char *name) {
 Tensor fresh(at::IntArrayRef shape, ScalarType type, const at::Device &dev) {
     return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
-void *stream_of(PyObject *o, const at::Device &dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-    return PyLong_AsVoidPtr(o);
+void *stream_of(const at::Device &dev) {
+    return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
 }
 template <typename T>
 T *ptr(const Tensor &t) {
@@ -138,9 +137,9 @@ bool counted(Py_ssize_t n, Py_ssize_t want) {
     return false;
 }
 
-// (x, weight, eps, residual, quantize, keep, residual_out, stream)
+// (x, weight, eps, residual, quantize, keep, residual_out)
 PyObject *rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!counted(n, 8)) return nullptr;
+    if (!counted(n, 7)) return nullptr;
     const double eps = PyFloat_AsDouble(a[2]);
     if (PyErr_Occurred()) return nullptr;
     return guarded([&] {
@@ -175,14 +174,14 @@ PyObject *rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 small(hidden, "x"), code_of(type), (float)eps, keep ? y.data_ptr() : nullptr,
                 res_out.defined() ? res_out.data_ptr() : nullptr,
                 quantize ? ptr<uint8_t>(q) : nullptr, quantize ? ptr<float>(scales) : nullptr,
-                stream_of(a[7], dev)));
+                stream_of(dev)));
         return Py_BuildValue("(NNNN)", wrapped(y), wrapped(res_out), wrapped(q), wrapped(scales));
     });
 }
 
-// (logits, top_k, scoring, bias, groups, group_limit, group_score, norm, factor, stream)
+// (logits, top_k, scoring, bias, groups, group_limit, group_score, norm, factor)
 PyObject *route_topk(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!counted(n, 10)) return nullptr;
+    if (!counted(n, 9)) return nullptr;
     const long k = PyLong_AsLong(a[1]), scoring = PyLong_AsLong(a[2]), groups = PyLong_AsLong(a[4]),
                limit = PyLong_AsLong(a[5]), score = PyLong_AsLong(a[6]);
     const double factor = PyFloat_AsDouble(a[8]);
@@ -203,14 +202,14 @@ PyObject *route_topk(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                    small(groups, "groups"), small(limit, "group_limit"), (int)score,
                                    a[7] == Py_True, (float)factor, code_of(x.scalar_type())};
         check(moeop_route_topk(&c, x.data_ptr(), row_stride(x), bias, small(rows, "logits"),
-                               ptr<int32_t>(ids), ptr<float>(wts), stream_of(a[9], dev)));
+                               ptr<int32_t>(ids), ptr<float>(wts), stream_of(dev)));
         return Py_BuildValue("(NN)", wrapped(ids), wrapped(wts));
     });
 }
 
-// (a, a_scales, b, b_scales, out_dtype code, out, stream)
+// (a, a_scales, b, b_scales, out_dtype code, out)
 PyObject *matmul_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!counted(n, 7)) return nullptr;
+    if (!counted(n, 6)) return nullptr;
     const long code = PyLong_AsLong(a[4]);
     if (PyErr_Occurred()) return nullptr;
     return guarded([&] {
@@ -226,15 +225,15 @@ PyObject *matmul_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                : need(a[5], "out", type_of(code), {m, cols}, dev);
         check(moeop_matmul_fp8(ptr<uint8_t>(x), row_stride(x), ptr<float>(sa), ptr<uint8_t>(w),
                                row_stride(w), ptr<float>(sb), small(m, "a"), small(cols, "b"),
-                               small(k, "a"), out.data_ptr(), (int)code, stream_of(a[6], dev)));
+                               small(k, "a"), out.data_ptr(), (int)code, stream_of(dev)));
         return wrapped(out);
     });
 }
 
 // (q, scales, ids, wts, gate, gate_scales, up, up_scales, down, down_scales, workspace, addend,
-//  out, stream)
+//  out)
 PyObject *experts_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!counted(n, 14)) return nullptr;
+    if (!counted(n, 13)) return nullptr;
     return guarded([&] {
         const Tensor &q = first(a[0], "q", 2), &gate = first(a[4], "gate", 3),
                      &ids = first(a[2], "ids", 2);
@@ -272,7 +271,7 @@ PyObject *experts_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                       ptr<float>(gs), ptr<float>(us), ptr<float>(ds)};
         check(moeop_experts_fp8(&c, &w, ptr<uint8_t>(q), ptr<float>(scales), ptr<int32_t>(ids),
                                 ptr<float>(wts), addend, ptr<uint16_t>(out), small(t, "q"),
-                                ws.data_ptr(), (size_t)ws.numel(), stream_of(a[13], dev)));
+                                ws.data_ptr(), (size_t)ws.numel(), stream_of(dev)));
         return wrapped(out);
     });
 }

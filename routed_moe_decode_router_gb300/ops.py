@@ -75,7 +75,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         with torch.cuda.stream(stream):
             return rms_norm(x, weight, eps, residual, quantize, keep, residual_out)
     return NormOut(*(_ext or _load()).rms_norm(x, weight, eps, residual, bool(quantize),
-                                               bool(keep), residual_out, None))
+                                               bool(keep), residual_out))
 
 
 def route_topk(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
@@ -99,7 +99,7 @@ def route_topk(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                          "not %r and %r" % (scoring, group_score)) from None
     return (_ext or _load()).route_topk(
         logits, top_k, scoring_code, bias, groups, group_limit, score_code,
-        bool(norm_topk_prob), routed_scaling_factor, None)
+        bool(norm_topk_prob), routed_scaling_factor)
 
 
 def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -114,7 +114,7 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     code = _DTYPES.get(out_dtype if out is None else out.dtype)
     if code is None:
         raise ValueError("out_dtype is %s, expected bfloat16, float16 or float32" % out_dtype)
-    return (_ext or _load()).matmul_fp8(a, a_scales, b, b_scales, code, out, None)
+    return (_ext or _load()).matmul_fp8(a, a_scales, b, b_scales, code, out)
 
 
 class ExpertsWorkspace:
@@ -148,7 +148,7 @@ def experts_fp8(q: torch.Tensor, scales: torch.Tensor, ids: torch.Tensor, wts: t
                                down_scales, ws, addend, out)
     return (_ext or _load()).experts_fp8(
         q, scales, ids, wts, gate, gate_scales, up, up_scales, down, down_scales,
-        None if ws is None else ws.buf, addend, out, None)
+        None if ws is None else ws.buf, addend, out)
 
 
 def device_status(stream=None) -> int:
