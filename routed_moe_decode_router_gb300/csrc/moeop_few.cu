@@ -13,7 +13,7 @@
 // shared memory, in order.
 //
 // One GB300, in a CUDA graph: 1 x 4096 x 4096 4.5 us (3.7 TB/s with the launch),
-// experts (hidden 2048, 128 x 768, top 8) of one row 14.0 us, against 8.5 and
+// experts (hidden 2048, 128 x 768, top 8) of one row 14.1 us, against 8.5 and
 // 24.2 us through tensor memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -256,7 +256,9 @@ __global__ void __launch_bounds__(256, 3) few_gate_up_kernel(const ExpertsParams
 // Block: 16 columns of the output, for every pair, and their weighted sums.
 // First h becomes e4m3 codes and scales in shared memory; then a unit of work
 // is a group and a share of its inputs.  The first unit's weights do not
-// depend on h and are on their way before it is there.
+// depend on h and are asked for before it is there.  That overlaps little of
+// the kernel before: 512 threads of 128 registers are all that an SM has, so a
+// block starts only where no gate/up block is left.
 constexpr int kDownWarps = 16;
 // Row of codes: 64 bytes past a multiple of 128, so that the rows of two
 // columns lie in different banks.

@@ -25,12 +25,14 @@
 // timing.
 //
 // Bound by the way out of tensor memory: 128 inputs of a 128 x 256 tile are
-// 512 cycles of MMAs, but some 165 instructions in each of the 16 warps, four
-// to a scheduler, and 96 KB through shared memory (768 cycles); they take 900.
-// One GB300: 8192 x 4096 x 4096 118 us (2.3 PFLOP/s, tensor pipe 52% active),
-// 333 x 1000 x 2048 8.1 us; experts (hidden 2048, 128 x 768, top 8), 4096
+// 512 cycles of MMAs, but take 900.  Each of the 16 warps, four to a scheduler,
+// has some 145 instructions for them and waits for its loads of 8 columns one
+// at a time; no unit is saturated (8192 x 4096 x 4096: issue slots 54%, tensor
+// pipe 52%, L1 46%).
+// One GB300: 8192 x 4096 x 4096 119 us (2.3 PFLOP/s) in a short run, 127 when
+// thousands in a row meet the power limit; 333 x 1000 x 2048 8.1 us; experts (hidden 2048, 128 x 768, top 8), 4096
 // rows 322 us: gate/up 162, down 113, the weighted sum 47 (6.1 TB/s), lists
-// 10; experts (hidden 4096, 160 x 1536, top 8), 61 rows 419 us.  The products y
+// 10; experts (hidden 4096, 160 x 1536, top 8), 61 rows 419 to 428 us.  The products y
 // are fp32: rounded to bf16 on their way they would take 37 us less of the
 // 4096 rows and 5 of the 61, and leave an error of 2^-9 of each product where
 // slots cancel.
@@ -385,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) acc[i] = 0;
             bool hit = bar_done(&tm_full[it % kBufs], it / kBufs & 1);
-            // (unrolled, the other forms spill registers: 4096 rows 286 -> 430 us)
+            // (unrolled, the gate/up form spills 224 bytes of registers: 4096
+            // rows of experts 286 -> 430 us with both forms unrolled)
 #pragma unroll(MODE == kDense ? 2 : 1)
             for (int b = kb0; b < kb1; ++b, ++it) {
                 const int buf = it % kBufs;

@@ -7,7 +7,9 @@
 // Bound by memory: every input is read once and every output written once.
 // A thread owns 8 consecutive elements (16 bytes of a 16-bit type) per
 // vector, 16 threads one group of 128, so a group's amax is four shuffles and
-// the row stays in registers between the two passes.
+// the row is not read again for the second pass: it stays in registers, but
+// for what the limits below make the compiler spill (at 2049 to 4096 elements
+// 60 to 112 bytes a thread, which stay in L1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -81,7 +83,8 @@ __device__ __forceinline__ void store8(T *p, int col, int n, const float (&v)[8]
 // the number of blocks on an SM, so up to 4096 elements the registers are
 // held to 32 (8 blocks of 256).  8192 rows of 4096 bf16 with everything: 51 us
 // (5.9 TB/s; 49 with codes by the reciprocal alone) against 66 us with 512
-// threads of one vector and 3 blocks.
+// threads of one vector and 3 blocks; fp32 92 us (6.2 TB/s).  Rows that do not
+// start on 16 bytes go element by element: 8192 x 4095 bf16 200 us.
 // WIDE, where there is an SM for every row: one vector per thread, and the
 // weights are asked for together with the row (one row of 4096: 2.3 us
 // against 3.0).

@@ -16,17 +16,20 @@
 // with u = 2^-24, expf, the divisions and the sum of E terms (E/32 serial, 5
 // in the tree) leave p within (E/32 + 16) u of its value, relative to the
 // largest p of the row; a sigmoid within 8 u; adding the bias rounds by u
-// |key|.  About one row in a thousand takes the second way with N(0, 1.5)
-// logits, 256 experts and a bias.  64-bit arithmetic is slow here (an SM does
+// |key|, and a group's sum of two by u of their magnitudes.  About one row in a
+// thousand takes the second way with N(0, 1.5) fp32 logits, 256 experts and a
+// bias that tells them apart.  Equal keys count as near: of bf16 logits with a
+// constant bias a third of the rows does.  64-bit arithmetic is slow here (an SM does
 // two such operations a cycle): where only the order of the keys is in doubt,
 // as nearly always, just the candidates' keys are computed, one to a lane, and
 // the same for a sigmoid group's place; else the block's threads share the
 // row's experts out.
 //
 // Bound by instructions: with 256 experts, sigmoid, bias and 8 groups some
-// 1260 a row, five in eight issue slots taken.  One GB300: 16384 rows 23.8 us,
-// 1 row 3.9 us (5.2 where the biases are asked for after the scores), 777 rows
-// of 160 experts by softmax 3.6 us.
+// 1270 a row, six in ten issue slots taken.  One GB300: 16384 rows 24 us, 1 row
+// 3.9 us (5.2 where the biases are asked for after the scores), 777 rows of 160
+// experts by softmax 3.6 us.  16384 x 256 by softmax: 17 us; with a bias of
+// zeros 27 us, of bf16 logits 102; 8 groups by the largest 29 us, bf16 65.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
