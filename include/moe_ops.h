@@ -2,7 +2,9 @@
  * moe_ops.h -- C ABI of the FP8 layer operators: the operators around and
  * inside a routed MoE layer whose weights are e4m3 with one scale per block
  * of 128 x 128, for any number of token rows (one decoded token to prompts
- * of thousands).  They are in the same library as moe_router.h and follow its
+ * of thousands), and the other operators of a decoding step: the paged cache
+ * of keys and values, attention over it, and the verification of drafted
+ * tokens.  They are in the same library as moe_router.h and follow its
  * conventions: device pointers, the caller's memory and stream, every check
  * on the host before the first launch, moe_status with moe_last_error(), no
  * allocation and no synchronisation (moeop_read_device_status excepted), and
@@ -30,6 +32,7 @@ extern "C" {
 #define MOEOP_MAX_GROUPS 32
 
 enum { MOEOP_BF16 = 0, MOEOP_FP16 = 1, MOEOP_FP32 = 2 };
+enum { MOEOP_E4M3 = 3 };           /* of a cache only */
 enum { MOEOP_GROUP_MAX = 0, MOEOP_GROUP_TOP2 = 1 };
 
 /* Root-mean-square norm with the residual's addition and an FP8 output.
@@ -120,6 +123,109 @@ MOE_API moe_status moeop_experts_fp8(const moeop_experts_config *cfg,
                                      const float *scales, const int32_t *ids, const float *wts,
                                      const uint16_t *addend, uint16_t *out, int rows, void *ws,
                                      size_t ws_bytes, void *stream);
+
+/* A paged cache of keys and values.  Page p, key/value head h, place i of the
+ * page: dim elements at k + p * k_stride + (h * page + i) * dim, so that a head's
+ * places of a page are one contiguous run.  e4m3: codes, and an fp32 scale for
+ * each head and place (k_scales + p * k_scales_stride + h * page + i); value =
+ * code * scale.  A slot is a place in the cache: page number * page + i.  The
+ * strides are in elements, from one page to the next.
+ * k, v and their strides 16-byte aligned; scales NULL unless e4m3. */
+typedef struct moeop_kv_cache {
+    void *k, *v;
+    float *k_scales, *v_scales;
+    int64_t k_stride, v_stride, k_scales_stride, v_scales_stride;
+    int pages, heads;            /* pages * page < 2^31; heads 1..1024 */
+    int page;                    /* a multiple of 16, 16..1024 */
+    int dim;                     /* 64, 128 or 256 */
+    int type;                    /* MOEOP_BF16, MOEOP_FP16 or MOEOP_E4M3 */
+} moeop_kv_cache;
+
+/* Write the keys and values of `tokens` tokens, [tokens][heads][dim] with row
+ * strides in elements, to their slots.  e4m3: scale = max(largest magnitude of
+ * the dim, 1e-30) / 448, code = e4m3(value / scale), from any dtype; a cache of
+ * 16 bits takes rows of its own type and keeps them as they are.  A slot outside
+ * the cache is passed over.  The slots of a call are distinct: what a slot given
+ * twice holds afterwards is not defined (the others are not touched by it).
+ * k, v and their strides 16-byte aligned. */
+MOE_API moe_status moeop_kv_write(const moeop_kv_cache *cache, const void *k, int64_t k_stride,
+                                  const void *v, int64_t v_stride, int dtype,
+                                  const int32_t *slots, int tokens, void *stream);
+
+/* Read slots back: k, v [tokens][heads][dim] of type dtype, contiguous, 16-byte
+ * aligned.  A slot outside the cache gives zeros. */
+MOE_API moe_status moeop_kv_read(const moeop_kv_cache *cache, const int32_t *slots, int tokens,
+                                 void *k, void *v, int dtype, void *stream);
+
+/* Attention of the last `rows` tokens of each of `batch` sequences over their
+ * cached tokens (their own among them: write first).  Sequence b has lengths[b]
+ * tokens (negative: none; more than width * page: that many); token j is at
+ * place j % page of page table[b][j / page], row r at position
+ * lengths[b] - rows + r.  A row sees the tokens up to its own position, with a
+ * window only the last `window` of them, its own included; a page number
+ * outside the cache takes its tokens out.
+ *   out = sum_j softmax(scale * q . k_j)_j v_j
+ * with each of the group = q_heads / heads query heads of a key/value head.  A
+ * row that sees nothing (a position before the first token, length 0), or only
+ * scores of -inf, is zero.  What a row does not see does not reach it, NaN and
+ * infinities included.
+ * q [batch][rows][q_heads][dim] with strides (elements) of batch and rows, out the
+ * same, contiguous, both of type dtype: bf16 or fp16, the cache's own type where
+ * that is one of 16 bits.  Products, softmax statistics and sums are in fp32;
+ * probabilities enter the second product as two 16-bit numbers whose sum is
+ * within 2^-16 (bf16; 2^-22 fp16, e4m3) of them.  out is rounded once.
+ * Scores beyond the range of fp32 give NaN, as they do in a softmax. */
+typedef struct moeop_attend_config {
+    int batch;                   /* 0..2048 */
+    int rows;                    /* 1..64 */
+    int q_heads;                 /* a multiple of the cache's heads; rows * group <= 256 */
+    int width;                   /* pages in a row of the table, >= 1 */
+    int window;                  /* 0 = none */
+    float scale;                 /* finite */
+    int dtype;                   /* of q and out */
+} moeop_attend_config;
+
+/* Bytes of workspace for calls of this batch (and smaller ones), rows, q_heads,
+ * heads and dim (0 = refused).  It is initialised once, by
+ * moeop_attend_workspace_init, and every call leaves it ready for the next, of
+ * the same or another shape.  256-byte aligned; calls that overlap on the GPU
+ * need one each. */
+MOE_API size_t moeop_attend_workspace_size(int batch, int rows, int q_heads, int heads, int dim);
+MOE_API moe_status moeop_attend_workspace_init(void *ws, size_t ws_bytes, void *stream);
+MOE_API moe_status moeop_attend_paged(const moeop_attend_config *cfg, const moeop_kv_cache *cache,
+                                      const void *q, int64_t q_batch_stride, int64_t q_row_stride,
+                                      const int32_t *table, int64_t table_stride,
+                                      const int32_t *lengths, void *out, void *ws,
+                                      size_t ws_bytes, void *stream);
+
+/* Which drafted tokens stay, and the token after them, for each of `batch`
+ * sequences (speculative sampling: the result is distributed as the target).
+ * draft [batch][drafts]: token ids, ended early by a negative one.  target
+ * [batch][drafts + 1][vocab]: the target's probabilities before each draft and
+ * after the last.  draft_probs [batch][drafts][vocab]: those that the drafts
+ * were drawn from, or NULL (each draft certain: probability 1 of itself).
+ *   draft i stays while accept_u[b][i] * draft_probs[b][i][x] < target[b][i][x]
+ * (in 64 bits).  The token after those that stay is drawn, at the first draft
+ * refused, from max(target - draft_probs, 0) (from target where that is 0
+ * everywhere), after the last draft from target: the lowest id whose running
+ * sum exceeds sample_u[b] times the whole sum.
+ * tokens [batch][drafts + 1]: those that stay, the one drawn (-1 if no weight is
+ * positive), then -1; accepted [batch]: how many stayed.
+ * Probabilities are numbers from 0 to 1 (less, or NaN, counts as 0, more as 1)
+ * and are counted in steps of 2^-44, exactly, so that no order of summation
+ * decides; their sum need not be 1.  A draft of vocab or more is refused.
+ * sample_u: in [0, 1) (less, or NaN, counts as 0, more as the largest below 1). */
+typedef struct moeop_verify_config {
+    int batch;                   /* 0..65535 */
+    int drafts;                  /* 0..31 */
+    int vocab;                   /* 1..2^19 */
+    int64_t target_stride, draft_stride;  /* elements between rows of vocab */
+} moeop_verify_config;
+
+MOE_API moe_status moeop_verify_draft(const moeop_verify_config *cfg, const int32_t *draft,
+                                      const float *target, const float *draft_probs,
+                                      const float *accept_u, const float *sample_u,
+                                      int32_t *tokens, int32_t *accepted, void *stream);
 
 /* Synchronise `stream`, read the current device's status word of these
  * operators into *code (MOE_DEV_*) and clear it.  MOE_DEV_WAIT_TIMEOUT: an

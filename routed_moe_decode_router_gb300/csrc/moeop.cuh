@@ -96,6 +96,88 @@ cudaError_t allow_few_smem();
 
 cudaError_t status_word(uint32_t **p);  // the current device's status word
 
+// Quotients of numbers below 2^31 by one that many share: a multiplication
+// (T. Granlund and P. Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct Divisor {
+    uint32_t d, mul, shift;
+    Divisor() = default;
+    explicit Divisor(uint32_t by) : d(by), shift(0) {
+        while (shift < 31 && (1u << shift) < by) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - by)) / by + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t over(uint32_t n) const {
+        return (__umulhi(n, mul) + n) >> shift;
+    }
+#endif
+};
+
+// moeop_kv_write and moeop_kv_read: the cache, and the rows outside of it.
+struct CacheParams {
+    void *k, *v;
+    float *k_scales, *v_scales;
+    int64_t k_stride, v_stride, k_scales_stride, v_scales_stride;
+    int slots, heads, page, dim, cache_type;
+    void *k_io, *v_io;
+    int64_t k_io_stride, v_io_stride;
+    int io_type, tokens, lanes_log2;  // 2^lanes_log2 = dim / 16 lanes to a row
+    const int32_t *slots_of;
+    Divisor by_page, by_heads;
+};
+cudaError_t launch_kv_write(const CacheParams &p, cudaStream_t st);
+cudaError_t launch_kv_read(const CacheParams &p, cudaStream_t st);
+
+// moeop_verify_draft.
+struct VerifyParams {
+    moeop_verify_config c;
+    const int32_t *draft;
+    const float *target, *draft_probs, *accept_u, *sample_u;
+    int32_t *tokens, *accepted;
+};
+cudaError_t launch_verify_draft(const VerifyParams &p, cudaStream_t st);
+
+// moeop_attend_paged.
+struct AttendParams {
+    const void *k, *v;
+    const float *k_scales, *v_scales;
+    int64_t k_stride, v_stride, k_scales_stride, v_scales_stride;
+    int pages, heads, page;
+    const void *q;
+    int64_t q_batch_stride, q_row_stride;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lengths;
+    void *out;
+    int batch, rows, group, width, window, dtype;
+    float scale_log2;          // of the scores, times log2(e)
+    int blocks;                // of query rows of a key/value head
+    uint32_t *counters;        // kAttendCounters, zero between calls
+    float *parts;              // sums of a warp's or thread block's share of an item
+};
+// Query rows (row, head of the group) that a thread block takes together.
+constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 16; }
+// Thread blocks for each block of query rows: together one for every SM.
+constexpr int kAttendSms = 152, kAttendCounters = 256, kAttendMaxBatch = 2048;
+constexpr int attend_grid(int blocks) { return blocks < kAttendSms ? kAttendSms / blocks : 1; }
+// Workspace of moeop_attend_paged: the counters, in every shape the same, then a
+// partial sum for each warp (up to 16 in a thread block, 8 where dim is 256) and
+// two for each thread block: three numbers for a row, and the row.
+struct AttendWs {
+    size_t parts, total;
+    static AttendWs make(int m, int dim) {
+        const int block = attend_block(dim, m), blocks = (m + block - 1) / block;
+        const size_t part = (size_t)block * (3 + dim) * 4;
+        AttendWs w{};
+        w.parts = kAttendCounters * 4;
+        w.total = w.parts + part * blocks * attend_grid(blocks) * ((dim == 256 ? 8 : 16) + 2);
+        return w;
+    }
+};
+cudaError_t launch_attend_f8(const AttendParams &p, int dim, cudaStream_t st);
+cudaError_t launch_attend_bf(const AttendParams &p, int dim, cudaStream_t st);
+cudaError_t launch_attend_hf(const AttendParams &p, int dim, cudaStream_t st);
+
 #ifdef __CUDACC__
 // Four values -> four e4m3 codes, nearest even, beyond +-448 the largest.
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {

@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "moe_ops.h"
@@ -276,6 +277,228 @@ PyObject *experts_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// The four tensors of a cache: k and v [pages][heads][page][dim], contiguous but for
+// the stride of the pages, and with e4m3 the scales [pages][heads][page].
+struct Cache {
+    moeop_kv_cache c{};
+    at::Device dev;
+    explicit Cache(PyObject *const *a) : dev(at::kCUDA) {
+        const Tensor &k = first(a[0], "the cache's k", 4);
+        dev = k.device();
+        const ScalarType type = k.scalar_type();
+        c.type = type == kF8 ? (int)MOEOP_E4M3 : type == at::kFloat ? -1 : code_of(type);
+        if (c.type < 0)
+            value_error(std::string("the cache's k has dtype ") + c10::toString(type) +
+                        ", expected float8_e4m3fn, bfloat16 or float16");
+        const int64_t pages = k.size(0), heads = k.size(1), page = k.size(2), dim = k.size(3);
+        c.pages = small(pages, "pages"), c.heads = small(heads, "heads");
+        c.page = small(page, "page"), c.dim = small(dim, "dim");
+        paged(k, "the cache's k", type, {pages, heads, page, dim});
+        c.k = k.data_ptr(), c.k_stride = page_stride(k);
+        const Tensor &v = tensor(a[1], "the cache's v");
+        paged(v, "the cache's v", type, {pages, heads, page, dim});
+        c.v = v.data_ptr(), c.v_stride = page_stride(v);
+        if (c.type == MOEOP_E4M3) {
+            const Tensor &ks = tensor(a[2], "the cache's k_scales"),
+                         &vs = tensor(a[3], "the cache's v_scales");
+            paged(ks, "the cache's k_scales", at::kFloat, {pages, heads, page});
+            paged(vs, "the cache's v_scales", at::kFloat, {pages, heads, page});
+            c.k_scales = ptr<float>(ks), c.k_scales_stride = page_stride(ks);
+            c.v_scales = ptr<float>(vs), c.v_scales_stride = page_stride(vs);
+        } else if (a[2] != Py_None || a[3] != Py_None) {
+            value_error("a cache of 16 bits has no scales");
+        }
+    }
+    static int64_t page_stride(const Tensor &t) {
+        return t.size(0) > 1 ? t.stride(0) : t.numel();
+    }
+    void paged(const Tensor &t, const char *name, ScalarType type, at::IntArrayRef shape) const {
+        const auto n = [&] { return std::string(name); };
+        if (t.scalar_type() != type)
+            value_error(n() + " has dtype " + c10::toString(t.scalar_type()) + ", expected " +
+                        c10::toString(type));
+        if (t.sizes() != shape)
+            value_error(n() + " has shape " + text(t.sizes()) + ", expected " + text(shape));
+        if (t.device() != dev) value_error(n() + " is on " + t.device().str() + ", expected " +
+                                           dev.str());
+        int64_t inner = 1;
+        for (int64_t i = t.dim() - 1; i > 0; --i) {
+            if (t.size(i) > 1 && t.stride(i) != inner)
+                value_error(n() + " must be contiguous in its pages");
+            inner *= t.size(i);
+        }
+    }
+};
+
+// A tensor whose last two dimensions are contiguous; the strides of those before
+// them are taken.
+void rows_of_heads(const Tensor &t, const char *name, int64_t heads, int64_t dim) {
+    const int64_t d = t.dim();
+    if ((dim > 1 && t.stride(d - 1) != 1) || (heads > 1 && t.stride(d - 2) != dim))
+        value_error(std::string(name) + " must be contiguous in its rows of heads");
+}
+
+// (k of the cache, v, k_scales, v_scales, k, v, slots)
+PyObject *kv_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!counted(n, 7)) return nullptr;
+    return guarded([&] {
+        const Cache cache(a);
+        const moeop_kv_cache &c = cache.c;
+        const Tensor &k = tensor(a[4], "k"), &v = tensor(a[5], "v");
+        const ScalarType type = k.scalar_type();
+        if (k.dim() != 3) value_error("k has " + std::to_string(k.dim()) + " dimensions, expected 3");
+        if (code_of(type) < 0)
+            value_error(std::string("k has dtype ") + c10::toString(type) +
+                        ", expected bfloat16, float16 or float32");
+        const int64_t t = k.size(0);
+        for (const Tensor *x : {&k, &v}) {
+            const char *name = x == &k ? "k" : "v";
+            if (x->scalar_type() != type)
+                value_error(std::string(name) + " has dtype " + c10::toString(x->scalar_type()) +
+                            ", expected " + c10::toString(type));
+            if (x->sizes() != at::IntArrayRef({t, c.heads, c.dim}))
+                value_error(std::string(name) + " has shape " + text(x->sizes()) + ", expected " +
+                            text({t, c.heads, c.dim}));
+            if (x->device() != cache.dev)
+                value_error(std::string(name) + " is on " + x->device().str() + ", expected " +
+                            cache.dev.str());
+            if (t) rows_of_heads(*x, name, c.heads, c.dim);
+        }
+        const Tensor &slots = need(a[6], "slots", at::kInt, {t}, cache.dev);
+        check(moeop_kv_write(&c, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+                             code_of(type), ptr<int32_t>(slots), small(t, "k"),
+                             stream_of(cache.dev)));
+        Py_RETURN_NONE;
+    });
+}
+
+// (k of the cache, v, k_scales, v_scales, slots, dtype code)
+PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!counted(n, 6)) return nullptr;
+    const long code = PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    return guarded([&] {
+        const Cache cache(a);
+        const moeop_kv_cache &c = cache.c;
+        const Tensor &slots = tensor(a[4], "slots");
+        if (slots.dim() != 1)
+            value_error("slots has " + std::to_string(slots.dim()) + " dimensions, expected 1");
+        const int64_t t = slots.size(0);
+        need(slots, "slots", at::kInt, {t}, cache.dev);
+        small(t, "slots");
+        const Tensor k = fresh({t, c.heads, c.dim}, type_of(code), cache.dev),
+                     v = fresh({t, c.heads, c.dim}, type_of(code), cache.dev);
+        check(moeop_kv_read(&c, ptr<int32_t>(slots), (int)t, k.data_ptr(), v.data_ptr(), (int)code,
+                            stream_of(cache.dev)));
+        return Py_BuildValue("(NN)", wrapped(k), wrapped(v));
+    });
+}
+
+// (k of the cache, v, k_scales, v_scales, q, table, lengths, scale, window, workspace, out)
+PyObject *attend_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!counted(n, 11)) return nullptr;
+    const double scale = a[7] == Py_None ? 0.0 : PyFloat_AsDouble(a[7]);
+    const long window = PyLong_AsLong(a[8]);
+    if (PyErr_Occurred()) return nullptr;
+    return guarded([&] {
+        const Cache cache(a);
+        const moeop_kv_cache &k = cache.c;
+        const Tensor &q = tensor(a[4], "q");
+        if (q.dim() != 3 && q.dim() != 4)
+            value_error("q has " + std::to_string(q.dim()) + " dimensions, expected 3 or 4");
+        const bool four = q.dim() == 4;
+        const ScalarType type = q.scalar_type();
+        if (type != at::kBFloat16 && type != at::kHalf)
+            value_error(std::string("q has dtype ") + c10::toString(type) +
+                        ", expected bfloat16 or float16");
+        const int64_t batch = q.size(0), rows = four ? q.size(1) : 1, heads = q.size(q.dim() - 2),
+                      dim = q.size(q.dim() - 1);
+        if (dim != k.dim)
+            value_error("q has " + std::to_string(dim) + " elements to a head, the cache " +
+                        std::to_string(k.dim));
+        if (q.device() != cache.dev)
+            value_error("q is on " + q.device().str() + ", expected " + cache.dev.str());
+        if (q.numel()) rows_of_heads(q, "q", heads, dim);
+        const Tensor &table = tensor(a[5], "table");
+        if (table.dim() != 2)
+            value_error("table has " + std::to_string(table.dim()) + " dimensions, expected 2");
+        need(table, "table", at::kInt, {batch, table.size(1)}, cache.dev, true);
+        const Tensor &lengths = need(a[6], "lengths", at::kInt, {batch}, cache.dev);
+        const Tensor out = a[10] == Py_None ? fresh(q.sizes(), type, cache.dev)
+                                            : need(a[10], "out", type, q.sizes(), cache.dev);
+        const moeop_attend_config c{small(batch, "q"), small(rows, "q"), small(heads, "q"),
+                                    small(table.size(1), "table"), small(window, "window"),
+                                    a[7] == Py_None ? 1.f / std::sqrt((float)dim) : (float)scale,
+                                    code_of(type)};
+        Tensor ws;
+        if (a[9] == Py_None) {
+            const size_t bytes =
+                moeop_attend_workspace_size(c.batch, c.rows, c.q_heads, k.heads, k.dim);
+            if (!bytes) throw Status{MOE_ERR_INVALID_ARG};
+            ws = fresh({(int64_t)bytes}, at::kByte, cache.dev);
+            check(moeop_attend_workspace_init(ws.data_ptr(), bytes, stream_of(cache.dev)));
+        } else {
+            ws = tensor(a[9], "the workspace");
+            if (ws.device() != cache.dev)
+                value_error("the workspace is on " + ws.device().str() + ", expected " +
+                            cache.dev.str());
+        }
+        check(moeop_attend_paged(&c, &k, q.data_ptr(), q.stride(0), four ? q.stride(1) : 0,
+                                 ptr<int32_t>(table), row_stride(table), ptr<int32_t>(lengths),
+                                 out.data_ptr(), ws.data_ptr(), (size_t)ws.numel(),
+                                 stream_of(cache.dev)));
+        return wrapped(out);
+    });
+}
+
+// Probabilities [batch][rows][vocab]: one stride from row to row, through the batch.
+int64_t prob_stride(const Tensor &t, const char *name, int64_t batch, int64_t rows, int64_t vocab,
+                    const at::Device &dev) {
+    const auto n = [&] { return std::string(name); };
+    if (t.scalar_type() != at::kFloat)
+        value_error(n() + " has dtype " + c10::toString(t.scalar_type()) + ", expected Float");
+    if (t.sizes() != at::IntArrayRef({batch, rows, vocab}))
+        value_error(n() + " has shape " + text(t.sizes()) + ", expected " +
+                    text({batch, rows, vocab}));
+    if (t.device() != dev)
+        value_error(n() + " is on " + t.device().str() + ", expected " + dev.str());
+    if (!t.numel()) return vocab;
+    const int64_t stride = rows > 1 ? t.stride(1) : batch > 1 ? t.stride(0) : vocab;
+    if ((vocab > 1 && t.stride(2) != 1) ||
+        (rows > 1 && batch > 1 && t.stride(0) != rows * stride))
+        value_error(n() + " must have contiguous rows at one stride");
+    return stride;
+}
+
+// (draft, target, accept_u, sample_u, draft_probs)
+PyObject *verify_draft(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!counted(n, 5)) return nullptr;
+    return guarded([&] {
+        const Tensor &target = first(a[1], "target_probs", 3), &draft = tensor(a[0], "draft");
+        const at::Device dev = target.device();
+        const int64_t batch = target.size(0), rows = target.size(1), vocab = target.size(2);
+        if (rows < 1) value_error("target_probs has no rows");
+        need(draft, "draft", at::kInt, {batch, rows - 1}, dev);
+        const Tensor &accept = need(a[2], "accept_u", at::kFloat, {batch, rows - 1}, dev),
+                     &sample = need(a[3], "sample_u", at::kFloat, {batch}, dev);
+        moeop_verify_config c{small(batch, "target_probs"), small(rows - 1, "target_probs"),
+                              small(vocab, "target_probs"),
+                              prob_stride(target, "target_probs", batch, rows, vocab, dev), vocab};
+        const float *probs = nullptr;
+        if (a[4] != Py_None) {
+            const Tensor &t = tensor(a[4], "draft_probs");
+            c.draft_stride = prob_stride(t, "draft_probs", batch, rows - 1, vocab, dev);
+            probs = ptr<float>(t);
+        }
+        const Tensor tokens = fresh({batch, rows}, at::kInt, dev),
+                     accepted = fresh({batch}, at::kInt, dev);
+        check(moeop_verify_draft(&c, ptr<int32_t>(draft), ptr<float>(target), probs,
+                                 ptr<float>(accept), ptr<float>(sample), ptr<int32_t>(tokens),
+                                 ptr<int32_t>(accepted), stream_of(dev)));
+        return Py_BuildValue("(NN)", wrapped(tokens), wrapped(accepted));
+    });
+}
+
 PyObject *set_error_class(PyObject *, PyObject *cls) {
     Py_INCREF(cls);
     Py_XDECREF(g_moe_error);
@@ -285,6 +508,7 @@ PyObject *set_error_class(PyObject *, PyObject *cls) {
 
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(rms_norm), FAST(route_topk), FAST(matmul_fp8), FAST(experts_fp8),
+                           FAST(kv_write), FAST(kv_read), FAST(attend_paged), FAST(verify_draft),
                            {"set_error_class", set_error_class, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_moe_ops", nullptr, -1, g_methods,

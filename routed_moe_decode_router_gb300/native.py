@@ -22,7 +22,7 @@ MOE_SCORING_SOFTMAX, MOE_SCORING_SIGMOID = 0, 1
 MOE_ROUTER_BF16, MOE_ROUTER_NVFP4 = 0, 1
 MOE_EXPERT_NVFP4, MOE_EXPERT_FP8, MOE_EXPERT_BF16 = 0, 1, 2
 MOEOP_BLOCK = 128
-MOEOP_BF16, MOEOP_FP16, MOEOP_FP32 = 0, 1, 2
+MOEOP_BF16, MOEOP_FP16, MOEOP_FP32, MOEOP_E4M3 = 0, 1, 2, 3
 MOEOP_GROUP_MAX, MOEOP_GROUP_TOP2 = 0, 1
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -94,14 +94,33 @@ class ExpertsWeights(C.Structure):
                 ("down_scales", C.c_void_p)]
 
 
+class KvCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scales", C.c_void_p),
+                ("v_scales", C.c_void_p), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("k_scales_stride", C.c_int64), ("v_scales_stride", C.c_int64),
+                ("pages", C.c_int), ("heads", C.c_int), ("page", C.c_int), ("dim", C.c_int),
+                ("type", C.c_int)]
+
+
+class AttendConfig(C.Structure):
+    _fields_ = [("batch", C.c_int), ("rows", C.c_int), ("q_heads", C.c_int), ("width", C.c_int),
+                ("window", C.c_int), ("scale", C.c_float), ("dtype", C.c_int)]
+
+
+class VerifyConfig(C.Structure):
+    _fields_ = [("batch", C.c_int), ("drafts", C.c_int), ("vocab", C.c_int),
+                ("target_stride", C.c_int64), ("draft_stride", C.c_int64)]
+
+
 EXPORTS = ("moe_abi_version", "moe_last_error", "moe_check_config",
            "moe_workspace_size", "moe_workspace_init", "moe_route", "moe_union",
            "moe_forward", "moe_forward_timed", "moe_read_routing",
            "moe_read_device_status", "moe_forward_static", "moe_nvfp4_to_t_layout")
 
 OPS_EXPORTS = ("moeop_rms_norm", "moeop_route_topk", "moeop_matmul_fp8",
-               "moeop_experts_workspace_size", "moeop_experts_fp8",
-               "moeop_read_device_status")
+               "moeop_experts_workspace_size", "moeop_experts_fp8", "moeop_kv_write",
+               "moeop_kv_read", "moeop_attend_workspace_size", "moeop_attend_workspace_init",
+               "moeop_attend_paged", "moeop_verify_draft", "moeop_read_device_status")
 
 _lib = None
 _lock = threading.Lock()
@@ -152,6 +171,14 @@ def lib():
         L.moeop_experts_workspace_size.argtypes = [C.POINTER(ExpertsConfig), i]
         L.moeop_experts_fp8.argtypes = [C.POINTER(ExpertsConfig), C.POINTER(ExpertsWeights), vp,
                                         vp, vp, vp, vp, vp, i, vp, sz, vp]
+        L.moeop_kv_write.argtypes = [C.POINTER(KvCache), vp, i64, vp, i64, i, vp, i, vp]
+        L.moeop_kv_read.argtypes = [C.POINTER(KvCache), vp, i, vp, vp, i, vp]
+        L.moeop_attend_workspace_size.restype = sz
+        L.moeop_attend_workspace_size.argtypes = [i, i, i, i, i]
+        L.moeop_attend_workspace_init.argtypes = [vp, sz, vp]
+        L.moeop_attend_paged.argtypes = [C.POINTER(AttendConfig), C.POINTER(KvCache), vp, i64, i64,
+                                         vp, i64, vp, vp, vp, sz, vp]
+        L.moeop_verify_draft.argtypes = [C.POINTER(VerifyConfig), vp, vp, vp, vp, vp, vp, vp, vp]
         L.moeop_read_device_status.argtypes = [C.POINTER(C.c_int), vp]
         for name in EXPORTS[2:] + OPS_EXPORTS:
             if not name.endswith("workspace_size"):
@@ -277,6 +304,41 @@ def moeop_experts_fp8(cfg, w, q: int, scales: int, ids: int, wts: int, addend: i
                       rows: int, ws: int, ws_bytes: int, stream: int = 0):
     _check(lib().moeop_experts_fp8(C.byref(cfg), C.byref(w), q, scales, ids, wts, addend, out,
                                    rows, ws, ws_bytes, stream))
+
+
+def moeop_kv_write(cache: KvCache, k: int, k_stride: int, v: int, v_stride: int, dtype: int,
+                   slots: int, tokens: int, stream: int = 0):
+    _check(lib().moeop_kv_write(C.byref(cache), k, k_stride, v, v_stride, dtype, slots, tokens,
+                                stream))
+
+
+def moeop_kv_read(cache: KvCache, slots: int, tokens: int, k: int, v: int, dtype: int,
+                  stream: int = 0):
+    _check(lib().moeop_kv_read(C.byref(cache), slots, tokens, k, v, dtype, stream))
+
+
+def moeop_attend_workspace_size(batch: int, rows: int, q_heads: int, heads: int, dim: int) -> int:
+    n = lib().moeop_attend_workspace_size(batch, rows, q_heads, heads, dim)
+    if n == 0:
+        raise MoeError(1, lib().moe_last_error().decode())
+    return n
+
+
+def moeop_attend_workspace_init(ws: int, ws_bytes: int, stream: int = 0):
+    _check(lib().moeop_attend_workspace_init(ws, ws_bytes, stream))
+
+
+def moeop_attend_paged(cfg: AttendConfig, cache: KvCache, q: int, q_batch_stride: int,
+                       q_row_stride: int, table: int, table_stride: int, lengths: int, out: int,
+                       ws: int, ws_bytes: int, stream: int = 0):
+    _check(lib().moeop_attend_paged(C.byref(cfg), C.byref(cache), q, q_batch_stride, q_row_stride,
+                                    table, table_stride, lengths, out, ws, ws_bytes, stream))
+
+
+def moeop_verify_draft(cfg: VerifyConfig, draft: int, target: int, draft_probs: int, accept_u: int,
+                       sample_u: int, tokens: int, accepted: int, stream: int = 0):
+    _check(lib().moeop_verify_draft(C.byref(cfg), draft, target, draft_probs, accept_u, sample_u,
+                                    tokens, accepted, stream))
 
 
 def moeop_read_device_status(stream: int = 0) -> int:

@@ -1,6 +1,8 @@
 """PyTorch-facing calls of the FP8 layer operators (include/moe_ops.h): norm
 with an FP8 output, grouped expert routing, the block-scaled FP8 product and
-the routed experts, for any number of token rows.
+the routed experts, for any number of token rows; and of a decoding step's
+others: the paged cache of keys and values, attention over it, and the
+verification of drafted tokens.
 
 Like layer.py it only marshals: tensors are checked by their attributes
 before any pointer reaches the library, every step runs in the CUDA library
@@ -149,6 +151,113 @@ def experts_fp8(q: torch.Tensor, scales: torch.Tensor, ids: torch.Tensor, wts: t
     return (_ext or _load()).experts_fp8(
         q, scales, ids, wts, gate, gate_scales, up, up_scales, down, down_scales,
         None if ws is None else ws.buf, addend, out)
+
+
+class KvCache(NamedTuple):
+    """A paged cache of keys and values: k, v [pages, heads, page, dim] of bf16,
+    fp16 or e4m3, with e4m3 one float32 scale per head and place,
+    [pages, heads, page].  Contiguous but for the stride of the pages, so that
+    keys and values may lie in one tensor.  page: a multiple of 16 up to 1024;
+    dim: 64, 128 or 256.  A slot is a place in it: page number * page + place."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
+
+
+def new_kv_cache(pages: int, heads: int, page: int, dim: int, dtype: torch.dtype = F8,
+                 device="cuda") -> KvCache:
+    """An empty cache (zeros) in e4m3, bf16 or fp16."""
+    k, v = (torch.zeros(pages, heads, page, dim, dtype=dtype, device=device) for _ in range(2))
+    if dtype != F8:
+        return KvCache(k, v)
+    return KvCache(k, v, *(torch.zeros(pages, heads, page, device=device) for _ in range(2)))
+
+
+def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+             stream=None) -> None:
+    """Write the keys and values [T, heads, dim] of T tokens to their slots
+    (int32 [T]; one outside the cache, as -1, is passed over).  An e4m3 cache
+    takes bf16, fp16 or fp32 and quantises: scale = max(amax of the dim, 1e-30) /
+    448; a cache of 16 bits takes its own type.  Tokens may be strided.  The slots
+    of a call are distinct: a slot given twice holds nothing defined."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_write(cache, k, v, slots)
+    return (_ext or _load()).kv_write(*cache, k, v, slots)
+
+
+def kv_read(cache: KvCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+            stream=None):
+    """(k, v) [T, heads, dim] in dtype (bf16, fp16 or fp32) of the slots (int32
+    [T]; one outside the cache gives zeros)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_read(cache, slots, dtype)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("dtype is %s, expected bfloat16, float16 or float32" % dtype)
+    return (_ext or _load()).kv_read(*cache, slots, code)
+
+
+class AttendWorkspace:
+    """Caller-owned scratch of attend_paged for calls of these rows, heads and
+    dim and up to `batch` sequences (initialised here, on the current stream).
+    Calls that overlap on the GPU need one each."""
+
+    def __init__(self, batch: int, rows: int, q_heads: int, heads: int, dim: int,
+                 device="cuda"):
+        self.nbytes = N.moeop_attend_workspace_size(batch, rows, q_heads, heads, dim)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+
+    @property
+    def ptr(self) -> int:
+        return self.buf.data_ptr()
+
+
+def attend_paged(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lengths: torch.Tensor,
+                 scale: Optional[float] = None, window: int = 0,
+                 ws: Optional[AttendWorkspace] = None, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Attention of the last R tokens of each sequence over its cached tokens,
+    their own among them (write them first).
+
+    q [B, R, q_heads, dim] (or [B, q_heads, dim], R = 1) in bf16 or fp16, the
+    cache's own type where that is one of 16 bits; B and R may be strided.  table
+    [B, W] int32: the pages of each sequence in order; lengths [B] int32: its
+    tokens.  Row r is at position length - R + r and sees the positions up to its
+    own, with a window the last `window` of them.  A page number outside the cache
+    (as -1) takes its tokens out; a row that sees nothing is zero, so a free place
+    of a batch has length 0, and a sequence with fewer new tokens has them in its
+    last rows.  scale: 1 / sqrt(dim) if not given.  Returns q's shape and type."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attend_paged(q, cache, table, lengths, scale, window, ws, out)
+    return (_ext or _load()).attend_paged(*cache, q, table, lengths, scale, window,
+                                          None if ws is None else ws.buf, out)
+
+
+class VerifyOut(NamedTuple):
+    tokens: torch.Tensor     # int32 [B, K + 1]: the drafts that stay, one more token, then -1
+    accepted: torch.Tensor   # int32 [B]: how many drafts stay
+
+
+def verify_draft(draft: torch.Tensor, target_probs: torch.Tensor, accept_u: torch.Tensor,
+                 sample_u: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                 stream=None) -> VerifyOut:
+    """Which of the K drafted tokens [B, K] (int32; a negative one ends a
+    sequence's drafts) stay, and the token after them, so that what comes out is
+    distributed as the target.  target_probs [B, K + 1, V], draft_probs [B, K, V]
+    float32 (none: the drafts are certain); accept_u [B, K] and sample_u [B]:
+    uniform float32 numbers in [0, 1).  Draft i stays while accept_u * draft_probs <
+    target_probs at it; the next token is drawn from max(target - draft, 0) where a
+    draft is refused, else from the target, as the lowest id whose running sum
+    exceeds sample_u times the whole (-1 where no probability is positive)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_draft(draft, target_probs, accept_u, sample_u, draft_probs)
+    return VerifyOut(*(_ext or _load()).verify_draft(draft, target_probs, accept_u, sample_u,
+                                                     draft_probs))
 
 
 def device_status(stream=None) -> int:
