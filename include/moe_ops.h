@@ -130,7 +130,7 @@ MOE_API moe_status moeop_experts_fp8(const moeop_experts_config *cfg,
  * each head and place (k_scales + p * k_scales_stride + h * page + i); value =
  * code * scale.  A slot is a place in the cache: page number * page + i.  The
  * strides are in elements, from one page to the next.
- * k, v and their strides 16-byte aligned; scales NULL unless e4m3. */
+ * All four arrays and their strides 16-byte aligned; scales NULL unless e4m3. */
 typedef struct moeop_kv_cache {
     void *k, *v;
     float *k_scales, *v_scales;

@@ -96,6 +96,12 @@ cudaError_t allow_few_smem();
 
 cudaError_t status_word(uint32_t **p);  // the current device's status word
 
+struct alignas(64) TensorMap {
+    uint64_t v[16];
+};
+cudaError_t make_cache_map(TensorMap *m, const void *p, int row_bytes, int64_t rows,
+                           int64_t page_bytes, int64_t pages);
+
 // Quotients of numbers below 2^31 by one that many share: a multiplication
 // (T. Granlund and P. Montgomery, "Division by invariant integers using
 // multiplication", 1994).
@@ -152,13 +158,15 @@ struct AttendParams {
     int batch, rows, group, width, window, dtype;
     float scale_log2;          // of the scores, times log2(e)
     int blocks;                // of query rows of a key/value head
+    Divisor by_group, by_page, by_grid;  // by_grid: thread blocks for a block of query rows
     uint32_t *counters;        // kAttendCounters, zero between calls
     float *parts;              // sums of a warp's or thread block's share of an item
+    uint32_t *status;
 };
 // Query rows (row, head of the group) that a thread block takes together.
 constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 16; }
 // Thread blocks for each block of query rows: together one for every SM.
-constexpr int kAttendSms = 152, kAttendCounters = 256, kAttendMaxBatch = 2048;
+constexpr int kAttendSms = 152, kAttendCounters = 3 * 256, kAttendMaxBatch = 2048;
 constexpr int attend_grid(int blocks) { return blocks < kAttendSms ? kAttendSms / blocks : 1; }
 // Workspace of moeop_attend_paged: the counters, in every shape the same, then a
 // partial sum for each warp (up to 16 in a thread block, 8 where dim is 256) and

@@ -96,7 +96,7 @@ moe_status check_cache(const moeop_kv_cache *c) {
     if (bad(c->k, 16) || bad(c->v, 16))
         return fail(MOE_ERR_INVALID_ARG, "the cache's k and v must be 16-byte aligned and not NULL");
     for (const int64_t stride : {c->k_stride, c->v_stride})
-        if (stride < places * c->dim || stride * es % 16 || stride >= (1LL << 40))
+        if (stride < places * c->dim || stride * es % 16 || stride * es >= (1LL << 40))
             return fail(MOE_ERR_INVALID_ARG,
                         "the cache's strides must be at least heads * page * dim and multiples of "
                         "16 bytes");
@@ -108,12 +108,14 @@ moe_status check_cache(const moeop_kv_cache *c) {
             return fail(MOE_ERR_INVALID_ARG, "a cache of 16 bits has no scales");
         return MOE_OK;
     }
-    if (bad(c->k_scales, 4) || bad(c->v_scales, 4))
-        return fail(MOE_ERR_INVALID_ARG, "k_scales or v_scales is NULL or misaligned");
+    if (bad(c->k_scales, 16) || bad(c->v_scales, 16))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "k_scales and v_scales must be 16-byte aligned and not NULL");
     for (const int64_t stride : {c->k_scales_stride, c->v_scales_stride})
-        if (stride < places || stride >= (1LL << 40))
+        if (stride < places || stride % 4 || stride >= (1LL << 38))
             return fail(MOE_ERR_INVALID_ARG,
-                        "the strides of the cache's scales must be at least heads * page");
+                        "the strides of the cache's scales must be at least heads * page and "
+                        "multiples of 4");
     const int64_t ksb = c->k_scales_stride * 4, vsb = c->v_scales_stride * 4, ns = places * 4;
     if (!apart(c->k_scales, ksb, ns, c->v_scales, vsb, ns, c->pages) ||
         !apart(c->k, kb, n, c->k_scales, ksb, ns, c->pages) ||
@@ -481,6 +483,7 @@ moe_status moeop_attend_paged(const moeop_attend_config *cfg, const moeop_kv_cac
     p.scale_log2 = (float)(c.scale * 1.4426950408889634);
     const int block = attend_block(cache->dim, m);
     p.blocks = (m + block - 1) / block;
+    p.by_group = Divisor(group), p.by_page = Divisor(cache->page);
     p.counters = static_cast<uint32_t *>(ws);
     p.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + L.parts);
     const auto launch = cache->type == MOEOP_E4M3  ? launch_attend_f8

@@ -7,27 +7,28 @@
 //
 // Bound by memory: a token's key and value are read once for all query rows of
 // their head (rows x group of them), 4 dim operations a row.  What keeps the
-// memory busy is bytes under way, so every warp has a ring of its own, filled by
-// 16-byte cp.async two or more tiles ahead, and no warp waits for another.
+// memory busy is bytes under way, and what may keep it waiting is instructions
+// (a tile of e4m3 has 170 cycles of its SM at the memory's rate), so every warp has
+// a ring of its own, filled by TMA two or more tiles ahead at a few instructions a
+// tile, and no warp waits for another.
 //
 // - Work.  A sequence's tokens for one key/value head are an item, cut into
 //   tiles of 16 tokens (a tile never leaves its page).  The tiles of all items
 //   in a row are dealt to the warps of the grid in equal contiguous shares, so
 //   lengths may differ as they like, one long sequence fills the GPU as well as
 //   many short ones, and the ring runs on from one item into the next.
-// - Product.  The 16 tokens are the rows of mma.sync (m16n8k16), the query rows
-//   its 8 columns: S = K Q^T, then O^T = V^T P^T with the d's as rows.  So a group
-//   of up to 8 rows pays for 8, not 16.  Which inputs of a sum stand in which
-//   place of a fragment is free as long as both operands agree: a lane's place
-//   for the d's of K and the d's of V is what 16 contiguous bytes of a row hold,
-//   so fragments are cut from what the lane itself copied, without ldmatrix and
-//   without a bank conflict, and e4m3 pairs become f16 pairs by one conversion.
-//   (tcgen05 would want 64 rows or more: here there are 8 or 16, and the tensor
-//   cores are idle most of the time as it is.)
-// - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo.
-// - e4m3: the scale of a key multiplies its score, that of a value its weight.
-//   A weight is exp(s_j - m) vs_j, so the sums O have a running maximum of their
-//   own, of s_j + log vs_j, and keep the range of f16 whatever the scales are.
+// - Product.  The 16 tokens are the rows of mma.sync, the query rows its 8 columns:
+//   S = K Q^T, then O^T = V^T P^T with the d's as rows.  So a group of up to 8
+//   rows pays for 8, not 16.  (tcgen05 would want 64 rows or more: here there are
+//   8 or 16, and the tensor cores are idle most of the time as it is.)  Fragments
+//   come by ldmatrix from the swizzled tiles, V transposed on the way.
+// - e4m3 is widened to f16, exactly.  A key's scale multiplies its score, a value's
+//   its weight: weights are exp(s_j - m) vs_j, so the sums O have a running maximum
+//   of their own, of s_j + log vs_j, and keep the range of f16 whatever the scales.
+//   (mma.sync on e4m3 itself, Q in two e4m3 numbers, takes 80 instructions a tile more.)
+// - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo, but for
+//   e4m3 with bf16 outputs: one f16 number is 2^-12 off, a rounding of the output
+//   up to 2^-9.
 // - Maxima are raised only where a score exceeds them by 2^8, so that most tiles
 //   need one vote and no reduction.
 // - Join.  A warp's share of an item goes to shared memory (its last item) or to
@@ -39,59 +40,42 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "moe_device.cuh"
 #include "moeop.cuh"
+#include "moeop_tc.cuh"
 
 namespace moe {
 namespace op {
 namespace attend {
 
 constexpr int kTile = 16;        // tokens
-constexpr int kMaxSmem = 227 << 10;
 constexpr float kSlack = 8.f;    // what a score may exceed the running maximum by (log2)
 
 // TYPE of the cache, D: dim, NT: groups of 8 query rows.
 // A tile is 32 rows of D elements; warps x stages of them fill shared memory.
-// Warps as the registers allow (Q: NT D / 8, O: NT D / 4 a thread).
+// Warps as the registers allow (O alone: NT D / 4 a thread).
 template <int TYPE, int D, int NT>
 struct Shape {
     static constexpr bool F8 = TYPE == MOEOP_E4M3;
     static constexpr int kSize = F8 ? 1 : 2;
     static constexpr int kRow = D * kSize;                // bytes of a row
-    static constexpr int E = 16 / kSize;                  // elements of 16 bytes
-    static constexpr int kStage = 2 * kTile * kRow + (F8 ? 128 : 0);
-    static constexpr int kWarps = kRow == 512 ? 4 : kRow == 256 ? 8 : NT * D > 128 ? 12 : 16;
-    static constexpr int kStages = kRow == 64 ? 5 : NT * D > 128 && kRow == 128 ? 4 : 3;
+    static constexpr int kHalf = kTile * kRow;            // the keys of a tile
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kWarps = kRow == 512 ? 4 : kRow == 256 || NT * D > 128 ? 8 : 12;
+    static constexpr int kStages = kRow == 64 ? 6 : kRow == 128 ? (kWarps == 8 ? 6 : 4) : 3;
     static constexpr int M = 8 * NT;
-    // a partial sum: m, l and the sums' own maximum of each row, then O
+    // a partial sum: m, l and the sums' own maximum of each row, then O^T
     static constexpr int kStats = 3 * M, kPart = kStats + M * D;
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int KC = kRow / 64;                  // 16-byte pieces of a key per lane
-    static constexpr int VB = kRow / 8;                   // bytes of a value per lane
-    static_assert(kPart * 4 <= kStages * kStage, "a partial sum lies in its warp's ring");
-    static_assert(kStage % 16 == 0, "");
+    static constexpr int smem(int batch) { return 1024 + kRing + (2 * batch + 1) * 4; }
+    static constexpr int kSteps = kRow / 32;              // 32 bytes of a row: an MMA's
+    static_assert(M * D * 4 <= kStages * kStage, "a share's sums lie in its warp's ring");
+    static_assert(kWarps <= 16, "two shares of each warp: a lane for each");
+    static_assert(kStage % 1024 == 0, "the swizzle's period");
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 8 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 4 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -107,6 +91,19 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
+template <bool TRANS>
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr)
+                     : "memory");
+}
 template <int TYPE>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (TYPE == MOEOP_BF16)
@@ -114,78 +111,80 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     else
         mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
 }
-// Two numbers as 16-bit pairs hi and lo: hi + lo is within 2^-16 (bf16) or 2^-22
-// (f16) of them.
 template <int TYPE>
-__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
-    if (TYPE == MOEOP_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        const __nv_bfloat162 l =
-            __floats2bfloat162_rn(x - __low2float(h), y - __high2float(h));
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    } else {
-        const __half2 h = __floats2half2_rn(x, y);
-        const __half2 l = __floats2half2_rn(x - __low2float(h), y - __high2float(h));
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    }
+__device__ __forceinline__ uint32_t pair(float x, float y) {
+    if (TYPE == MOEOP_BF16) return (uint32_t)f2bf16_rn(x) | (uint32_t)f2bf16_rn(y) << 16;
+    return pack_f16x2(x, y);
 }
-// Some element of a word of the cache is an infinity or NaN.
+template <int TYPE>
+__device__ __forceinline__ float2 unpair(uint32_t v) {
+    if (TYPE == MOEOP_BF16) return make_float2(bf16_lo(v), bf16_hi(v));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+// Some element of a pair is an infinity or NaN.
 template <int TYPE>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-    if (TYPE == MOEOP_E4M3) return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
     if (TYPE == MOEOP_BF16) return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
     return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+__device__ __forceinline__ float inverse(float x) {    // within 2^-23
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 // exp2(a - b), 0 where a is -inf.
 __device__ __forceinline__ float ratio(float a, float b) {
     return a == -INFINITY ? 0.f : ex2(a - b);
 }
 
-// The tiles of a batch in a row: sequence by sequence, head by head.
-struct Tiles {
-    const int *first;    // [batch + 1] of a sequence, divided by heads
-    const int *length;   // [batch]
-    int heads;
-    // the item that tile x belongs to
-    __device__ __forceinline__ int sequence(int64_t x, int batch) const {
+// An item among the tiles of a batch: sequence by sequence, head by head.
+struct alignas(16) Item {
+    int b, h, tiles;      // sequence, head, tiles of the item
+    int start;            // its first tile among all
+    Item() = default;
+    // the item of tile x; first: tiles of the sequences before each, for one head
+    __device__ __forceinline__ Item(const int *first, int heads, int batch, int x) {
         int lo = 0, hi = batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if ((int64_t)first[mid] * heads <= x) lo = mid;
+            if (first[mid] * heads <= x) lo = mid;
             else hi = mid;
         }
-        return lo;
+        b = lo;
+        tiles = first[lo + 1] - first[lo];
+        const int base = first[lo] * heads;
+        // the quotient is below 1024: one off at most
+        h = (int)((float)(x - base) / (float)tiles);
+        if (h * tiles > x - base) --h;
+        if ((h + 1) * tiles <= x - base) ++h;
+        start = base + h * tiles;
     }
-    __device__ __forceinline__ int count(int b) const { return first[b + 1] - first[b]; }
-};
-struct Item {
-    int b, h, tiles;      // sequence, head, tiles of the item
-    int64_t start;        // its first tile among all
-    __device__ __forceinline__ Item(const Tiles &t, int64_t x, int batch) {
-        b = t.sequence(x, batch);
-        tiles = t.count(b);
-        const int64_t base = (int64_t)t.first[b] * t.heads;
-        h = (int)(x - base) / tiles;
-        start = base + (int64_t)h * tiles;
-    }
-    __device__ __forceinline__ void next(const Tiles &t) {
+    __device__ __forceinline__ void next(const int *first, int heads) {
         start += tiles;
-        if (++h == t.heads) h = 0, ++b, tiles = t.count(b);
+        if (++h == heads) h = 0, ++b, tiles = first[b + 1] - first[b];
     }
+    __device__ __forceinline__ int end() const { return start + tiles; }
 };
-// Equal shares of `tiles` tiles for `workers` warps.
+// Where the share of thread block c of n begins: equal shares of `tiles`.
 struct Shares {
-    int64_t tiles;
-    int workers;
-    __device__ __forceinline__ int64_t begin(int w) const {
-        return w >= workers ? tiles : tiles * w / workers;
-    }
-    __device__ __forceinline__ int owner(int64_t x) const {
-        return (int)(((x + 1) * workers - 1) / tiles);
+    int each, more;       // the first `more` blocks take one tile more
+    __device__ __forceinline__ Shares(int tiles, const Divisor &n)
+        : each((int)n.over(tiles)), more(tiles - each * (int)n.d) {}
+    __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(int x) const {
+        const int big = more * (each + 1);
+        return x < big ? x / (each + 1) : more + (x - big) / max(each, 1);
     }
 };
+// An item of up to kWhole tiles is not cut between blocks: the cut goes to its
+// nearer end.  To join what two blocks have of an item takes 4 us, in which a block
+// reads some 40 tiles.
+constexpr int kWhole = 96;
+__device__ __forceinline__ int cut(const int *first, int heads, int batch, int tiles, int x) {
+    if (x <= 0 || x >= tiles) return min(x, tiles);
+    const Item i(first, heads, batch, x);
+    return i.tiles > kWhole ? x : x - i.start < i.end() - x ? i.start : i.end();
+}
 
 // First tile of a sequence of n tokens that some row sees (0 without a window).
 __device__ __forceinline__ int first_tile(const AttendParams &p, int n) {
@@ -194,26 +193,39 @@ __device__ __forceinline__ int first_tile(const AttendParams &p, int n) {
 
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
-    attend_kernel(const AttendParams p) {
+    attend_kernel(const __grid_constant__ TensorMap kmap, const __grid_constant__ TensorMap vmap,
+                  const AttendParams p) {
     using S = Shape<TYPE, D, NT>;
     constexpr bool F8 = S::F8;
-    constexpr int W = S::kWarps, E = S::E, KC = S::KC, VB = S::VB, M = S::M;
-    constexpr int kSteps = D / 16;              // of 16 inputs in Q K^T
-    extern __shared__ __align__(128) char smem[];
-    __shared__ int scan[32];
-    __shared__ int64_t starts[W + 1];
-    __shared__ int joins[2];
-    int *first = reinterpret_cast<int *>(smem + S::kRing);
-    int *length = first + p.batch + 1;
+    constexpr int W = S::kWarps, M = S::M, kStages = S::kStages, kSteps = S::kSteps;
+    extern __shared__ char raw[];
+    __shared__ uint64_t bars[W][kStages];
+    __shared__ int scan[W], joined[2];
+    // the shares of an item that a warp has and others too, in the order of their
+    // tiles: the item it did not begin (2 w) and its last one (2 w + 1)
+    __shared__ Item lasts[W], fronts[W];
+    __shared__ float stats[2 * W][3][M], worth_of[2 * W > 16 ? 2 * W : 16][M];
+    __shared__ int shares_of[W];         // which of its two shares a warp has, as bits
+    char *const smem = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    int *const first = reinterpret_cast<int *>(smem + S::kRing);
+    int *const length = first + p.batch + 1;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int g = lane / 4, t = lane % 4;
     const int mb = blockIdx.y;                  // block of query rows
     const int m_all = p.rows * p.group;
 
-    // Tiles of the sequences before each one
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars[warp][i], 1);
+        fence_mbar_init();
+        if (warp == W - 1) tma_prefetch_map(&kmap), tma_prefetch_map(&vmap);
+    }
+    // Tiles of the sequences before each one.  Up to 32 every warp counts them for
+    // itself (and all write the same): no barrier.
     int sum = 0;
+    const bool few = p.batch <= 32;
     for (int b0 = 0; b0 < p.batch; b0 += W * 32) {
-        const int b = b0 + threadIdx.x;
+        const int b = b0 + (few ? lane : threadIdx.x);
         int n = 0, c = 0;
         if (b < p.batch) {
             n = min(max(__ldg(p.lengths + b), 0), p.width * p.page);
@@ -226,29 +238,35 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             const int left = __shfl_up_sync(~0u, run, o);
             if (lane >= o) run += left;
         }
-        if (lane == 31) scan[warp] = run;
-        __syncthreads();
         int before = sum;
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) before += scan[w];
-            sum += scan[w];
+        if (few) {
+            sum = __shfl_sync(~0u, run, 31);
+        } else {
+            if (lane == 31) scan[warp] = run;
+            __syncthreads();
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) before += scan[w];
+                sum += scan[w];
+            }
         }
         if (b < p.batch) first[b] = before + run - c;
-        __syncthreads();
+        if (!few) __syncthreads();
     }
-    if (threadIdx.x == 0) first[p.batch] = sum;
-    Shares shares;
-    shares.tiles = (int64_t)sum * p.heads;
-    shares.workers = (int)min((int64_t)gridDim.x * W, shares.tiles);
-    if ((int64_t)blockIdx.x * W >= shares.workers) return;
-    if (threadIdx.x <= W) starts[threadIdx.x] = shares.begin(blockIdx.x * W + threadIdx.x);
-    __syncthreads();
-    const Tiles all{first, length, p.heads};
-    const int64_t begin = starts[warp], end = starts[warp + 1];
+    if (lane == 0) first[p.batch] = sum;
+    if (few) __syncwarp();
+    else __syncthreads();
+    const int tiles = sum * p.heads;
+    const Shares shares(tiles, p.by_grid);
+    const int cs = cut(first, p.heads, p.batch, tiles, shares.begin(blockIdx.x)),
+              ce = cut(first, p.heads, p.batch, tiles, shares.begin(blockIdx.x + 1));
+    if (cs >= ce) return;
+    // equal shares for the block's warps
+    const int used = min(W, ce - cs), warp_each = (ce - cs) / W, warp_more = (ce - cs) % W;
+    auto warp_begin = [&](int w) { return cs + w * warp_each + min(w, warp_more); };
+    const int begin = warp_begin(warp), end = warp_begin(warp + 1);
 
-    char *ring = smem + warp * (S::kStages * S::kStage);
+    char *const ring = smem + warp * (kStages * S::kStage);
     const uint32_t ring_addr = smem_u32(ring);
-    float *const tail = reinterpret_cast<float *>(ring);
     // sums of items begun by another warp: one for each warp of the grid, then two
     // for each block
     float *const heads_at =
@@ -256,154 +274,160 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     float *const blocks_at =
         p.parts + ((int64_t)mb * gridDim.x * (W + 2) + (int64_t)gridDim.x * W) * S::kPart;
 
+    int has = 0;
     if (begin < end) {
         // -------------------------------------------------------------------
-        // Loads: the item, tile and page that are next
+        // Q of an item, as it is
         // -------------------------------------------------------------------
-        Item li(all, begin, p.batch);
-        int64_t lx = begin;                        // next tile to load
-        int ltile, lpage, lplace;                  // in its sequence; of its page
-        const int page_tiles = p.page / kTile;
-        int lid = -1;                              // page number
-        uint32_t valid = 0;                        // bit 0: the tile loaded last is in the cache
-        auto seek = [&]() {
-            ltile = first_tile(p, length[li.b]) + (int)(lx - li.start);
-            lpage = ltile / page_tiles;
-            lplace = ltile - lpage * page_tiles;
-        };
-        auto look = [&]() {                        // the page number, a tile ahead of its use
-            lid = lpage < p.width ? __ldg(p.table + li.b * p.table_stride + lpage) : -1;
-        };
-        seek();
-        look();
-        int stage_in = 0;
-        auto load = [&]() {
-            if (lx < end) {
-                const bool in = (unsigned)lid < (unsigned)p.pages;
-                valid = valid << 1 | (in ? 1u : 0u);
-                if (in) {
-                    const int n = length[li.b], tok = ltile * kTile;
-                    const int from = p.window ? max(0, n - p.rows - p.window + 1) : 0;
-                    const uint32_t dst = ring_addr + stage_in * S::kStage;
-                    const int64_t place = (int64_t)li.h * p.page + lplace * kTile;
-                    const char *k = static_cast<const char *>(p.k) +
-                                    (lid * p.k_stride + place * D) * S::kSize;
-                    const char *v = static_cast<const char *>(p.v) +
-                                    (lid * p.v_stride + place * D) * S::kSize;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int at = g + 8 * r;
-                        const bool there = tok + at < n && tok + at >= from;
-#pragma unroll
-                        for (int c = 0; c < KC; ++c)
-                            copy16(dst + (r * KC + c) * 512 + lane * 16,
-                                   k + at * S::kRow + (c * 4 + t) * 16, there);
-                    }
-                    const uint32_t vdst = dst + kTile * S::kRow;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int at = 2 * t + (r & 1) + (r & 2) * 4;
-                        const bool there = tok + at < n && tok + at >= from;
-                        if constexpr (VB == 8) {
-                            copy8(vdst + r * 256 + lane * 8, v + at * S::kRow + g * 8, there);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < VB / 16; ++c)
-                                copy16(vdst + (r * (VB / 16) + c) * 512 + lane * 16,
-                                       v + at * S::kRow + (c * 8 + g) * 16, there);
-                        }
-                    }
-                    if constexpr (F8) {
-                        const int at = lane % 16;
-                        const float *s =
-                            lane < 16 ? p.k_scales + lid * p.k_scales_stride + place
-                                      : p.v_scales + lid * p.v_scales_stride + place;
-                        copy4(dst + 2 * kTile * S::kRow + lane * 4, s + at,
-                              tok + at < n && tok + at >= from);
-                    }
-                }
-                ++lx;
-                if (++stage_in == S::kStages) stage_in = 0;
-                if (lx < end) {
-                    if (lx == li.start + li.tiles) {
-                        li.next(all);
-                        seek();
-                    } else {
-                        ++ltile;
-                        if (++lplace == page_tiles) lplace = 0, ++lpage;
-                    }
-                    look();
-                }
-            } else {
-                valid <<= 1;
-            }
-            copies_end();
-        };
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) load();
-
-        // -------------------------------------------------------------------
-        // Items
-        // -------------------------------------------------------------------
-        int stage = 0;
-        Item it(all, begin, p.batch);
-        for (int64_t x = begin; x < end;) {
-            const int n = length[it.b];
-            const int s0 = (int)(x - it.start);
-            const int s1 = (int)(min(end, it.start + it.tiles) - it.start);
-            const int tile0 = first_tile(p, n);
-
-            // Q as the right operand; e4m3: in f16, a bf16 row by the power of two
-            // that brings it there (exact within 2^-28 of its largest)
-            uint32_t q[NT][kSteps][2];
-            float qmul[NT][2];
-            int pos[NT][2];                       // of the rows of this lane's columns
+        Item it(first, p.heads, p.batch, begin);
+        if (lane == 0) fronts[warp] = it;
+        uint32_t q[NT][D / 16][2];
+        auto load_q = [&]() {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int m = mb * M + j * 8 + g;
                 const uint16_t *row = nullptr;
                 if (m < m_all) {
-                    const int r = m / p.group;
+                    const int r = p.by_group.over(m);
                     row = static_cast<const uint16_t *>(p.q) + it.b * p.q_batch_stride +
-                          r * p.q_row_stride +
-                          ((int64_t)it.h * p.group + (m - r * p.group)) * D;
+                          r * p.q_row_stride + ((int64_t)it.h * p.group + (m - r * p.group)) * D;
                 }
 #pragma unroll
-                for (int c = 0; c < KC; ++c)
-#pragma unroll
-                    for (int e = 0; e < E / 8; ++e) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (row)
-                            w = __ldg(reinterpret_cast<const uint4 *>(row + (c * 4 + t) * E + e * 8));
-                        const int k = c * (E / 4) + e * 2;
+                for (int k = 0; k < D / 16; ++k) {
+                    if constexpr (F8) {
+                        // a lane's bytes of a key are four in a row: so its numbers of Q
+                        const uint2 w = row ? __ldg(reinterpret_cast<const uint2 *>(
+                                                  row + k * 16 + t * 4))
+                                            : make_uint2(0, 0);
                         q[j][k][0] = w.x, q[j][k][1] = w.y;
-                        q[j][k + 1][0] = w.z, q[j][k + 1][1] = w.w;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            q[j][k][i] = row ? __ldg(reinterpret_cast<const uint32_t *>(
+                                                   row + k * 16 + i * 8 + t * 2))
+                                             : 0u;
                     }
+                }
+            }
+        };
+        // -------------------------------------------------------------------
+        // Loads: the item, tile and page that are next
+        // -------------------------------------------------------------------
+        Item li = it;
+        const int page_tiles = p.page / kTile;
+        int lx = begin;                            // next tile to load
+        int lpage, lplace;                         // its page in the sequence, tile of the page
+        int page0 = 0, ids = -1;                   // lane i: the number of page page0 + i
+        uint32_t valid = 0;                        // bit 0: the tile loaded last is in the cache
+        bool lost = false;                         // a wait ran out
+        // a lane's scale of the next tile: of a key (lanes 0..15) or a value
+        const float *const scale_of = F8 ? (lane < 16 ? p.k_scales : p.v_scales) + lane % 16 : nullptr;
+        const int64_t scale_stride = lane < 16 ? p.k_scales_stride : p.v_scales_stride;
+        int64_t scale_at[kStages] = {};            // of the tiles under way, the last one first
+        auto pages = [&]() {                       // a tile ahead of their use
+            page0 = lpage;
+            ids = page0 + lane < p.width
+                      ? __ldg(p.table + li.b * p.table_stride + page0 + lane)
+                      : -1;
+        };
+        auto seek = [&]() {
+            const int tok = (first_tile(p, length[li.b]) + lx - li.start) * kTile;
+            lpage = p.by_page.over(tok);
+            lplace = tok - lpage * p.page;
+            pages();
+        };
+        seek();
+        load_q();
+        int stage_in = 0;
+        auto load = [&]() {
+            const int id = __shfl_sync(~0u, ids, lpage - page0);
+            const bool in = lx < end && !lost && (unsigned)id < (unsigned)p.pages;
+            valid = valid << 1 | (in ? 1u : 0u);
+#pragma unroll
+            for (int i = kStages - 1; i; --i) scale_at[i] = scale_at[i - 1];
+            if (in) {
+                const int place = uniform(li.h * p.page + lplace);
+                const uint32_t dst = uniform(ring_addr + stage_in * S::kStage);
+                if (F8) scale_at[0] = id * scale_stride + place;
+                uint64_t *bar = &bars[warp][stage_in];
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, S::kStage);
+                    tma_rows(dst, &kmap, place, id, bar);
+                    tma_rows(dst + S::kHalf, &vmap, place, id, bar);
+                }
+                __syncwarp();
+            }
+            if (++stage_in == kStages) stage_in = 0;
+            if (++lx < end) {
+                if (lx == li.end()) {
+                    li.next(first, p.heads);
+                    seek();
+                } else if ((lplace += kTile) == p.page) {
+                    lplace = 0;
+                    if (++lpage == page0 + 32) pages();
+                }
+            }
+        };
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) load();
+        float scale_next = F8 ? __ldg(scale_of + scale_at[kStages - 2]) : 0.f;
+
+        // where a lane's rows of the matrices lie in a tile: K and e4m3 V have the
+        // tokens 8..15 in the second matrix, V in 16 bits in the third
+        const int row_k = lane % 16, col_k = lane / 16;
+        const int row_v = F8 ? row_k : lane % 8 + lane / 16 * 8, col_v = F8 ? col_k : lane / 8 % 2;
+        auto offset = [](int row, int col) {
+            return S::kRow == 64 ? row * 64 + ((col ^ (row / 2 % 4)) * 16)
+                                 : row * 128 + ((col ^ (row % 8)) * 16);
+        };
+        const uint32_t off_k = offset(row_k, col_k), off_v = S::kHalf + offset(row_v, col_v);
+        // P as one number or two
+        const bool two = !F8 || p.dtype == MOEOP_FP16;
+
+        // -------------------------------------------------------------------
+        // Items
+        // -------------------------------------------------------------------
+        int stage = 0;
+        uint32_t phases = 0;
+        for (int x = begin; x < end;) {
+            const int n = length[it.b];
+            const int s0 = x - it.start, s1 = min(end, it.end()) - it.start;
+            const int tile0 = first_tile(p, n);
+
+            // Q as the right operand: with e4m3 a bf16 row goes to f16 by the power of
+            // two that brings it there, exact within 2^-28 of its largest
+            float qmul[NT][2];
+            int pos[NT][2];                       // of the rows of this lane's columns
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
                 float f = p.scale_log2;
                 if (F8 && p.dtype == MOEOP_BF16) {
-                    float big = 0.f;
+                    uint32_t most = 0;            // magnitudes order as whole numbers do
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k)
+                    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            big = fmaxf(big, fmaxf(fabsf(bf16_lo(q[j][k][i])),
-                                                   fabsf(bf16_hi(q[j][k][i]))));
-                    big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+                            most = __vmaxu2(most, q[j][k][i] & 0x7FFF7FFFu);
+                    most = __vmaxu2(most, __shfl_xor_sync(~0u, most, 1));
+                    most = __vmaxu2(most, __shfl_xor_sync(~0u, most, 2));
+                    const float big = __uint_as_float(max(most << 16, most & 0xFFFF0000u));
                     const int e = f16_block_exponent(big);
-                    const float up = exp2i(e);
+                    const float by = exp2i(e);
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k)
+                    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            q[j][k][i] = pack_f16x2(bf16_lo(q[j][k][i]) * up,
-                                                    bf16_hi(q[j][k][i]) * up);
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 v = unpair<MOEOP_BF16>(q[j][k][i]);
+                            q[j][k][i] = pack_f16x2(v.x * by, v.y * by);
+                        }
                     f *= exp2i(-e);
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     qmul[j][c] = F8 ? __shfl_sync(~0u, f, (2 * t + c) * 4) : f;
-                    pos[j][c] = n - p.rows + min(mb * M + j * 8 + 2 * t + c, m_all - 1) / p.group;
+                    pos[j][c] = p.rows == 1 ? n - 1
+                                            : n - p.rows + (int)p.by_group.over(min(
+                                                  mb * M + j * 8 + 2 * t + c, m_all - 1));
                 }
             }
 
@@ -421,65 +445,79 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             }
 
             for (int s = s0; s < s1; ++s) {
+                const float scale = scale_next;
                 load();
-                copies_wait<S::kStages - 1>();
-                __syncwarp();
-                const char *at = ring + stage * S::kStage;
-                if (++stage == S::kStages) stage = 0;
-                if (!(valid >> (S::kStages - 1) & 1)) continue;
+                if (F8) scale_next = __ldg(scale_of + scale_at[kStages - 2]);
+                const uint32_t at = ring_addr + stage * S::kStage;
+                const int now = stage;
+                if (++stage == kStages) stage = 0;
+                if (!(valid >> (kStages - 1) & 1)) continue;
+                if (!mbar_wait(&bars[warp][now], phases >> now & 1)) {
+                    lost = true;
+                    if (lane == 0) atomicExch(p.status, (uint32_t)MOE_DEV_WAIT_TIMEOUT);
+                }
+                phases ^= 1u << now;
                 const int tok = (tile0 + s) * kTile;
 
-                // scores
-                float x2[NT][4] = {}, y2[NT][4] = {};
+                // scores: two MMAs in turn, that none waits for the one before
+                float acc[NT][2][4] = {};
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const uint4 lo = *reinterpret_cast<const uint4 *>(at + c * 512 + lane * 16);
-                    const uint4 hi =
-                        *reinterpret_cast<const uint4 *>(at + (KC + c) * 512 + lane * 16);
-                    const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t r[4];
+                    load_matrices<false>(r, (at + off_k + k / 4 * 2048) ^ (k % 4 * 32));
+                    if constexpr (F8) {
 #pragma unroll
-                    for (int k = 0; k < E / 4; ++k) {
-                        uint32_t f[4];
-                        if (F8) {
-                            f[0] = e4m3x2_to_f16x2(a[k]), f[2] = e4m3x2_to_f16x2(a[k] >> 16);
-                            f[1] = e4m3x2_to_f16x2(b[k]), f[3] = e4m3x2_to_f16x2(b[k] >> 16);
-                        } else {
-                            f[0] = a[(2 * k) % 4], f[2] = a[(2 * k + 1) % 4];
-                            f[1] = b[(2 * k) % 4], f[3] = b[(2 * k + 1) % 4];
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t f[4] = {
+                                e4m3x2_to_f16x2(r[2 * h]), e4m3x2_to_f16x2(r[2 * h + 1]),
+                                e4m3x2_to_f16x2(r[2 * h] >> 16),
+                                e4m3x2_to_f16x2(r[2 * h + 1] >> 16)};
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma<TYPE>(acc[j][h], f, q[j][2 * k + h][0], q[j][2 * k + h][1]);
                         }
-                        // two sums in turn: an MMA need not wait for the one before
+                    } else {
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
-                            mma<TYPE>(k % 2 ? y2[j] : x2[j], f, q[j][c * (E / 4) + k][0],
-                                      q[j][c * (E / 4) + k][1]);
+                            mma<TYPE>(acc[j][k % 2], r, q[j][k][0], q[j][k][1]);
                     }
                 }
                 float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
                 if (F8) {
-                    const float *sc = reinterpret_cast<const float *>(at + 2 * kTile * S::kRow);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        ks[r] = sc[g + 8 * r], vs[r] = sc[16 + g + 8 * r];
+                        ks[r] = __shfl_sync(~0u, scale, g + 8 * r);
+                        vs[r] = __shfl_sync(~0u, scale, 16 + g + 8 * r);
                         lv[r] = fmaxf(lg2(vs[r]), -120.f);
                     }
                 }
                 const bool partly = tok + kTile - 1 > n - p.rows ||
                                     (p.window && tok < n - p.window);
+                float x2[NT][4];
                 bool up = false;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float v = (x2[j][c] + y2[j][c]) * (F8 ? ks[c / 2] * qmul[j][c % 2]
-                                                              : qmul[j][c % 2]);
-                        if (partly) {
+                        const float by = F8 ? ks[c / 2] * qmul[j][c % 2] : qmul[j][c % 2];
+                        x2[j][c] = (acc[j][0][c] + acc[j][1][c]) * by;
+                    }
+                if (partly) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
                             const int token = tok + g + c / 2 * 8, last = pos[j][c % 2];
                             if (token > last || (p.window && token <= last - p.window))
-                                v = -INFINITY;
+                                x2[j][c] = -INFINITY;
                         }
-                        x2[j][c] = v;
-                        up |= v > top[j][c % 2] + kSlack;
-                        if (F8) up |= v + lv[c / 2] > otop[j][c % 2] + kSlack;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        up |= x2[j][c] > top[j][c % 2] + kSlack;
+                        if (F8) up |= x2[j][c] + lv[c / 2] > otop[j][c % 2] + kSlack;
                     }
                 if (__any_sync(~0u, up)) {
 #pragma unroll
@@ -518,90 +556,85 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const float from = top[j][c % 2] == -INFINITY ? 0.f : top[j][c % 2];
-                        const float e = ex2(x2[j][c] - from);
-                        sums[j][c % 2] += e;
-                        w[c] = e;
-                        // a token that is not seen has e = 0 whatever its scale holds
-                        if (F8) w[c] = x2[j][c] == -INFINITY ? 0.f : e * vs[c / 2] * lift[j][c % 2];
+                        w[c] = ex2(x2[j][c] - from);
+                        sums[j][c % 2] += w[c];
+                        // a token that is not seen weighs 0 whatever its scale holds
+                        if (F8)
+                            w[c] = x2[j][c] == -INFINITY ? 0.f : w[c] * (vs[c / 2] * lift[j][c % 2]);
                     }
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        split<TYPE>(w[2 * r], w[2 * r + 1], ph[j][r], pl[j][r]);
-                        ph[j][r] = transposed(ph[j][r]);
-                        pl[j][r] = transposed(pl[j][r]);
+                        const uint32_t hi = pair<TYPE>(w[2 * r], w[2 * r + 1]);
+                        ph[j][r] = transposed(hi);
+                        if (two) {
+                            const float2 h = unpair<TYPE>(hi);
+                            pl[j][r] = transposed(pair<TYPE>(w[2 * r] - h.x, w[2 * r + 1] - h.y));
+                        }
                     }
                 }
 
-                // sums of the values
-                const char *vat = at + kTile * S::kRow;
-                uint32_t odd = 0;
+                // sums of the values: use(i, fragment of 16 d's and the 16 tokens)
                 auto values = [&](auto use) {
 #pragma unroll
-                    for (int c = 0; c < (VB + 15) / 16; ++c) {
-                        constexpr int kWords = VB < 16 ? 2 : 4;
-                        uint32_t v[4][4];
+                    for (int k = 0; k < kSteps; ++k) {
+                        uint32_t v[4];
+                        load_matrices<true>(v, (at + off_v + k / 4 * 2048) ^ (k % 4 * 32));
+                        if constexpr (F8) {
+                            // pairs of d's of two tokens -> pairs of tokens of two d's
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if constexpr (VB == 8) {
-                                const uint2 w =
-                                    *reinterpret_cast<const uint2 *>(vat + r * 256 + lane * 8);
-                                v[r][0] = w.x, v[r][1] = w.y;
-                            } else {
-                                const uint4 w = *reinterpret_cast<const uint4 *>(
-                                    vat + (r * (VB / 16) + c) * 512 + lane * 16);
-                                v[r][0] = w.x, v[r][1] = w.y, v[r][2] = w.z, v[r][3] = w.w;
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t a = __byte_perm(v[2 * h], 0, 0x3120);
+                                const uint32_t b = __byte_perm(v[2 * h + 1], 0, 0x3120);
+                                const uint32_t f[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16),
+                                                       e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16)};
+                                use(2 * k + h, f);
                             }
-                        }
-#pragma unroll
-                        for (int k = 0; k < kWords; ++k) {
-                            if (F8) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const uint32_t a =
-                                        __byte_perm(v[0][k], v[1][k], h ? 0x7362 : 0x5140);
-                                    const uint32_t b =
-                                        __byte_perm(v[2][k], v[3][k], h ? 0x7362 : 0x5140);
-                                    const uint32_t f[4] = {
-                                        e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16),
-                                        e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16)};
-                                    use((c * kWords + k) * 2 + h, f);
-                                }
-                            } else {
-                                const uint32_t f[4] = {__byte_perm(v[0][k], v[1][k], 0x5410),
-                                                       __byte_perm(v[0][k], v[1][k], 0x7632),
-                                                       __byte_perm(v[2][k], v[3][k], 0x5410),
-                                                       __byte_perm(v[2][k], v[3][k], 0x7632)};
-                                use(c * kWords + k, f);
-                            }
+                        } else {
+                            use(k, v);
                         }
                     }
                 };
-                if (partly && p.rows > 1) {
-                    // a value that one row sees and another does not
-#pragma unroll
-                    for (int r = 0; r < 4 * VB / 4; ++r)
-                        odd |= not_finite<TYPE>(*reinterpret_cast<const uint32_t *>(
-                            vat + (r * 32 + lane) * 4));
-                }
-                if (!__any_sync(~0u, odd != 0)) {
+                if (!partly) {
                     values([&](int i, const uint32_t (&f)[4]) {
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             mma<TYPE>(o[i][j], f, ph[j][0], ph[j][1]);
-                            mma<TYPE>(o[i][j], f, pl[j][0], pl[j][1]);
+                            if (two) mma<TYPE>(o[i][j], f, pl[j][0], pl[j][1]);
                         }
                     });
                 } else {
-                    // 0 times an infinity would reach the rows that do not see it:
-                    // row by row, with the values that it sees
-                    for (int r = 0; r < p.rows; ++r) {
-                        const int last = n - p.rows + r;
-                        uint32_t keep[2] = {0, 0};
+                    // Values that no row sees are taken out: 0 times what lies there
+                    // may be NaN.  Where a value that some rows see and others do not
+                    // is none, row by row, with the values that each sees.
+                    uint32_t any[2] = {0, 0}, some[2] = {0, 0};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int token = tok + 2 * t + (i & 1) + (i & 2) * 4;
-                            if (token <= last && !(p.window && token <= last - p.window))
-                                keep[i / 2] |= i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                    for (int i = 0; i < 4; ++i) {
+                        const int token = tok + 2 * t + (i & 1) + (i & 2) * 4;
+                        const uint32_t bits = i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                        if (token < n && !(p.window && token <= n - p.rows - p.window)) {
+                            any[i / 2] |= bits;
+                            if (token > n - p.rows || (p.window && token < n - p.window))
+                                some[i / 2] |= bits;
+                        }
+                    }
+                    uint32_t odd = 0;
+                    if (p.rows > 1)
+                        values([&](int, const uint32_t (&f)[4]) {
+                            odd |= not_finite<TYPE>(f[0] & some[0]) | not_finite<TYPE>(f[1] & some[0]) |
+                                   not_finite<TYPE>(f[2] & some[1]) | not_finite<TYPE>(f[3] & some[1]);
+                        });
+                    const bool each = __any_sync(~0u, odd != 0);
+                    for (int r = 0; r < (each ? p.rows : 1); ++r) {
+                        const int last = n - p.rows + r;
+                        uint32_t keep[2] = {any[0], any[1]};
+                        if (each) {
+                            keep[0] = keep[1] = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int token = tok + 2 * t + (i & 1) + (i & 2) * 4;
+                                if (token <= last && !(p.window && token <= last - p.window))
+                                    keep[i / 2] |= i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                            }
                         }
                         values([&](int i, const uint32_t (&f)[4]) {
                             const uint32_t a[4] = {f[0] & keep[0], f[1] & keep[0], f[2] & keep[1],
@@ -610,14 +643,15 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                             for (int j = 0; j < NT; ++j) {
                                 float d[4] = {0.f, 0.f, 0.f, 0.f};
                                 mma<TYPE>(d, a, ph[j][0], ph[j][1]);
-                                mma<TYPE>(d, a, pl[j][0], pl[j][1]);
+                                if (two) mma<TYPE>(d, a, pl[j][0], pl[j][1]);
 #pragma unroll
                                 for (int c = 0; c < 4; ++c)
-                                    if (pos[j][c % 2] == last) o[i][j][c] += d[c];
+                                    if (!each || pos[j][c % 2] == last) o[i][j][c] += d[c];
                             }
                         });
                     }
                 }
+                __syncwarp();                  // the stage may be filled again
             }
 
             // the sums of the rows' weights over the lanes
@@ -629,8 +663,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                     for (int d = 4; d < 32; d *= 2)
                         sums[j][c] += __shfl_xor_sync(~0u, sums[j][c], d);
 
-            // d of a lane's i-th value of a row
-            constexpr int kRun = VB < 16 ? 8 : E;
+            // o[i][j][2 h + c] is of d = 16 i + 2 g + h (e4m3) or 16 i + 8 h + g
             if (s0 == 0 && s1 == it.tiles) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -639,222 +672,299 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                         const int m = mb * M + j * 8 + 2 * t + c;
                         if (m >= m_all) continue;
                         const float l = sums[j][c];
-                        float f = l == 0.f ? 0.f : 1.f / l;
-                        if (F8 && l != 0.f) f /= lift[j][c];
-                        const int r = m / p.group;
+                        const float f = l == 0.f ? 0.f : inverse(F8 ? l * lift[j][c] : l);
+                        const int r = p.by_group.over(m);
                         uint16_t *row = static_cast<uint16_t *>(p.out) +
                                         (((int64_t)it.b * p.rows + r) * p.heads + it.h) *
                                             p.group * D +
                                         (int64_t)(m - r * p.group) * D;
 #pragma unroll
-                        for (int u = 0; u < D / 8; u += 8) {   // runs of 8
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float a = o[u / 2 + i][j][c] * f,
-                                            b = o[u / 2 + i][j][c + 2] * f;
-                                w[i] = p.dtype == MOEOP_BF16
-                                           ? (uint32_t)f2bf16_rn(a) | (uint32_t)f2bf16_rn(b) << 16
-                                           : pack_f16x2(a, b);
+                        for (int i = 0; i < D / 16; ++i) {
+                            const float a = o[i][j][c] * f, b = o[i][j][c + 2] * f;
+                            const uint32_t w = p.dtype == MOEOP_BF16 ? pair<MOEOP_BF16>(a, b)
+                                                                     : pair<MOEOP_FP16>(a, b);
+                            if (F8) {
+                                *reinterpret_cast<uint32_t *>(row + 16 * i + 2 * g) = w;
+                            } else {
+                                row[16 * i + g] = (uint16_t)w;
+                                row[16 * i + 8 + g] = (uint16_t)(w >> 16);
                             }
-                            *reinterpret_cast<uint4 *>(row + (u / kRun * 8 + g) * kRun + u % kRun) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
             } else {
                 // the last item's sums go to the ring, which is empty then
                 const bool last = it.start + s1 == end;
-                if (last) {
-                    copies_wait<0>();
-                    __syncwarp();
-                }
-                float *part = last ? tail : heads_at + (int64_t)warp * S::kPart;
+                const int share = 2 * warp + (last ? 1 : 0);
+                float *part = last ? reinterpret_cast<float *>(ring)
+                                   : heads_at + (int64_t)warp * S::kPart;
+                has |= last ? 2 : 1;
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < NT; ++j) {
+                    if (g == 0) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int m = j * 8 + 2 * t + c;
-                        if (g == 0) {
-                            part[m] = top[j][c];
-                            part[M + m] = sums[j][c];
-                            part[2 * M + m] = F8 ? otop[j][c] : top[j][c];
+                        for (int c = 0; c < 2; ++c) {
+                            const int m = j * 8 + 2 * t + c;
+                            stats[share][0][m] = top[j][c];
+                            stats[share][1][m] = sums[j][c];
+                            stats[share][2][m] = F8 ? otop[j][c] : top[j][c];
                         }
-                        float *row = part + S::kStats + m * D;
-#pragma unroll
-                        for (int u = 0; u < D / 8; u += 4)
-                            *reinterpret_cast<float4 *>(row + (u / kRun * 8 + g) * kRun + u % kRun) =
-                                make_float4(o[u / 2][j][c], o[u / 2][j][c + 2], o[u / 2 + 1][j][c],
-                                            o[u / 2 + 1][j][c + 2]);
                     }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int d = 16 * i + (F8 ? 2 * g + h : 8 * h + g);
+                            *reinterpret_cast<float2 *>(part + d * M + j * 8 + 2 * t) =
+                                make_float2(o[i][j][2 * h], o[i][j][2 * h + 1]);
+                        }
+                }
             }
             x = it.start + s1;
-            if (x < end) it.next(all);
+            if (x < end) {
+                it.next(first, p.heads);
+                load_q();
+            }
         }
-        copies_wait<0>();
+        if (lane == 0) lasts[warp] = it;
     }
+    if (lane == 0) shares_of[warp] = has;
     __syncthreads();
 
     // -----------------------------------------------------------------------
     // Join: the block's warps, then the blocks
     // -----------------------------------------------------------------------
-    // what a sum's rows are worth: to the common maximum, and at the end
-    auto store = [&](const Item &x, int m, int d, float4 v, float f) {
-        const int row = mb * M + m;
-        if (row >= m_all) return;
-        const int r = row / p.group;
+    // Four numbers of O^T, from number i of a partial sum on: d = i / M, rows i % M ..
+    auto store = [&](const Item &x, int i, const float (&v)[4]) {
         uint16_t *to = static_cast<uint16_t *>(p.out) +
-                       (((int64_t)x.b * p.rows + r) * p.heads + x.h) * p.group * D +
-                       (int64_t)(row - r * p.group) * D + d;
-        uint2 w;
-        if (p.dtype == MOEOP_BF16) {
-            w.x = (uint32_t)f2bf16_rn(v.x * f) | (uint32_t)f2bf16_rn(v.y * f) << 16;
-            w.y = (uint32_t)f2bf16_rn(v.z * f) | (uint32_t)f2bf16_rn(v.w * f) << 16;
-        } else {
-            w.x = pack_f16x2(v.x * f, v.y * f);
-            w.y = pack_f16x2(v.z * f, v.w * f);
+                       ((int64_t)x.b * p.rows * p.heads + x.h) * p.group * D + i / M;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int row = mb * M + i % M + c;
+            if (row >= m_all) return;
+            const int r = p.by_group.over(row);
+            to[((int64_t)r * (p.heads - 1) * p.group + row) * D] =
+                (uint16_t)(p.dtype == MOEOP_BF16 ? pair<MOEOP_BF16>(v[c], 0.f)
+                                                 : pair<MOEOP_FP16>(v[c], 0.f));
         }
-        *reinterpret_cast<uint2 *>(to) = w;
     };
     auto worth = [](float l, float top, float otop) {  // 2^(otop - top) / l
         if (l == 0.f) return 0.f;
-        return F8 && top != -INFINITY && otop != -INFINITY ? ex2(otop - top) / l : 1.f / l;
+        const float by = F8 && top != -INFINITY && otop != -INFINITY ? ex2(otop - top) : 1.f;
+        return by * inverse(l);
     };
-    const int64_t cs = starts[0], ce = starts[W];
-    int crosses = 0;
-    Item cross0(all, cs, p.batch), cross1 = cross0;
-    int64_t done = cs;                    // items up to here are joined
-    for (int w0 = -1; w0 < W; ++w0) {
-        // the block's first item where another block began it, then the last one
-        // of each warp
-        if (w0 >= 0 && starts[w0] >= starts[w0 + 1]) break;
-        if (w0 < 0 && cross0.start == cs) continue;
-        const Item x(all, w0 < 0 ? cs : starts[w0 + 1] - 1, p.batch);
-        const int64_t xe = x.start + x.tiles;
-        if (xe <= done || (w0 >= 0 && x.start < done)) continue;
-        const bool inside = x.start >= cs && xe <= ce;
-        const int64_t from = max(x.start, cs), to = min(xe, ce);
-        int a = 0, b = 0;
-        while (starts[a + 1] <= from) ++a;
-        b = a;
-        while (starts[b + 1] < to) ++b;
-        done = to;
-        if (inside && a == b) continue;   // written by its warp
-        float *out = blocks_at + (2 * blockIdx.x + (x.start >= cs ? 1 : 0)) * (int64_t)S::kPart;
-        for (int i = threadIdx.x; i < M * D / 4; i += W * 32) {
-            const int m = i / (D / 4), d = i % (D / 4) * 4;
-            auto part = [&](int w) -> const float * {
-                return starts[w + 1] <= xe ? reinterpret_cast<const float *>(
-                                                 smem + w * (S::kStages * S::kStage))
-                                           : heads_at + (int64_t)w * S::kPart;
-            };
-            float top = -INFINITY, otop = -INFINITY, l = 0.f;
-            for (int w = a; w <= b; ++w) {
-                top = fmaxf(top, part(w)[m]);
-                otop = fmaxf(otop, part(w)[2 * M + m]);
-            }
-            const float tref = top == -INFINITY ? 0.f : top, oref = otop == -INFINITY ? 0.f : otop;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = a; w <= b; ++w) {
-                const float *q = part(w);
-                l = fmaf(q[M + m], ex2(q[m] - tref), l);
-                const float f = ex2(q[2 * M + m] - oref);
-                const float4 u = *reinterpret_cast<const float4 *>(q + S::kStats + m * D + d);
-                v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y);
-                v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
-            }
-            if (inside) {
-                store(x, m, d, v, worth(l, top, otop));
-            } else {
-                if (d == 0) out[m] = top, out[M + m] = l, out[2 * M + m] = otop;
-                *reinterpret_cast<float4 *>(out + S::kStats + m * D + d) = v;
-            }
+    auto finite = [](float v) { return v == -INFINITY ? 0.f : v; };
+    // Lane e looks at share e.  A share that is not there counts to the item of the
+    // next one, with nothing.
+    Item mine;
+    mine.start = -1, mine.tiles = 0;
+    const bool there = lane < 2 * W && (shares_of[lane / 2] >> (lane & 1) & 1);
+    const uint32_t present = __ballot_sync(~0u, there);
+    if (lane < 2 * used) mine = !(lane & 1) && there ? fronts[lane / 2] : lasts[lane / 2];
+    const int before = __shfl_up_sync(~0u, mine.start, 1);
+    const uint32_t begins = __ballot_sync(~0u, lane == 0 || before != mine.start);
+    const uint32_t later = begins & ~((2u << lane) - 1);
+    const int from = 31 - __clz(begins & ((2u << lane) - 1)), to = later ? __ffs(later) - 2 : 31;
+    const bool inside = mine.start >= cs && mine.end() <= ce;
+    const uint32_t those = present >> from & ((2u << (to - from)) - 1);
+    // an item with one share here, all of it, was written by its warp: it has none
+    const uint32_t need = __ballot_sync(~0u, lane == from && those != 0);
+    const int groups = __popc(need);
+    // what each share's rows are worth: to the common maximum, or in the end
+    float *const blocks_out = blocks_at + 2 * blockIdx.x * (int64_t)S::kPart;
+#pragma unroll 1
+    for (int m = warp; m < M; m += W) {
+        const float top = there ? stats[lane][0][m] : -INFINITY, l = there ? stats[lane][1][m] : 0.f,
+                    otop = there ? stats[lane][2][m] : -INFINITY;
+        float tall = top, oall = otop;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {             // to the end of the item's shares
+            const float a = __shfl_down_sync(~0u, tall, d), b = __shfl_down_sync(~0u, oall, d);
+            if (lane + d <= to) tall = fmaxf(tall, a), oall = fmaxf(oall, b);
         }
-        if (!inside) (crosses++ ? cross1 : cross0) = x;
+        tall = __shfl_sync(~0u, tall, from), oall = __shfl_sync(~0u, oall, from);
+        float sum_l = there ? l * ex2(top - finite(tall)) : 0.f;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const float a = __shfl_down_sync(~0u, sum_l, d);
+            if (lane + d <= to) sum_l += a;
+        }
+        sum_l = __shfl_sync(~0u, sum_l, from);
+        const float f = ex2(otop - finite(oall));
+        if (there) worth_of[lane][m] = inside ? f * worth(sum_l, tall, oall) : f;
+        if (there && !inside && lane == from + __ffs(those) - 1) {
+            float *out = blocks_out + (mine.start >= cs ? S::kPart : 0);
+            out[m] = tall, out[M + m] = sum_l, out[2 * M + m] = oall;
+        }
     }
+    __syncthreads();
+    // the warps share the items out
+    const int slices = groups > 0 && groups < W ? W / groups : 1;
+#pragma unroll 1
+    for (int k = warp / slices; k < groups; k += W / slices) {
+        uint32_t rest = need;
+        for (int i = 0; i < k; ++i) rest &= rest - 1;
+        const int e0 = __ffs(rest) - 1;
+        const bool here = __shfl_sync(~0u, inside ? 1 : 0, e0);
+        const uint32_t bits = __shfl_sync(~0u, those, e0) << e0;
+        Item x;
+        x.b = __shfl_sync(~0u, mine.b, e0), x.h = __shfl_sync(~0u, mine.h, e0);
+        x.start = __shfl_sync(~0u, mine.start, e0);
+        float *const out = blocks_out + (x.start >= cs ? S::kPart : 0) + S::kStats;
+#pragma unroll 1
+        for (int i = (warp % slices * 32 + lane) * 4; i < M * D; i += slices * 128) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t left = bits;
+#pragma unroll 4
+            for (int n = __popc(bits); n; --n) {
+                const int e = __ffs(left) - 1;
+                left &= left - 1;
+                const float *part =
+                    e & 1 ? reinterpret_cast<const float *>(smem + e / 2 * (kStages * S::kStage))
+                          : heads_at + (int64_t)(e / 2) * S::kPart;
+                const float4 u = *reinterpret_cast<const float4 *>(part + i);
+                const float4 f = *reinterpret_cast<const float4 *>(&worth_of[e][i % M]);
+                v[0] = fmaf(u.x, f.x, v[0]), v[1] = fmaf(u.y, f.y, v[1]);
+                v[2] = fmaf(u.z, f.z, v[2]), v[3] = fmaf(u.w, f.w, v[3]);
+            }
+            if (here)
+                store(x, i, v);
+            else
+                *reinterpret_cast<float4 *>(out + i) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    // -----------------------------------------------------------------------
+    // The last block to reach an item joins it; beyond kJoin blocks the last of
+    // each kJoin of them joins theirs, the last of those the whole.  atomicInc
+    // leaves the counters zero.
+    // -----------------------------------------------------------------------
+    constexpr int kJoin = 16;
+    const Item head = fronts[0], back = lasts[used - 1];
+    const bool from_before = head.start < cs, goes_on = back.start >= cs && back.end() > ce;
+    const int crosses = (from_before ? 1 : 0) + (goes_on ? 1 : 0);
     if (!crosses) return;
-    // the last block to reach an item joins it; atomicInc leaves the counter zero
+    float *const all = reinterpret_cast<float *>(smem);        // the ring is free
+    // counters by a block that no other item has in this place: the one where the
+    // item begins, or where one of its groups does
+    uint32_t *const counters = p.counters + mb * gridDim.x;
+    auto arrive = [&](uint32_t *counter, int parts) {
+        __threadfence();
+        const bool last =
+            parts == 1 || atomicInc(counter, parts - 1) == (uint32_t)parts - 1;
+        __threadfence();
+        return last;
+    };
+    auto crossing = [&](int k) { return from_before && k == 0 ? head : back; };
     __syncthreads();
     if ((int)threadIdx.x < crosses) {
-        const Item &x = threadIdx.x ? cross1 : cross0;
-        const int first_block = shares.owner(x.start) / W,
-                  last_block = shares.owner(x.start + x.tiles - 1) / W;
-        __threadfence();
-        // an item's counter is its first block's: no other item goes on from there
-        uint32_t *counter = p.counters + mb * gridDim.x + first_block;
-        joins[threadIdx.x] =
-            atomicInc(counter, last_block - first_block) == (uint32_t)(last_block - first_block);
-        __threadfence();
+        const Item x = crossing(threadIdx.x);
+        const int c0 = shares.owner(x.start), count = shares.owner(x.end() - 1) - c0 + 1;
+        const int group = (blockIdx.x - c0) / kJoin, from = c0 + group * kJoin;
+        joined[threadIdx.x] =
+            arrive(counters + from + (group ? 256 : 0), min(count - group * kJoin, kJoin));
     }
     __syncthreads();
-    float *const stats = reinterpret_cast<float *>(smem);      // the ring is free
+#pragma unroll 1
     for (int k = 0; k < crosses; ++k) {
-        if (!joins[k]) continue;
-        const Item &x = k ? cross1 : cross0;
-        const int c0 = shares.owner(x.start) / W;
-        const int parts = shares.owner(x.start + x.tiles - 1) / W - c0 + 1;
-        // a block's share is its second sum where the item begins in it
-        auto part = [&](int i) {
-            return blocks_at + (2 * (c0 + i) + (i == 0 ? 1 : 0)) * (int64_t)S::kPart;
-        };
-        // stats: the three numbers of each part's rows, then what the part is worth
-        for (int i = threadIdx.x; i < parts * S::kStats; i += W * 32)
-            stats[i] = __ldcg(part(i / S::kStats) + i % S::kStats);
-        float *const final = stats + parts * S::kStats;
-        __syncthreads();
-        for (int m = warp; m < M; m += W) {
-            float top = -INFINITY, otop = -INFINITY, l = 0.f;
-            for (int i = lane; i < parts; i += 32) {
-                top = fmaxf(top, stats[i * S::kStats + m]);
-                otop = fmaxf(otop, stats[i * S::kStats + 2 * M + m]);
-            }
+        if (!joined[k]) continue;
+        const Item x = crossing(k);
+        const int c0 = shares.owner(x.start), count = shares.owner(x.end() - 1) - c0 + 1;
+        const int group = (blockIdx.x - c0) / kJoin, groups = (count + kJoin - 1) / kJoin;
+        int parts = min(count - group * kJoin, kJoin), from = c0 + group * kJoin, step = 1;
+#pragma unroll 1
+        while (true) {
+            // a block's share is its second sum where the item begins in it
+            auto part = [&](int i) {
+                const int c = from + i * step;
+                return blocks_at + (2 * c + (c == c0 ? 1 : 0)) * (int64_t)S::kPart;
+            };
+            const bool whole = step > 1 || groups == 1;
+            // the three numbers of each part's rows, then what the part is worth
+            for (int i = threadIdx.x; i < parts * S::kStats; i += W * 32)
+                all[i] = __ldcg(part(i / S::kStats) + i % S::kStats);
+            __syncthreads();
+#pragma unroll 1
+            for (int m = warp; m < M; m += W) {
+                const float *s = all + lane * S::kStats;
+                const bool in = lane < parts;
+                const float top = in ? s[m] : -INFINITY, otop = in ? s[2 * M + m] : -INFINITY;
+                float tall = top, oall = otop;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                otop = fmaxf(otop, __shfl_xor_sync(~0u, otop, o));
-            }
-            const float tref = top == -INFINITY ? 0.f : top, oref = otop == -INFINITY ? 0.f : otop;
-            for (int i = lane; i < parts; i += 32) {
-                float *s = stats + i * S::kStats;
-                l = fmaf(s[M + m], ex2(s[m] - tref), l);
-                s[m] = ex2(s[2 * M + m] - oref);
-            }
+                for (int d = kJoin / 2; d; d >>= 1) {
+                    tall = fmaxf(tall, __shfl_xor_sync(~0u, tall, d));
+                    oall = fmaxf(oall, __shfl_xor_sync(~0u, oall, d));
+                }
+                float l = in ? s[M + m] * ex2(top - finite(tall)) : 0.f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-            if (lane == 0) final[m] = worth(l, top, otop);
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < M * D / 4; i += W * 32) {
-            const int m = i / (D / 4), d = i % (D / 4) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int d = kJoin / 2; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+                if (in) {
+                    const float f = ex2(otop - finite(oall));
+                    worth_of[lane][m] = whole ? f * worth(l, tall, oall) : f;
+                }
+                if (lane == 0 && !whole) {
+                    float *out = part(0);
+                    out[m] = tall, out[M + m] = l, out[2 * M + m] = oall;
+                }
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int i = threadIdx.x * 4; i < M * D; i += W * 128) {
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-            for (int w = 0; w < parts; ++w) {
-                const float f = stats[w * S::kStats + m];
-                const float4 u = __ldcg(
-                    reinterpret_cast<const float4 *>(part(w) + S::kStats + m * D + d));
-                v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y);
-                v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+                for (int w = 0; w < parts; ++w) {
+                    const float4 u =
+                        __ldcg(reinterpret_cast<const float4 *>(part(w) + S::kStats + i));
+                    const float4 f = *reinterpret_cast<const float4 *>(&worth_of[w][i % M]);
+                    v[0] = fmaf(u.x, f.x, v[0]), v[1] = fmaf(u.y, f.y, v[1]);
+                    v[2] = fmaf(u.z, f.z, v[2]), v[3] = fmaf(u.w, f.w, v[3]);
+                }
+                if (whole)
+                    store(x, i, v);
+                else
+                    *reinterpret_cast<float4 *>(part(0) + S::kStats + i) =
+                        make_float4(v[0], v[1], v[2], v[3]);
             }
-            store(x, m, d, v, final[m]);
+            __syncthreads();
+            if (whole) break;
+            parts = groups, from = c0, step = kJoin;
+            if (threadIdx.x == 0) joined[k] = arrive(counters + c0 + 512, parts);
+            __syncthreads();
+            if (!joined[k]) break;
         }
-        __syncthreads();
     }
 }
 
 template <int TYPE, int D, int NT>
-cudaError_t launch(const AttendParams &p, cudaStream_t st) {
+cudaError_t launch(AttendParams p, cudaStream_t st) {
     using S = Shape<TYPE, D, NT>;
     const auto kernel = attend_kernel<TYPE, D, NT>;
-    // every call: the attribute is the device's, and costs less than a lookup
-    const int smem = S::kRing + (2 * p.batch + 1) * 4;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+    // the limit of shared memory is set once on each device
+    static std::atomic<uint64_t> allowed{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (device & 63);
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      S::smem(kAttendMaxBatch))) != cudaSuccess)
+            return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    TensorMap kmap, vmap;
+    const int64_t rows = (int64_t)p.heads * p.page;
+    if ((e = status_word(&p.status)) != cudaSuccess ||
+        (e = make_cache_map(&kmap, p.k, S::kRow, rows, p.k_stride * S::kSize, p.pages)) !=
+            cudaSuccess ||
+        (e = make_cache_map(&vmap, p.v, S::kRow, rows, p.v_stride * S::kSize, p.pages)) !=
+            cudaSuccess)
+        return e;
     // no more blocks than there can be tiles for their warps
     int64_t tiles = (int64_t)p.width * p.page / kTile;
     if (p.window && (p.window + p.rows) / kTile + 2 < tiles) tiles = (p.window + p.rows) / kTile + 2;
     const int64_t most = (tiles * p.batch * p.heads + S::kWarps - 1) / S::kWarps;
     const int grid = attend_grid(p.blocks);
-    kernel<<<dim3((unsigned)(most < grid ? most : grid), p.blocks), S::kWarps * 32, smem, st>>>(p);
+    p.by_grid = Divisor((uint32_t)(most < grid ? most : grid));
+    kernel<<<dim3(p.by_grid.d, p.blocks), S::kWarps * 32, S::smem(p.batch), st>>>(
+        kmap, vmap, p);
     return cudaGetLastError();
 }
 template <int TYPE>

@@ -3,13 +3,10 @@
 #pragma once
 
 #include "moe_device.cuh"
+#include "moeop.cuh"
 
 namespace moe {
 namespace op {
-
-struct alignas(64) TensorMap {
-    uint64_t v[16];
-};
 
 // Bounded wait that also ends when another role of the block gave up.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort) {
@@ -60,6 +57,15 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const TensorMap *m, int x,
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+// Box from row y of page z on, whole rows.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const TensorMap *m, int y, int z,
+                                         uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %2, %4}], [%5];" ::"r"(dst),
+        "l"(m), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
 // Four rows of a map whose box is one row high.

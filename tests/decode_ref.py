@@ -58,7 +58,13 @@ def attend(q, cache, table, lengths, scale=None, window=0):
             # scores: d products and additions and some 16 other steps of fp32, each
             # relative to the sum of magnitudes (the exponent's own rounding among
             # them); exp2 2^-22; both in numerator and denominator
-            rel = 2 * (torch.exp((2 * d + 32) * 2.0 ** -23 * size) - 1 + 2.0 ** -21)
+            off = (2 * d + 32) * 2.0 ** -23 * size
+            if cache.k_scales is not None:
+                # q in e4m3 numbers, the last of which counts in steps of 2^-9 of 2^-5
+                # where the row's largest is 2^7: half a step is 2^-22 of that
+                off = off + 2.0 ** -22 * abs(scale) * x.abs().amax(2) * \
+                    k.abs().sum(2).amax(0).unsqueeze(1)
+            rel = 2 * (torch.exp(off) - 1 + 2.0 ** -21)
             # weights as two 16-bit numbers; additions of the tokens and the joins
             rel = rel + (2.0 ** -16 if q.dtype == torch.bfloat16 and cache.k_scales is None
                          else 2.0 ** -21) + (len(at) + 64) * 2.0 ** -22
