@@ -99,7 +99,7 @@ cudaError_t status_word(uint32_t **p);  // the current device's status word
 struct alignas(64) TensorMap {
     uint64_t v[16];
 };
-cudaError_t make_cache_map(TensorMap *m, const void *p, int row_bytes, int64_t rows,
+cudaError_t make_cache_map(TensorMap *m, const void *p, int row_bytes, int box_rows, int64_t rows,
                            int64_t page_bytes, int64_t pages);
 
 // Quotients of numbers below 2^31 by one that many share: a multiplication
@@ -162,6 +162,7 @@ struct AttendParams {
     uint32_t *counters;        // kAttendCounters, zero between calls
     float *parts;              // sums of a warp's or thread block's share of an item
     uint32_t *status;
+    bool wide;                 // a tile never leaves its page
 };
 // Query rows (row, head of the group) that a thread block takes together.
 constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 16; }
@@ -169,8 +170,8 @@ constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 1
 constexpr int kAttendSms = 152, kAttendCounters = 3 * 256, kAttendMaxBatch = 2048;
 constexpr int attend_grid(int blocks) { return blocks < kAttendSms ? kAttendSms / blocks : 1; }
 // Workspace of moeop_attend_paged: the counters, in every shape the same, then a
-// partial sum for each warp (up to 16 in a thread block, 8 where dim is 256) and
-// two for each thread block: three numbers for a row, and the row.
+// partial sum for each warp (up to 8 in a thread block) and two for each thread
+// block: three numbers for a row, and the row.
 struct AttendWs {
     size_t parts, total;
     static AttendWs make(int m, int dim) {
@@ -178,7 +179,7 @@ struct AttendWs {
         const size_t part = (size_t)block * (3 + dim) * 4;
         AttendWs w{};
         w.parts = kAttendCounters * 4;
-        w.total = w.parts + part * blocks * attend_grid(blocks) * ((dim == 256 ? 8 : 16) + 2);
+        w.total = w.parts + part * blocks * attend_grid(blocks) * (8 + 2);
         return w;
     }
 };
@@ -187,6 +188,30 @@ cudaError_t launch_attend_bf(const AttendParams &p, int dim, cudaStream_t st);
 cudaError_t launch_attend_hf(const AttendParams &p, int dim, cudaStream_t st);
 
 #ifdef __CUDACC__
+// Launch that may start while the kernel before it in the stream still runs; the
+// kernel waits for that (pdl_wait) before its first read of memory.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                         cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[2];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = cluster;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Four values -> four e4m3 codes, nearest even, beyond +-448 the largest.
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

@@ -13,11 +13,11 @@
 // tile, and no warp waits for another.
 //
 // - Work.  A sequence's tokens for one key/value head are an item, cut into
-//   tiles of 16 tokens (a tile never leaves its page).  The tiles of all items
+//   tiles of 16 or 32 tokens (16 never leave their page).  The tiles of all items
 //   in a row are dealt to the warps of the grid in equal contiguous shares, so
 //   lengths may differ as they like, one long sequence fills the GPU as well as
 //   many short ones, and the ring runs on from one item into the next.
-// - Product.  The 16 tokens are the rows of mma.sync, the query rows its 8 columns:
+// - Product.  16 tokens are the rows of mma.sync, the query rows its 8 columns:
 //   S = K Q^T, then O^T = V^T P^T with the d's as rows.  So a group of up to 8
 //   rows pays for 8, not 16.  (tcgen05 would want 64 rows or more: here there are
 //   8 or 16, and the tensor cores are idle most of the time as it is.)  Fragments
@@ -50,30 +50,32 @@ namespace moe {
 namespace op {
 namespace attend {
 
-constexpr int kTile = 16;        // tokens
 constexpr float kSlack = 8.f;    // what a score may exceed the running maximum by (log2)
 
 // TYPE of the cache, D: dim, NT: groups of 8 query rows.
-// A tile is 32 rows of D elements; warps x stages of them fill shared memory.
-// Warps as the registers allow (O alone: NT D / 4 a thread).
+// A tile is kTok tokens, 8 KB of keys and values where it can be; warps x stages of
+// them fill shared memory.  Eight warps: with more the registers of O (NT D / 4 a
+// thread) spill, and what every warp does once costs more.
 template <int TYPE, int D, int NT>
 struct Shape {
     static constexpr bool F8 = TYPE == MOEOP_E4M3;
     static constexpr int kSize = F8 ? 1 : 2;
     static constexpr int kRow = D * kSize;                // bytes of a row
-    static constexpr int kHalf = kTile * kRow;            // the keys of a tile
-    static constexpr int kStage = 2 * kHalf;
-    static constexpr int kWarps = kRow == 512 ? 4 : kRow == 256 || NT * D > 128 ? 8 : 12;
-    static constexpr int kStages = kRow == 64 ? 6 : kRow == 128 ? (kWarps == 8 ? 6 : 4) : 3;
+    static constexpr int kSubs = kRow <= 128 ? 2 : 1;     // a tile's groups of 16 tokens
+    static constexpr int kTok = 16 * kSubs;
+    static constexpr int kSub = 16 * kRow, kHalf = kSubs * kSub, kStage = 2 * kHalf;
+    static constexpr int kWarps = kRow == 512 ? 4 : 8;
+    static constexpr int kStages = kRow == 64 ? 6 : 3;
     static constexpr int M = 8 * NT;
     // a partial sum: m, l and the sums' own maximum of each row, then O^T
     static constexpr int kStats = 3 * M, kPart = kStats + M * D;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int smem(int batch) { return 1024 + kRing + (2 * batch + 1) * 4; }
     static constexpr int kSteps = kRow / 32;              // 32 bytes of a row: an MMA's
+    static constexpr int kWhole = 1536 / kTok;
     static_assert(M * D * 4 <= kStages * kStage, "a share's sums lie in its warp's ring");
     static_assert(kWarps <= 16, "two shares of each warp: a lane for each");
-    static_assert(kStage % 1024 == 0, "the swizzle's period");
+    static_assert(kStage % 1024 == 0 && kSub % 1024 == 0, "the swizzle's period");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -154,7 +156,7 @@ struct alignas(16) Item {
         tiles = first[lo + 1] - first[lo];
         const int base = first[lo] * heads;
         // the quotient is below 1024: one off at most
-        h = (int)((float)(x - base) / (float)tiles);
+        h = (int)((float)(x - base) * inverse((float)tiles));
         if (h * tiles > x - base) --h;
         if ((h + 1) * tiles <= x - base) ++h;
         start = base + h * tiles;
@@ -176,19 +178,19 @@ struct Shares {
         return x < big ? x / (each + 1) : more + (x - big) / max(each, 1);
     }
 };
-// An item of up to kWhole tiles is not cut between blocks: the cut goes to its
-// nearer end.  To join what two blocks have of an item takes 4 us, in which a block
-// reads some 40 tiles.
-constexpr int kWhole = 96;
-__device__ __forceinline__ int cut(const int *first, int heads, int batch, int tiles, int x) {
+// An item of up to `whole` tiles is not cut between blocks: the cut goes to its
+// nearer end.  To join what two blocks have of an item takes some 4 us.
+__device__ __forceinline__ int cut(const int *first, int heads, int batch, int tiles, int whole,
+                                   int x) {
     if (x <= 0 || x >= tiles) return min(x, tiles);
     const Item i(first, heads, batch, x);
-    return i.tiles > kWhole ? x : x - i.start < i.end() - x ? i.start : i.end();
+    return i.tiles > whole ? x : x - i.start < i.end() - x ? i.start : i.end();
 }
 
 // First tile of a sequence of n tokens that some row sees (0 without a window).
+template <int TOK>
 __device__ __forceinline__ int first_tile(const AttendParams &p, int n) {
-    return p.window ? max(0, n - p.rows - p.window + 1) / kTile : 0;
+    return p.window ? max(0, n - p.rows - p.window + 1) / TOK : 0;
 }
 
 template <int TYPE, int D, int NT>
@@ -198,13 +200,16 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     using S = Shape<TYPE, D, NT>;
     constexpr bool F8 = S::F8;
     constexpr int W = S::kWarps, M = S::M, kStages = S::kStages, kSteps = S::kSteps;
+    constexpr int kTok = S::kTok, kSubs = S::kSubs;
     extern __shared__ char raw[];
     __shared__ uint64_t bars[W][kStages];
+    __shared__ int2 places[W][kStages][kSubs];   // of a tile's tokens: page, row in the page
     __shared__ int scan[W], joined[2];
     // the shares of an item that a warp has and others too, in the order of their
     // tiles: the item it did not begin (2 w) and its last one (2 w + 1)
     __shared__ Item lasts[W], fronts[W];
-    __shared__ float stats[2 * W][3][M], worth_of[2 * W > 16 ? 2 * W : 16][M];
+    __shared__ float stats[2 * W][3][M];
+    __shared__ __align__(16) float worth_of[2 * W > 16 ? 2 * W : 16][M];
     __shared__ int shares_of[W];         // which of its two shares a warp has, as bits
     char *const smem = raw + (1024 - smem_u32(raw) % 1024) % 1024;
     int *const first = reinterpret_cast<int *>(smem + S::kRing);
@@ -214,22 +219,24 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     const int mb = blockIdx.y;                  // block of query rows
     const int m_all = p.rows * p.group;
 
+    // Tiles of the sequences before each one.  Up to 32 every warp counts them for
+    // itself (and all write the same): no barrier.
+    int sum = 0;
+    const bool few = p.batch <= 32;
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < kStages; ++i) mbar_init(&bars[warp][i], 1);
         fence_mbar_init();
         if (warp == W - 1) tma_prefetch_map(&kmap), tma_prefetch_map(&vmap);
     }
-    // Tiles of the sequences before each one.  Up to 32 every warp counts them for
-    // itself (and all write the same): no barrier.
-    int sum = 0;
-    const bool few = p.batch <= 32;
+    pdl_trigger();
+    pdl_wait();
     for (int b0 = 0; b0 < p.batch; b0 += W * 32) {
         const int b = b0 + (few ? lane : threadIdx.x);
         int n = 0, c = 0;
         if (b < p.batch) {
             n = min(max(__ldg(p.lengths + b), 0), p.width * p.page);
-            c = max(1, (n + kTile - 1) / kTile - first_tile(p, n));
+            c = max(1, (n + kTok - 1) / kTok - first_tile<kTok>(p, n));
             length[b] = n;
         }
         int run = c;
@@ -257,8 +264,10 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     else __syncthreads();
     const int tiles = sum * p.heads;
     const Shares shares(tiles, p.by_grid);
-    const int cs = cut(first, p.heads, p.batch, tiles, shares.begin(blockIdx.x)),
-              ce = cut(first, p.heads, p.batch, tiles, shares.begin(blockIdx.x + 1));
+    // one lane for either end
+    const int end_of = cut(first, p.heads, p.batch, tiles, S::kWhole,
+                           shares.begin(blockIdx.x + (lane & 1)));
+    const int cs = __shfl_sync(~0u, end_of, 0), ce = __shfl_sync(~0u, end_of, 1);
     if (cs >= ce) return;
     // equal shares for the block's warps
     const int used = min(W, ce - cs), warp_each = (ce - cs) / W, warp_more = (ce - cs) % W;
@@ -267,12 +276,11 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
 
     char *const ring = smem + warp * (kStages * S::kStage);
     const uint32_t ring_addr = smem_u32(ring);
-    // sums of items begun by another warp: one for each warp of the grid, then two
-    // for each block
-    float *const heads_at =
-        p.parts + ((int64_t)mb * gridDim.x * (W + 2) + (int64_t)blockIdx.x * W) * S::kPart;
-    float *const blocks_at =
-        p.parts + ((int64_t)mb * gridDim.x * (W + 2) + (int64_t)gridDim.x * W) * S::kPart;
+    // partial sums: of items begun by another warp, one for each warp of the grid; of
+    // items begun or ended by another block, two for each block
+    float *const mb_at = p.parts + (int64_t)mb * gridDim.x * (W + 2) * S::kPart;
+    float *const heads_at = mb_at + (int64_t)blockIdx.x * W * S::kPart;
+    float *const blocks_at = mb_at + (int64_t)gridDim.x * W * S::kPart;
 
     int has = 0;
     if (begin < end) {
@@ -314,16 +322,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         // Loads: the item, tile and page that are next
         // -------------------------------------------------------------------
         Item li = it;
-        const int page_tiles = p.page / kTile;
         int lx = begin;                            // next tile to load
-        int lpage, lplace;                         // its page in the sequence, tile of the page
+        int lpage, lplace;                         // its page in the sequence, place in the page
         int page0 = 0, ids = -1;                   // lane i: the number of page page0 + i
-        uint32_t valid = 0;                        // bit 0: the tile loaded last is in the cache
+        // which groups of the tiles under way are in the cache: the last loaded lowest
+        uint32_t valid = 0;
         bool lost = false;                         // a wait ran out
-        // a lane's scale of the next tile: of a key (lanes 0..15) or a value
-        const float *const scale_of = F8 ? (lane < 16 ? p.k_scales : p.v_scales) + lane % 16 : nullptr;
-        const int64_t scale_stride = lane < 16 ? p.k_scales_stride : p.v_scales_stride;
-        int64_t scale_at[kStages] = {};            // of the tiles under way, the last one first
         auto pages = [&]() {                       // a tile ahead of their use
             page0 = lpage;
             ids = page0 + lane < p.width
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                       : -1;
         };
         auto seek = [&]() {
-            const int tok = (first_tile(p, length[li.b]) + lx - li.start) * kTile;
+            const int tok = (first_tile<kTok>(p, length[li.b]) + lx - li.start) * kTok;
             lpage = p.by_page.over(tok);
             lplace = tok - lpage * p.page;
             pages();
@@ -340,20 +344,37 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         load_q();
         int stage_in = 0;
         auto load = [&]() {
-            const int id = __shfl_sync(~0u, ids, lpage - page0);
-            const bool in = lx < end && !lost && (unsigned)id < (unsigned)p.pages;
-            valid = valid << 1 | (in ? 1u : 0u);
+            const bool live = lx < end && !lost;
+            int id[kSubs], row[kSubs];
+            uint32_t in = 0;
 #pragma unroll
-            for (int i = kStages - 1; i; --i) scale_at[i] = scale_at[i - 1];
+            for (int u = 0; u < kSubs; ++u) {
+                const bool next = lplace + 16 * u >= p.page;
+                id[u] = __shfl_sync(~0u, ids, lpage - page0 + next);
+                row[u] = li.h * p.page + lplace + 16 * u - (next ? p.page : 0);
+                if (!live || (unsigned)id[u] >= (unsigned)p.pages) id[u] = -1;
+                else in |= 1u << u;
+                if (lane == u) places[warp][stage_in][u] = make_int2(id[u], row[u]);
+            }
+            valid = valid << kSubs | in;
             if (in) {
-                const int place = uniform(li.h * p.page + lplace);
                 const uint32_t dst = uniform(ring_addr + stage_in * S::kStage);
-                if (F8) scale_at[0] = id * scale_stride + place;
                 uint64_t *bar = &bars[warp][stage_in];
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u) id[u] = uniform(id[u]), row[u] = uniform(row[u]);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(bar, S::kStage);
-                    tma_rows(dst, &kmap, place, id, bar);
-                    tma_rows(dst + S::kHalf, &vmap, place, id, bar);
+                    mbar_arrive_expect_tx(bar, __popc(in) * 2 * S::kSub);
+                    if (p.wide) {
+                        tma_rows(dst, &kmap, row[0], id[0], bar);
+                        tma_rows(dst + S::kHalf, &vmap, row[0], id[0], bar);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < kSubs; ++u)
+                            if (id[u] >= 0) {
+                                tma_rows(dst + u * S::kSub, &kmap, row[u], id[u], bar);
+                                tma_rows(dst + S::kHalf + u * S::kSub, &vmap, row[u], id[u], bar);
+                            }
+                    }
                 }
                 __syncwarp();
             }
@@ -362,15 +383,27 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                 if (lx == li.end()) {
                     li.next(first, p.heads);
                     seek();
-                } else if ((lplace += kTile) == p.page) {
-                    lplace = 0;
-                    if (++lpage == page0 + 32) pages();
+                } else {
+                    lplace += kTok;
+                    while (lplace >= p.page) lplace -= p.page, ++lpage;
+                    if (lpage - page0 >= 31) pages();
                 }
             }
         };
 #pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) load();
-        float scale_next = F8 ? __ldg(scale_of + scale_at[kStages - 2]) : 0.f;
+        // the scales of the next tile: lane i's of token i
+        float ks_next = 1.f, vs_next = 1.f;
+        auto scales = [&](int at) {
+            if constexpr (F8) {
+                __syncwarp();
+                const int2 w = places[warp][at][lane / 16 % kSubs];
+                const int64_t i = w.y + lane % 16;
+                ks_next = __ldg(p.k_scales + (w.x < 0 ? 0 : w.x * p.k_scales_stride + i));
+                vs_next = __ldg(p.v_scales + (w.x < 0 ? 0 : w.x * p.v_scales_stride + i));
+            }
+        };
+        scales(0);
 
         // where a lane's rows of the matrices lie in a tile: K and e4m3 V have the
         // tokens 8..15 in the second matrix, V in 16 bits in the third
@@ -392,7 +425,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         for (int x = begin; x < end;) {
             const int n = length[it.b];
             const int s0 = x - it.start, s1 = min(end, it.end()) - it.start;
-            const int tile0 = first_tile(p, n);
+            const int tile0 = first_tile<kTok>(p, n);
 
             // Q as the right operand: with e4m3 a bf16 row goes to f16 by the power of
             // two that brings it there, exact within 2^-28 of its largest
@@ -445,87 +478,108 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             }
 
             for (int s = s0; s < s1; ++s) {
-                const float scale = scale_next;
+                const float ks_now = ks_next, vs_now = vs_next;
                 load();
-                if (F8) scale_next = __ldg(scale_of + scale_at[kStages - 2]);
                 const uint32_t at = ring_addr + stage * S::kStage;
                 const int now = stage;
                 if (++stage == kStages) stage = 0;
-                if (!(valid >> (kStages - 1) & 1)) continue;
+                scales(stage);
+                const uint32_t there = valid >> (kSubs * (kStages - 1)) & ((1u << kSubs) - 1);
+                if (!there) continue;
                 if (!mbar_wait(&bars[warp][now], phases >> now & 1)) {
                     lost = true;
                     if (lane == 0) atomicExch(p.status, (uint32_t)MOE_DEV_WAIT_TIMEOUT);
                 }
                 phases ^= 1u << now;
-                const int tok = (tile0 + s) * kTile;
+                const int tok = (tile0 + s) * kTok;
 
-                // scores: two MMAs in turn, that none waits for the one before
-                float acc[NT][2][4] = {};
+                // scores
+                float x2[kSubs][NT][4];
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    uint32_t r[4];
-                    load_matrices<false>(r, (at + off_k + k / 4 * 2048) ^ (k % 4 * 32));
-                    if constexpr (F8) {
+                for (int u = 0; u < kSubs; ++u) {
+                    // two sums in turn: an MMA need not wait for the one before
+                    float acc[NT][2][4] = {};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t f[4] = {
-                                e4m3x2_to_f16x2(r[2 * h]), e4m3x2_to_f16x2(r[2 * h + 1]),
-                                e4m3x2_to_f16x2(r[2 * h] >> 16),
-                                e4m3x2_to_f16x2(r[2 * h + 1] >> 16)};
+                    for (int k = 0; k < kSteps; ++k) {
+                        uint32_t r[4];
+                        load_matrices<false>(
+                            r, (at + off_k + u * S::kSub + k / 4 * 2048) ^ (k % 4 * 32));
+                        if constexpr (F8) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t f[4] = {
+                                    e4m3x2_to_f16x2(r[2 * h]), e4m3x2_to_f16x2(r[2 * h + 1]),
+                                    e4m3x2_to_f16x2(r[2 * h] >> 16),
+                                    e4m3x2_to_f16x2(r[2 * h + 1] >> 16)};
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+                                    mma<TYPE>(acc[j][h], f, q[j][2 * k + h][0], q[j][2 * k + h][1]);
+                            }
+                        } else {
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
-                                mma<TYPE>(acc[j][h], f, q[j][2 * k + h][0], q[j][2 * k + h][1]);
+                                mma<TYPE>(acc[j][k % 2], r, q[j][k][0], q[j][k][1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            mma<TYPE>(acc[j][k % 2], r, q[j][k][0], q[j][k][1]);
                     }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) x2[u][j][c] = acc[j][0][c] + acc[j][1][c];
                 }
-                float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-                if (F8) {
+                float vs[kSubs][2], lv[kSubs][2];
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        ks[r] = __shfl_sync(~0u, scale, g + 8 * r);
-                        vs[r] = __shfl_sync(~0u, scale, 16 + g + 8 * r);
-                        lv[r] = fmaxf(lg2(vs[r]), -120.f);
+                        float ks = 1.f;
+                        vs[u][r] = 1.f, lv[u][r] = 0.f;
+                        if (F8) {
+                            ks = __shfl_sync(~0u, ks_now, 16 * u + 8 * r + g);
+                            vs[u][r] = __shfl_sync(~0u, vs_now, 16 * u + 8 * r + g);
+                            lv[u][r] = fmaxf(lg2(vs[u][r]), -120.f);
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                x2[u][j][2 * r + c] *= F8 ? ks * qmul[j][c] : qmul[j][c];
                     }
+                const bool partly = tok + kTok - 1 > n - p.rows ||
+                                    (p.window && tok < n - p.window) || there + 1 != 1u << kSubs;
+                if (partly) {
+#pragma unroll
+                    for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int token = tok + 16 * u + g + c / 2 * 8, last = pos[j][c % 2];
+                                if (token > last || (p.window && token <= last - p.window) ||
+                                    !(there >> u & 1))
+                                    x2[u][j][c] = -INFINITY;
+                            }
                 }
-                const bool partly = tok + kTile - 1 > n - p.rows ||
-                                    (p.window && tok < n - p.window);
-                float x2[NT][4];
                 bool up = false;
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float by = F8 ? ks[c / 2] * qmul[j][c % 2] : qmul[j][c % 2];
-                        x2[j][c] = (acc[j][0][c] + acc[j][1][c]) * by;
-                    }
-                if (partly) {
+                for (int u = 0; u < kSubs; ++u)
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const int token = tok + g + c / 2 * 8, last = pos[j][c % 2];
-                            if (token > last || (p.window && token <= last - p.window))
-                                x2[j][c] = -INFINITY;
+                            up |= x2[u][j][c] > top[j][c % 2] + kSlack;
+                            if (F8) up |= x2[u][j][c] + lv[u][c / 2] > otop[j][c % 2] + kSlack;
                         }
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        up |= x2[j][c] > top[j][c % 2] + kSlack;
-                        if (F8) up |= x2[j][c] + lv[c / 2] > otop[j][c % 2] + kSlack;
-                    }
                 if (__any_sync(~0u, up)) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float a = fmaxf(x2[j][c], x2[j][c + 2]);
-                            float b = fmaxf(x2[j][c] + lv[0], x2[j][c + 2] + lv[1]);
+                            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                            for (int u = 0; u < kSubs; ++u) {
+                                a = fmaxf(a, fmaxf(x2[u][j][c], x2[u][j][c + 2]));
+                                b = fmaxf(b, fmaxf(x2[u][j][c] + lv[u][0], x2[u][j][c + 2] + lv[u][1]));
+                            }
 #pragma unroll
                             for (int d = 4; d < 32; d *= 2) {
                                 a = fmaxf(a, __shfl_xor_sync(~0u, a, d));
@@ -549,36 +603,42 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                 }
 
                 // weights
-                uint32_t ph[NT][2], pl[NT][2];
+                uint32_t ph[kSubs][NT][2], pl[kSubs][NT][2];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float w[4];
+                for (int u = 0; u < kSubs; ++u)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float from = top[j][c % 2] == -INFINITY ? 0.f : top[j][c % 2];
-                        w[c] = ex2(x2[j][c] - from);
-                        sums[j][c % 2] += w[c];
-                        // a token that is not seen weighs 0 whatever its scale holds
-                        if (F8)
-                            w[c] = x2[j][c] == -INFINITY ? 0.f : w[c] * (vs[c / 2] * lift[j][c % 2]);
-                    }
+                    for (int j = 0; j < NT; ++j) {
+                        float w[4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t hi = pair<TYPE>(w[2 * r], w[2 * r + 1]);
-                        ph[j][r] = transposed(hi);
-                        if (two) {
-                            const float2 h = unpair<TYPE>(hi);
-                            pl[j][r] = transposed(pair<TYPE>(w[2 * r] - h.x, w[2 * r + 1] - h.y));
+                        for (int c = 0; c < 4; ++c) {
+                            const float from = top[j][c % 2] == -INFINITY ? 0.f : top[j][c % 2];
+                            w[c] = ex2(x2[u][j][c] - from);
+                            sums[j][c % 2] += w[c];
+                            // a token that is not seen weighs 0 whatever its scale holds
+                            if (F8)
+                                w[c] = x2[u][j][c] == -INFINITY
+                                           ? 0.f
+                                           : w[c] * (vs[u][c / 2] * lift[j][c % 2]);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t hi = pair<TYPE>(w[2 * r], w[2 * r + 1]);
+                            ph[u][j][r] = transposed(hi);
+                            if (two) {
+                                const float2 h = unpair<TYPE>(hi);
+                                pl[u][j][r] =
+                                    transposed(pair<TYPE>(w[2 * r] - h.x, w[2 * r + 1] - h.y));
+                            }
                         }
                     }
-                }
 
                 // sums of the values: use(i, fragment of 16 d's and the 16 tokens)
-                auto values = [&](auto use) {
+                auto values = [&](int u, auto use) {
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
                         uint32_t v[4];
-                        load_matrices<true>(v, (at + off_v + k / 4 * 2048) ^ (k % 4 * 32));
+                        load_matrices<true>(v, (at + off_v + u * S::kSub + k / 4 * 2048) ^
+                                                   (k % 4 * 32));
                         if constexpr (F8) {
                             // pairs of d's of two tokens -> pairs of tokens of two d's
 #pragma unroll
@@ -595,60 +655,77 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                     }
                 };
                 if (!partly) {
-                    values([&](int i, const uint32_t (&f)[4]) {
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            mma<TYPE>(o[i][j], f, ph[j][0], ph[j][1]);
-                            if (two) mma<TYPE>(o[i][j], f, pl[j][0], pl[j][1]);
-                        }
-                    });
+                    for (int u = 0; u < kSubs; ++u)
+                        values(u, [&](int i, const uint32_t (&f)[4]) {
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                mma<TYPE>(o[i][j], f, ph[u][j][0], ph[u][j][1]);
+                                if (two) mma<TYPE>(o[i][j], f, pl[u][j][0], pl[u][j][1]);
+                            }
+                        });
                 } else {
                     // Values that no row sees are taken out: 0 times what lies there
                     // may be NaN.  Where a value that some rows see and others do not
                     // is none, row by row, with the values that each sees.
-                    uint32_t any[2] = {0, 0}, some[2] = {0, 0};
+#pragma unroll 1
+                    for (int u = 0; u < kSubs; ++u) {
+                        if (!(there >> u & 1)) continue;
+                        uint32_t any[2] = {0, 0}, some[2] = {0, 0}, p0[NT][2], p1[NT][2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int token = tok + 2 * t + (i & 1) + (i & 2) * 4;
-                        const uint32_t bits = i & 1 ? 0xFFFF0000u : 0xFFFFu;
-                        if (token < n && !(p.window && token <= n - p.rows - p.window)) {
-                            any[i / 2] |= bits;
-                            if (token > n - p.rows || (p.window && token < n - p.window))
-                                some[i / 2] |= bits;
-                        }
-                    }
-                    uint32_t odd = 0;
-                    if (p.rows > 1)
-                        values([&](int, const uint32_t (&f)[4]) {
-                            odd |= not_finite<TYPE>(f[0] & some[0]) | not_finite<TYPE>(f[1] & some[0]) |
-                                   not_finite<TYPE>(f[2] & some[1]) | not_finite<TYPE>(f[3] & some[1]);
-                        });
-                    const bool each = __any_sync(~0u, odd != 0);
-                    for (int r = 0; r < (each ? p.rows : 1); ++r) {
-                        const int last = n - p.rows + r;
-                        uint32_t keep[2] = {any[0], any[1]};
-                        if (each) {
-                            keep[0] = keep[1] = 0;
+                        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int token = tok + 2 * t + (i & 1) + (i & 2) * 4;
-                                if (token <= last && !(p.window && token <= last - p.window))
-                                    keep[i / 2] |= i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                            for (int r = 0; r < 2; ++r) {
+                                p0[j][r] = u ? ph[kSubs - 1][j][r] : ph[0][j][r];
+                                if (two) p1[j][r] = u ? pl[kSubs - 1][j][r] : pl[0][j][r];
+                            }
+                        const int tok_u = tok + 16 * u + 2 * t;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int token = tok_u + (i & 1) + (i & 2) * 4;
+                            const uint32_t bits = i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                            if (token < n && !(p.window && token <= n - p.rows - p.window)) {
+                                any[i / 2] |= bits;
+                                if (token > n - p.rows || (p.window && token < n - p.window))
+                                    some[i / 2] |= bits;
                             }
                         }
-                        values([&](int i, const uint32_t (&f)[4]) {
-                            const uint32_t a[4] = {f[0] & keep[0], f[1] & keep[0], f[2] & keep[1],
-                                                   f[3] & keep[1]};
+                        uint32_t odd = 0;
+                        if (p.rows > 1)
+                            values(u, [&](int, const uint32_t (&f)[4]) {
+                                odd |= not_finite<TYPE>(f[0] & some[0]) |
+                                       not_finite<TYPE>(f[1] & some[0]) |
+                                       not_finite<TYPE>(f[2] & some[1]) |
+                                       not_finite<TYPE>(f[3] & some[1]);
+                            });
+                        const bool each = __any_sync(~0u, odd != 0);
+#pragma unroll 1
+                        for (int r = 0; r < (each ? p.rows : 1); ++r) {
+                            const int last = n - p.rows + r;
+                            uint32_t keep[2] = {any[0], any[1]};
+                            if (each) {
+                                keep[0] = keep[1] = 0;
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma<TYPE>(d, a, ph[j][0], ph[j][1]);
-                                if (two) mma<TYPE>(d, a, pl[j][0], pl[j][1]);
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    if (!each || pos[j][c % 2] == last) o[i][j][c] += d[c];
+                                for (int i = 0; i < 4; ++i) {
+                                    const int token = tok_u + (i & 1) + (i & 2) * 4;
+                                    if (token <= last && !(p.window && token <= last - p.window))
+                                        keep[i / 2] |= i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                                }
                             }
-                        });
+                            values(u, [&](int i, const uint32_t (&f)[4]) {
+                                const uint32_t a[4] = {f[0] & keep[0], f[1] & keep[0],
+                                                       f[2] & keep[1], f[3] & keep[1]};
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) {
+                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma<TYPE>(d, a, p0[j][0], p0[j][1]);
+                                    if (two) mma<TYPE>(d, a, p1[j][0], p1[j][1]);
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+                                        if (!each || pos[j][c % 2] == last) o[i][j][c] += d[c];
+                                }
+                            });
+                        }
                     }
                 }
                 __syncwarp();                  // the stage may be filled again
@@ -769,22 +846,22 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     // an item with one share here, all of it, was written by its warp: it has none
     const uint32_t need = __ballot_sync(~0u, lane == from && those != 0);
     const int groups = __popc(need);
-    // what each share's rows are worth: to the common maximum, or in the end
     float *const blocks_out = blocks_at + 2 * blockIdx.x * (int64_t)S::kPart;
+    // what each share's rows are worth: to the common maximum, or in the end
 #pragma unroll 1
     for (int m = warp; m < M; m += W) {
         const float top = there ? stats[lane][0][m] : -INFINITY, l = there ? stats[lane][1][m] : 0.f,
                     otop = there ? stats[lane][2][m] : -INFINITY;
         float tall = top, oall = otop;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {             // to the end of the item's shares
+        for (int d = 1; d < 2 * W; d *= 2) {          // to the end of the item's shares
             const float a = __shfl_down_sync(~0u, tall, d), b = __shfl_down_sync(~0u, oall, d);
             if (lane + d <= to) tall = fmaxf(tall, a), oall = fmaxf(oall, b);
         }
         tall = __shfl_sync(~0u, tall, from), oall = __shfl_sync(~0u, oall, from);
         float sum_l = there ? l * ex2(top - finite(tall)) : 0.f;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
+        for (int d = 1; d < 2 * W; d *= 2) {
             const float a = __shfl_down_sync(~0u, sum_l, d);
             if (lane + d <= to) sum_l += a;
         }
@@ -813,19 +890,19 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
 #pragma unroll 1
         for (int i = (warp % slices * 32 + lane) * 4; i < M * D; i += slices * 128) {
             float v[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t left = bits;
-#pragma unroll 4
-            for (int n = __popc(bits); n; --n) {
-                const int e = __ffs(left) - 1;
-                left &= left - 1;
-                const float *part =
-                    e & 1 ? reinterpret_cast<const float *>(smem + e / 2 * (kStages * S::kStage))
-                          : heads_at + (int64_t)(e / 2) * S::kPart;
+            auto add = [&](const float *part, int e) {
                 const float4 u = *reinterpret_cast<const float4 *>(part + i);
                 const float4 f = *reinterpret_cast<const float4 *>(&worth_of[e][i % M]);
                 v[0] = fmaf(u.x, f.x, v[0]), v[1] = fmaf(u.y, f.y, v[1]);
                 v[2] = fmaf(u.z, f.z, v[2]), v[3] = fmaf(u.w, f.w, v[3]);
-            }
+            };
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if (bits >> (2 * w + 1) & 1)
+                    add(reinterpret_cast<const float *>(smem + w * (kStages * S::kStage)), 2 * w + 1);
+            // the warp that ended the item and went on: at most one
+            const int e = __ffs(bits & 0x55555555u) - 1;
+            if (e >= 0) add(heads_at + (int64_t)(e / 2) * S::kPart, e);
             if (here)
                 store(x, i, v);
             else
@@ -842,17 +919,20 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     const bool from_before = head.start < cs, goes_on = back.start >= cs && back.end() > ce;
     const int crosses = (from_before ? 1 : 0) + (goes_on ? 1 : 0);
     if (!crosses) return;
-    float *const all = reinterpret_cast<float *>(smem);        // the ring is free
     // counters by a block that no other item has in this place: the one where the
     // item begins, or where one of its groups does
     uint32_t *const counters = p.counters + mb * gridDim.x;
+    // true for the last; what the blocks wrote before their barrier is then visible
     auto arrive = [&](uint32_t *counter, int parts) {
-        __threadfence();
-        const bool last =
-            parts == 1 || atomicInc(counter, parts - 1) == (uint32_t)parts - 1;
-        __threadfence();
-        return last;
+        uint32_t before = 0;
+        if (parts > 1)
+            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                         : "=r"(before)
+                         : "l"(counter), "r"(parts - 1)
+                         : "memory");
+        return before == (uint32_t)parts - 1;
     };
+    float *const all = reinterpret_cast<float *>(smem);        // the ring is free
     auto crossing = [&](int k) { return from_before && k == 0 ? head : back; };
     __syncthreads();
     if ((int)threadIdx.x < crosses) {
@@ -923,8 +1003,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                     *reinterpret_cast<float4 *>(part(0) + S::kStats + i) =
                         make_float4(v[0], v[1], v[2], v[3]);
             }
-            __syncthreads();
             if (whole) break;
+            __syncthreads();
             parts = groups, from = c0, step = kJoin;
             if (threadIdx.x == 0) joined[k] = arrive(counters + c0 + 512, parts);
             __syncthreads();
@@ -951,21 +1031,22 @@ cudaError_t launch(AttendParams p, cudaStream_t st) {
     }
     TensorMap kmap, vmap;
     const int64_t rows = (int64_t)p.heads * p.page;
+    p.wide = p.page % S::kTok == 0;
     if ((e = status_word(&p.status)) != cudaSuccess ||
-        (e = make_cache_map(&kmap, p.k, S::kRow, rows, p.k_stride * S::kSize, p.pages)) !=
-            cudaSuccess ||
-        (e = make_cache_map(&vmap, p.v, S::kRow, rows, p.v_stride * S::kSize, p.pages)) !=
-            cudaSuccess)
+        (e = make_cache_map(&kmap, p.k, S::kRow, p.wide ? S::kTok : 16, rows,
+                            p.k_stride * S::kSize, p.pages)) != cudaSuccess ||
+        (e = make_cache_map(&vmap, p.v, S::kRow, p.wide ? S::kTok : 16, rows,
+                            p.v_stride * S::kSize, p.pages)) != cudaSuccess)
         return e;
     // no more blocks than there can be tiles for their warps
-    int64_t tiles = (int64_t)p.width * p.page / kTile;
-    if (p.window && (p.window + p.rows) / kTile + 2 < tiles) tiles = (p.window + p.rows) / kTile + 2;
+    int64_t tiles = (int64_t)p.width * p.page / S::kTok + 1;
+    if (p.window && (p.window + p.rows) / S::kTok + 2 < tiles)
+        tiles = (p.window + p.rows) / S::kTok + 2;
     const int64_t most = (tiles * p.batch * p.heads + S::kWarps - 1) / S::kWarps;
     const int grid = attend_grid(p.blocks);
     p.by_grid = Divisor((uint32_t)(most < grid ? most : grid));
-    kernel<<<dim3(p.by_grid.d, p.blocks), S::kWarps * 32, S::smem(p.batch), st>>>(
-        kmap, vmap, p);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(p.by_grid.d, p.blocks), S::kWarps * 32, S::smem(p.batch), 1, st,
+                        kmap, vmap, p);
 }
 template <int TYPE>
 cudaError_t launch_type(const AttendParams &p, int dim, cudaStream_t st) {

@@ -112,6 +112,8 @@ template <int CACHE, int IN>
 __global__ void __launch_bounds__(256) write_kernel(const CacheParams p) {
     using T = typename TypeOf<IN>::T;
     const Place at(p);
+    pdl_trigger();
+    pdl_wait();
     // the lanes of a row are all there or none is; those beyond the last token
     // take part in the shuffles
     Eight<T> raw[2][2] = {};
@@ -171,6 +173,8 @@ __global__ void __launch_bounds__(256) read_kernel(const CacheParams p) {
     using C = typename TypeOf<CACHE>::T;
     using T = typename TypeOf<OUT>::T;
     const Place at(p);
+    pdl_trigger();
+    pdl_wait();
     if (!at.live) return;
     uint32_t page, in_page;
     const bool got = at.row(p, __ldg(p.slots_of + at.token), &page, &in_page);
@@ -216,8 +220,7 @@ __global__ void __launch_bounds__(256) read_kernel(const CacheParams p) {
 template <typename K>
 cudaError_t launch(K kernel, const CacheParams &p, cudaStream_t st) {
     const int64_t threads = (int64_t)p.tokens * p.heads << p.lanes_log2;
-    kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3((unsigned)((threads + 255) / 256)), 256, 0, 1, st, p);
 }
 
 }  // namespace

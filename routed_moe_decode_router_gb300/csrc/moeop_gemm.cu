@@ -832,9 +832,9 @@ int split_of(const Dev &d, int64_t tiles, int kb) {
 }  // namespace
 
 // Map of one array of a paged cache: `rows` rows of row_bytes (64, or a multiple
-// of 128) to a page, in tiles of 16 rows.  A tile lies in shared memory as
-// columns of 16 rows x (up to) 128 bytes, swizzled.
-cudaError_t make_cache_map(TensorMap *m, const void *p, int row_bytes, int64_t rows,
+// of 128) to a page, in tiles of box_rows.  A tile lies in shared memory as
+// columns of box_rows x (up to) 128 bytes, swizzled.
+cudaError_t make_cache_map(TensorMap *m, const void *p, int row_bytes, int box_rows, int64_t rows,
                            int64_t page_bytes, int64_t pages) {
     Dev *d;
     const cudaError_t e = device(&d);
@@ -842,7 +842,7 @@ cudaError_t make_cache_map(TensorMap *m, const void *p, int row_bytes, int64_t r
     const cuuint32_t width = row_bytes < 128 ? 64 : 128, cols = row_bytes / width;
     const cuuint64_t dims[4] = {width, (cuuint64_t)rows, cols, (cuuint64_t)pages};
     const cuuint64_t strides[3] = {(cuuint64_t)row_bytes, width, (cuuint64_t)page_bytes};
-    const cuuint32_t box[4] = {width, 16, cols, 1}, elem[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {width, (cuuint32_t)box_rows, cols, 1}, elem[4] = {1, 1, 1, 1};
     const CUresult r = g_encode(
         reinterpret_cast<CUtensorMap *>(m), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
         const_cast<void *>(p), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -194,6 +194,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
     __shared__ uint64_t warp_total[kWarps], block_total;
     const int blocks = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
     const int b = blockIdx.x / blocks, lane = threadIdx.x % 32, n = p.c.drafts;
+    pdl_trigger();
+    pdl_wait();
     // lane i decides about draft i; every warp does, which saves a barrier
     int x = -1;
     bool good = false;
@@ -231,17 +233,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
 }  // namespace
 
 cudaError_t launch_verify_draft(const VerifyParams &p, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    cfg.gridDim = dim3((unsigned)p.c.batch * kBlocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kBlocks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel, p);
+    return launch_early(verify_kernel, dim3((unsigned)p.c.batch * kBlocks), kThreads, 0, kBlocks, st,
+                        p);
 }
 
 }  // namespace op
