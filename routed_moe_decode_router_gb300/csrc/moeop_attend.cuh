@@ -73,11 +73,15 @@ struct Shape {
     static constexpr int smem(int batch) { return 1024 + kRing + (2 * batch + 1) * 4; }
     static constexpr int kSteps = kRow / 32;              // 32 bytes of a row: an MMA's
     static constexpr int kWhole = 1536 / kTok;
-    static_assert(M * D * 4 <= kStages * kStage, "a share's sums lie in its warp's ring");
+    static_assert(2 * M * D * 4 <= kStages * kStage, "two shares' sums lie in their warp's ring");
     static_assert(kWarps <= 16, "two shares of each warp: a lane for each");
     static_assert(kStage % 1024 == 0 && kSub % 1024 == 0, "the swizzle's period");
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -144,13 +148,14 @@ struct alignas(16) Item {
     int b, h, tiles;      // sequence, head, tiles of the item
     int start;            // its first tile among all
     Item() = default;
-    // the item of tile x; first: tiles of the sequences before each, for one head
+    // the item of tile x (the same in all lanes); first: tiles of the sequences before
+    // each, for one head.  A warp looks at 32 of them at a time.
     __device__ __forceinline__ Item(const int *first, int heads, int batch, int x) {
-        int lo = 0, hi = batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (first[mid] * heads <= x) lo = mid;
-            else hi = mid;
+        const int lane = threadIdx.x % 32;
+        int lo = 0;
+        for (int step = batch > 1024 ? 1024 : batch > 32 ? 32 : 1; step; step /= 32) {
+            const int at = lo + lane * step;
+            lo += (__popc(__ballot_sync(~0u, at < batch && first[at] * heads <= x)) - 1) * step;
         }
         b = lo;
         tiles = first[lo + 1] - first[lo];
@@ -264,10 +269,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     else __syncthreads();
     const int tiles = sum * p.heads;
     const Shares shares(tiles, p.by_grid);
-    // one lane for either end
-    const int end_of = cut(first, p.heads, p.batch, tiles, S::kWhole,
-                           shares.begin(blockIdx.x + (lane & 1)));
-    const int cs = __shfl_sync(~0u, end_of, 0), ce = __shfl_sync(~0u, end_of, 1);
+    const int cs = cut(first, p.heads, p.batch, tiles, S::kWhole, shares.begin(blockIdx.x)),
+              ce = cut(first, p.heads, p.batch, tiles, S::kWhole, shares.begin(blockIdx.x + 1));
     if (cs >= ce) return;
     // equal shares for the block's warps
     const int used = min(W, ce - cs), warp_each = (ce - cs) / W, warp_more = (ce - cs) % W;
@@ -803,6 +806,15 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             }
         }
         if (lane == 0) lasts[warp] = it;
+        // what the warp has of the item it did not begin follows into the ring
+        if (has & 1) {
+            const float *from = heads_at + (int64_t)warp * S::kPart;
+            __syncwarp();
+#pragma unroll 1
+            for (int i = lane * 4; i < M * D; i += 128)
+                copy16(ring_addr + (M * D + i) * 4, from + i);
+            copies_wait();
+        }
     }
     if (lane == 0) shares_of[warp] = has;
     __syncthreads();
@@ -845,7 +857,6 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     const uint32_t those = present >> from & ((2u << (to - from)) - 1);
     // an item with one share here, all of it, was written by its warp: it has none
     const uint32_t need = __ballot_sync(~0u, lane == from && those != 0);
-    const int groups = __popc(need);
     float *const blocks_out = blocks_at + 2 * blockIdx.x * (int64_t)S::kPart;
     // what each share's rows are worth: to the common maximum, or in the end
 #pragma unroll 1
@@ -874,12 +885,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         }
     }
     __syncthreads();
-    // the warps share the items out
-    const int slices = groups > 0 && groups < W ? W / groups : 1;
-#pragma unroll 1
-    for (int k = warp / slices; k < groups; k += W / slices) {
-        uint32_t rest = need;
-        for (int i = 0; i < k; ++i) rest &= rest - 1;
+    for (uint32_t rest = need; rest; rest &= rest - 1) {
         const int e0 = __ffs(rest) - 1;
         const bool here = __shfl_sync(~0u, inside ? 1 : 0, e0);
         const uint32_t bits = __shfl_sync(~0u, those, e0) << e0;
@@ -888,21 +894,20 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         x.start = __shfl_sync(~0u, mine.start, e0);
         float *const out = blocks_out + (x.start >= cs ? S::kPart : 0) + S::kStats;
 #pragma unroll 1
-        for (int i = (warp % slices * 32 + lane) * 4; i < M * D; i += slices * 128) {
+        for (int i = threadIdx.x * 4; i < M * D; i += W * 128) {
             float v[4] = {0.f, 0.f, 0.f, 0.f};
-            auto add = [&](const float *part, int e) {
-                const float4 u = *reinterpret_cast<const float4 *>(part + i);
+            uint32_t left = bits;
+#pragma unroll 4
+            for (int n = __popc(bits); n; --n) {
+                const int e = __ffs(left) - 1;
+                left &= left - 1;
+                // a warp's last item, and behind it the one that another began
+                const float4 u = *reinterpret_cast<const float4 *>(
+                    smem + e / 2 * (kStages * S::kStage) + ((~e & 1) * M * D + i) * 4);
                 const float4 f = *reinterpret_cast<const float4 *>(&worth_of[e][i % M]);
                 v[0] = fmaf(u.x, f.x, v[0]), v[1] = fmaf(u.y, f.y, v[1]);
                 v[2] = fmaf(u.z, f.z, v[2]), v[3] = fmaf(u.w, f.w, v[3]);
-            };
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                if (bits >> (2 * w + 1) & 1)
-                    add(reinterpret_cast<const float *>(smem + w * (kStages * S::kStage)), 2 * w + 1);
-            // the warp that ended the item and went on: at most one
-            const int e = __ffs(bits & 0x55555555u) - 1;
-            if (e >= 0) add(heads_at + (int64_t)(e / 2) * S::kPart, e);
+            }
             if (here)
                 store(x, i, v);
             else
