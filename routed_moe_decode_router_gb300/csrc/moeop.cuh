@@ -163,6 +163,7 @@ struct AttendParams {
     float *parts;              // sums of a warp's or thread block's share of an item
     uint32_t *status;
     bool wide;                 // a tile never leaves its page
+    bool apart;                // a kernel of its own joins what blocks have of an item
 };
 // Query rows (row, head of the group) that a thread block takes together.
 constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 16; }

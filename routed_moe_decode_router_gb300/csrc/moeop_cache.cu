@@ -83,6 +83,40 @@ __device__ __forceinline__ void narrow(const float (&v)[8], Eight<float> &r) {
     for (int i = 0; i < 8; ++i) r.u[i] = __float_as_uint(v[i]);
 }
 
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// Fp8Scale::over of two numbers at a time.
+__device__ __forceinline__ float2 over2(const Fp8Scale &s, float a, float b) {
+    const uint64_t v = pair(a, b), recip = pair(s.recip, s.recip), q = mul2(v, recip);
+    const uint64_t r = fma2(fma2(q, pair(-s.divisor, -s.divisor), v), recip, q);
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+    return f;
+}
+__device__ __forceinline__ uint32_t codes(const Fp8Scale &s, const float *v) {
+    const float2 a = over2(s, v[0], v[1]), b = over2(s, v[2], v[3]);
+    return pack_e4m3x4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float largest(const float (&v)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+
 // Where a thread works: 8 elements at `col` and 8 at `col` + dim / 2 of a head's
 // row of a token.
 struct Place {
@@ -109,7 +143,7 @@ struct Place {
 };
 
 template <int CACHE, int IN>
-__global__ void __launch_bounds__(256) write_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(256, IN == MOEOP_FP32 ? 4 : 5) write_kernel(const CacheParams p) {
     using T = typename TypeOf<IN>::T;
     const Place at(p);
     pdl_trigger();
@@ -146,8 +180,7 @@ __global__ void __launch_bounds__(256) write_kernel(const CacheParams p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 widen(raw[s][h], v[h]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[h][i]));
+                amax = fmaxf(amax, largest(v[h]));
             }
             for (int o = (1 << p.lanes_log2) / 2; o; o >>= 1)
                 amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
@@ -157,8 +190,7 @@ __global__ void __launch_bounds__(256) write_kernel(const CacheParams p) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     *reinterpret_cast<uint2 *>(y + h * at.half) =
-                        make_uint2(q.codes(v[h][0], v[h][1], v[h][2], v[h][3]),
-                                   q.codes(v[h][4], v[h][5], v[h][6], v[h][7]));
+                        make_uint2(codes(q, v[h]), codes(q, v[h] + 4));
                 if (at.col == 0)
                     (s ? p.v_scales : p.k_scales)[(int64_t)page * (s ? p.v_scales_stride
                                                                      : p.k_scales_stride) +

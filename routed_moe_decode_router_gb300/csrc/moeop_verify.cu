@@ -17,7 +17,7 @@
 // So weights are counted in steps of 2^-44, in whole numbers, whose sums are
 // exact in any order.  64-bit floating point would do too, but an SM adds two a
 // cycle; whole numbers come out of fp32 additions of a constant whose last bit
-// is the step wanted (its sum's lower bits are the number), all at full rate.
+// is the step wanted (its sum's lower bits are the number), two at a time.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -31,33 +31,59 @@ namespace op {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBlocks = 8;
+constexpr int kMaxWarps = 16, kBlocks = 8;
 
-// w in [0, 1] as hi 2^-22 + lo 2^-44, rounded to the nearest: the lower bits of
-// w + 3 (last bit 2^-22) and of what it left + 3 * 2^-22 (last bit 2^-44).
-__device__ __forceinline__ void steps(float w, int &hi, int &lo) {
-    constexpr float c1 = 3.f, c2 = 3.f / (1 << 22);
-    w = fminf(fmaxf(w, 0.f), 1.f);  // NaN: 0
-    const float t = w + c1;
-    hi = __float_as_int(t) - __float_as_int(c1);
-    lo = __float_as_int(w - (t - c1) + c2) - __float_as_int(c2);
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
-// The weight of an id in steps of 2^-44: p, or what p has more than q.
-template <bool REST>
-__device__ __forceinline__ uint64_t weight(float p, float q) {
-    int hi, lo;
-    steps(p, hi, lo);
-    int64_t n = ((int64_t)hi << 22) + lo;
-    if (REST) {
-        steps(q, hi, lo);
-        n -= ((int64_t)hi << 22) + lo;
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t both(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ int low(uint64_t v) { return (int)(uint32_t)v; }
+__device__ __forceinline__ int high(uint64_t v) { return (int)(v >> 32); }
+
+// What weights count so far: hi 2^-22 + lo 2^-44.  A lane's share is at most 128 of
+// them (2^19 ids, 8 blocks of 512 lanes), and both stay below 2^30.
+struct Count {
+    int hi = 0, lo = 0;
+    // The weight of an id: p, or what p has more than q.  A number w in [0, 1] is
+    // rounded to whole steps: the lower bits of w + 3 (last bit 2^-22), and of what
+    // that left + 3 * 2^-22 (last bit 2^-44).  p and q go together, and the
+    // constants fall away in their difference.
+    template <bool REST>
+    __device__ __forceinline__ void add(float p, float q) {
+        constexpr float c1 = 3.f, c2 = 3.f / (1 << 22);
+        p = __saturatef(p), q = REST ? __saturatef(q) : 0.f;   // NaN: 0
+        const uint64_t w = both(p, q), t = add2(w, both(c1, c1));
+        const uint64_t left = fma2(add2(t, both(-c1, -c1)), both(-1.f, -1.f), w);
+        const uint64_t l = add2(left, both(c2, c2));
+        if (!REST || p > q) hi += low(t) - high(t), lo += low(l) - high(l);
     }
-    return n > 0 ? (uint64_t)n : 0;
-}
+    __device__ __forceinline__ uint64_t steps() const {
+        return (uint64_t)(((int64_t)hi << 22) + lo);
+    }
+};
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const uint64_t left = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += left;
+    }
     return v;
 }
 
@@ -66,13 +92,12 @@ struct Row {
     int refused;         // without q: the id that is certain to have been drafted; -1: none
     int vocab;
     template <bool REST>
-    __device__ __forceinline__ uint64_t at(int i) const {
-        if (i >= vocab) return 0;
-        return weight<REST>(__ldg(p + i), !REST ? 0.f : q ? __ldg(q + i) : i == refused ? 1.f : 0.f);
+    __device__ __forceinline__ void at(int i, Count &c) const {
+        c.add<REST>(__ldg(p + i), !REST ? 0.f : q ? __ldg(q + i) : i == refused ? 1.f : 0.f);
     }
     // Ids i .. i + 3, p and q on 16 bytes.
     template <bool REST>
-    __device__ __forceinline__ uint64_t four(int i, uint64_t (&w)[4]) const {
+    __device__ __forceinline__ void four(int i, Count &c) const {
         const float4 a = __ldg(reinterpret_cast<const float4 *>(p + i));
         float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
         if (REST && q) b = __ldg(reinterpret_cast<const float4 *>(q + i));
@@ -80,73 +105,55 @@ struct Row {
             b.x = i == refused, b.y = i + 1 == refused;
             b.z = i + 2 == refused, b.w = i + 3 == refused;
         }
-        w[0] = weight<REST>(a.x, b.x), w[1] = weight<REST>(a.y, b.y);
-        w[2] = weight<REST>(a.z, b.z), w[3] = weight<REST>(a.w, b.w);
-        return w[0] + w[1] + w[2] + w[3];
+        c.add<REST>(a.x, b.x), c.add<REST>(a.y, b.y), c.add<REST>(a.z, b.z), c.add<REST>(a.w, b.w);
     }
 };
 
-// Sum of a lane's share of the ids from i0 to i1 (a multiple of 4 apart from
-// vocab itself).
+// A lane's share of the ids from i0 to i1 (multiples of 4 apart from vocab itself).
 template <bool REST, bool VEC>
 __device__ __forceinline__ uint64_t sum_piece(const Row &r, int i0, int i1, int lane) {
-    uint64_t s = 0;
+    Count c;
     if (VEC) {
 #pragma unroll 4
-        for (int i = i0 + lane * 4; i < i1; i += 128) {
-            uint64_t w[4];
-            s += r.four<REST>(i, w);
-        }
+        for (int i = i0 + lane * 4; i < i1; i += 128) r.four<REST>(i, c);
     } else {
 #pragma unroll 8
-        for (int i = i0 + lane; i < i1; i += 32) s += r.at<REST>(i);
+        for (int i = i0 + lane; i < i1; i += 32) r.at<REST>(i, c);
     }
-    return s;
+    return c.steps();
 }
 
-// The lowest id from i0 to i1 whose running sum exceeds `target`; the sum of
-// all of them does.
-template <bool REST, bool VEC>
+// The lowest id from i0 to i1 whose running sum exceeds `target`; the sum of all of
+// them does.  First the lane in whose part of them it is, then the id.
+template <bool REST>
 __device__ __forceinline__ int find(const Row &r, int i0, int i1, uint64_t target, int lane) {
-    constexpr int kEach = VEC ? 4 : 1;
-    uint64_t before = 0;
-    for (int i = i0; i < i1; i += 32 * kEach) {
-        uint64_t w[4] = {0, 0, 0, 0};
-        const int own = i + lane * kEach;
-        uint64_t s = 0;
-        if (own < i1) s = VEC ? r.four<REST>(own, w) : r.at<REST>(own);
-        if (!VEC) w[0] = s;
-        uint64_t run = s;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const uint64_t left = __shfl_up_sync(~0u, run, o);
-            if (lane >= o) run += left;
-        }
-        const unsigned over = __ballot_sync(~0u, before + run > target);
-        if (over) {
-            const int who = __ffs(over) - 1;
-            int id = own;
-            uint64_t c = before + run - s;
-#pragma unroll
-            for (int j = 0; j < kEach - 1; ++j) {
-                c += w[j];
-                if (c <= target && id == own + j) id = own + j + 1;
-            }
-            return __shfl_sync(~0u, id, who);
-        }
-        before += __shfl_sync(~0u, run, 31);
+    const int each = (i1 - i0 + 31) / 32;
+    Count c;
+#pragma unroll 8
+    for (int i = i0 + lane * each; i < min(i0 + (lane + 1) * each, i1); ++i) r.at<REST>(i, c);
+    uint64_t run = warp_scan(c.steps(), lane);
+    int who = __ffs(__ballot_sync(~0u, run > target)) - 1;
+    target -= __shfl_sync(~0u, run - c.steps(), who);
+    const int from = i0 + who * each, to = min(from + each, i1);
+    for (int i = from;; i += 32) {
+        Count one;
+        if (i + lane < to) r.at<REST>(i + lane, one);
+        run = warp_scan(one.steps(), lane);
+        const unsigned over = __ballot_sync(~0u, run > target);
+        if (over) return i + __ffs(over) - 1;
+        if (i + 32 >= to) return to - 1;  // not reached
+        target -= __shfl_sync(~0u, run, 31);
     }
-    return -1;  // not reached
 }
 
 template <bool VEC>
 __device__ __forceinline__ void draw(const VerifyParams &p, const Row &row, bool rest, int b,
                                      int accepted, uint64_t *warp_total, uint64_t *block_total) {
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), blocks = cluster.num_blocks();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int rank = cluster.block_rank();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     // equal pieces of whole fours, one for each warp of the cluster
-    const int fours = (p.c.vocab + 3) / 4, pieces = blocks * kWarps, piece = rank * kWarps + warp;
+    const int fours = (p.c.vocab + 3) / 4, pieces = kBlocks * warps, piece = rank * warps + warp;
     const int i0 = (int)((int64_t)fours * piece / pieces) * 4;
     const int i1 = min((int)((int64_t)fours * (piece + 1) / pieces) * 4, p.c.vocab);
     uint64_t before, total;
@@ -156,44 +163,39 @@ __device__ __forceinline__ void draw(const VerifyParams &p, const Row &row, bool
         s = warp_sum(s);
         if (lane == 0) warp_total[warp] = s;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            uint64_t t = 0;
-            for (int w = 0; w < kWarps; ++w) t += warp_total[w];
-            *block_total = t;
+        if (warp == 0) {
+            const uint64_t t = warp_sum(lane < warps ? warp_total[lane] : 0);
+            if (lane == 0) *block_total = t;
         }
         cluster.sync();
-        before = total = 0;
-        for (int k = 0; k < blocks; ++k) {
-            const uint64_t t = *cluster.map_shared_rank(block_total, k);
-            total += t;
-            if (k < rank) before += t;
-        }
-        cluster.sync();  // block_total may go, or be written again
+        const uint64_t own = lane < kBlocks ? *cluster.map_shared_rank(block_total, lane) : 0;
+        total = warp_sum(own);
+        before = warp_sum(lane < rank ? own : 0);
+        cluster.barrier_arrive();  // block_total was read here
         if (total || !rest) break;
         rest = false;  // p has nowhere more than q
+        cluster.barrier_wait();
     }
     int32_t *out = p.tokens + (size_t)b * (p.c.drafts + 1) + accepted;
-    if (!total) {
-        if (rank == 0 && threadIdx.x == 0) *out = -1;
-        return;
-    }
-    for (int w = 0; w < warp; ++w) before += warp_total[w];
+    if (!total && rank == 0 && threadIdx.x == 0) *out = -1;
+    before += warp_sum(lane < warp ? warp_total[lane] : 0);
     const uint64_t own = warp_total[warp];
     // u * total < total, rounded down: a whole sum exceeds u * total where it
     // exceeds this.  The product is rounded at 2^-53 of itself.
     const float u = fminf(fmaxf(__ldg(p.sample_u + b), 0.f), 1.f - 0x1p-24f);
     const uint64_t target = (uint64_t)((double)u * (double)total);
-    if (own && target >= before && target < before + own) {
-        const int id = rest ? find<true, VEC>(row, i0, i1, target - before, lane)
-                            : find<false, VEC>(row, i0, i1, target - before, lane);
+    if (target >= before && target < before + own) {
+        const int id = rest ? find<true>(row, i0, i1, target - before, lane)
+                            : find<false>(row, i0, i1, target - before, lane);
         if (lane == 0) *out = id;
     }
+    cluster.barrier_wait();        // block_total may go
 }
 
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams p) {
-    __shared__ uint64_t warp_total[kWarps], block_total;
-    const int blocks = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
-    const int b = blockIdx.x / blocks, lane = threadIdx.x % 32, n = p.c.drafts;
+__global__ void __launch_bounds__(kMaxWarps * 32, 2) verify_kernel(const VerifyParams p) {
+    __shared__ uint64_t warp_total[kMaxWarps], block_total;
+    const int rank = cg::this_cluster().block_rank();
+    const int b = blockIdx.x / kBlocks, lane = threadIdx.x % 32, n = p.c.drafts;
     pdl_trigger();
     pdl_wait();
     // lane i decides about draft i; every warp does, which saves a barrier
@@ -201,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
     bool good = false;
     if (lane < n) {
         x = __ldg(p.draft + (size_t)b * n + lane);
+        const float u = __ldg(p.accept_u + (size_t)b * n + lane);
         if ((unsigned)x < (unsigned)p.c.vocab) {
-            const float u = __ldg(p.accept_u + (size_t)b * n + lane);
             const float t =
                 __ldg(p.target + ((size_t)b * (n + 1) + lane) * p.c.target_stride + x);
             const float q = p.draft_probs
@@ -233,7 +235,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
 }  // namespace
 
 cudaError_t launch_verify_draft(const VerifyParams &p, cudaStream_t st) {
-    return launch_early(verify_kernel, dim3((unsigned)p.c.batch * kBlocks), kThreads, 0, kBlocks, st,
+    // 512 threads where the clusters of all sequences run at once (two blocks on each
+    // of 152 SMs), else 256 (four)
+    const int threads = p.c.batch * kBlocks <= 2 * 152 ? 512 : 256;
+    return launch_early(verify_kernel, dim3((unsigned)p.c.batch * kBlocks), threads, 0, kBlocks, st,
                         p);
 }
 
