@@ -26,9 +26,8 @@
 //   its weight: weights are exp(s_j - m) vs_j, so the sums O have a running maximum
 //   of their own, of s_j + log vs_j, and keep the range of f16 whatever the scales.
 //   (mma.sync on e4m3 itself, Q in two e4m3 numbers, takes 80 instructions a tile more.)
-// - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo, but for
-//   e4m3 with bf16 outputs: one f16 number is 2^-12 off, a rounding of the output
-//   up to 2^-9.
+// - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo (one f16
+//   number for e4m3 would be 2^-11 off, and saves no time).
 // - Maxima are raised only where a score exceeds them by 2^8, so that most tiles
 //   need one vote and no reduction.
 // - Join.  A warp's share of an item goes to shared memory (its last item) or to
@@ -242,7 +241,6 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         if (warp == W - 1) tma_prefetch_map(&kmap), tma_prefetch_map(&vmap);
     }
     pdl_wait();
-    pdl_trigger();     // the kernel that joins reads the lengths before it waits
     for (int b0 = 0; b0 < p.batch; b0 += W * 32) {
         const int b = b0 + (few ? lane : threadIdx.x);
         int n = 0, c = 0;
@@ -424,8 +422,6 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                                  : row * 128 + ((col ^ (row % 8)) * 16);
         };
         const uint32_t off_k = offset(row_k, col_k), off_v = S::kHalf + offset(row_v, col_v);
-        // P as one number or two
-        const bool two = !F8 || p.dtype == MOEOP_FP16;
 
         // -------------------------------------------------------------------
         // Items
@@ -634,11 +630,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                         for (int r = 0; r < 2; ++r) {
                             const uint32_t hi = pair<TYPE>(w[2 * r], w[2 * r + 1]);
                             ph[u][j][r] = transposed(hi);
-                            if (two) {
-                                const float2 h = unpair<TYPE>(hi);
-                                pl[u][j][r] =
-                                    transposed(pair<TYPE>(w[2 * r] - h.x, w[2 * r + 1] - h.y));
-                            }
+                            const float2 h = unpair<TYPE>(hi);
+                            pl[u][j][r] =
+                                transposed(pair<TYPE>(w[2 * r] - h.x, w[2 * r + 1] - h.y));
                         }
                     }
 
@@ -671,7 +665,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
                                 mma<TYPE>(o[i][j], f, ph[u][j][0], ph[u][j][1]);
-                                if (two) mma<TYPE>(o[i][j], f, pl[u][j][0], pl[u][j][1]);
+                                mma<TYPE>(o[i][j], f, pl[u][j][0], pl[u][j][1]);
                             }
                         });
                 } else {
@@ -687,7 +681,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 p0[j][r] = u ? ph[kSubs - 1][j][r] : ph[0][j][r];
-                                if (two) p1[j][r] = u ? pl[kSubs - 1][j][r] : pl[0][j][r];
+                                p1[j][r] = u ? pl[kSubs - 1][j][r] : pl[0][j][r];
                             }
                         const int tok_u = tok + 16 * u + 2 * t;
 #pragma unroll
@@ -729,7 +723,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                                 for (int j = 0; j < NT; ++j) {
                                     float d[4] = {0.f, 0.f, 0.f, 0.f};
                                     mma<TYPE>(d, a, p0[j][0], p0[j][1]);
-                                    if (two) mma<TYPE>(d, a, p1[j][0], p1[j][1]);
+                                    mma<TYPE>(d, a, p1[j][0], p1[j][1]);
 #pragma unroll
                                     for (int c = 0; c < 4; ++c)
                                         if (!each || pos[j][c % 2] == last) o[i][j][c] += d[c];
@@ -824,23 +818,33 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         }
     }
     if (lane == 0) shares_of[warp] = has;
+    // The next kernel may come (calls in a row, 9 x 6007: 44 us, so 41); the one that
+    // joins reads the lengths before it waits, and would only take room (32768 tokens
+    // of one sequence 20.1 us, so 19.0).
+    if (!p.apart) pdl_trigger();
     __syncthreads();
 
     // -----------------------------------------------------------------------
     // Join: the block's warps, then the blocks
     // -----------------------------------------------------------------------
-    // Four numbers of O^T, from number i of a partial sum on: d = i / M, rows i % M ..
-    auto store = [&](const Item &x, int i, const float (&v)[4]) {
-        uint16_t *to = static_cast<uint16_t *>(p.out) +
-                       ((int64_t)x.b * p.rows * p.heads + x.h) * p.group * D + i / M;
+    // Four numbers of a partial sum O^T from number i on are of d = i / M and the rows
+    // i % M ..: where those rows of the output are (NULL: nowhere), and the numbers.
+    auto rows_from = [&](const Item &x, int m, uint16_t *(&to)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const int row = mb * M + i % M + c;
-            if (row >= m_all) return;
-            const int r = p.by_group.over(row);
-            to[((int64_t)r * (p.heads - 1) * p.group + row) * D] =
-                (uint16_t)(p.dtype == MOEOP_BF16 ? pair<MOEOP_BF16>(v[c], 0.f)
-                                                 : pair<MOEOP_FP16>(v[c], 0.f));
+            const int row = mb * M + m + c, r = p.by_group.over(row);
+            to[c] = row < m_all ? static_cast<uint16_t *>(p.out) +
+                                      ((((int64_t)x.b * p.rows + r) * p.heads + x.h) * p.group +
+                                       (row - r * p.group)) * D
+                                : nullptr;
+        }
+    };
+    auto store = [&](uint16_t *const (&to)[4], int i, const float (&v)[4]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t w = p.dtype == MOEOP_BF16 ? pair<MOEOP_BF16>(v[c], 0.f)
+                                                     : pair<MOEOP_FP16>(v[c], 0.f);
+            if (to[c]) to[c][i / M] = (uint16_t)w;
         }
     };
     auto finite = [](float v) { return v == -INFINITY ? 0.f : v; };
@@ -887,7 +891,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         }
     }
     __syncthreads();
-    for (uint32_t rest = need; rest; rest &= rest - 1) {
+    // the warps share the items out
+    const int groups = __popc(need), slices = groups > 0 && groups < W ? W / groups : 1;
+#pragma unroll 1
+    for (int k = warp / slices; k < groups; k += W / slices) {
+        uint32_t rest = need;
+        for (int i = 0; i < k; ++i) rest &= rest - 1;
         const int e0 = __ffs(rest) - 1;
         const bool here = __shfl_sync(~0u, inside ? 1 : 0, e0);
         const uint32_t bits = __shfl_sync(~0u, those, e0) << e0;
@@ -895,25 +904,39 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         x.b = __shfl_sync(~0u, mine.b, e0), x.h = __shfl_sync(~0u, mine.h, e0);
         x.start = __shfl_sync(~0u, mine.start, e0);
         float *const out = blocks_out + (x.start >= cs ? S::kPart : 0) + S::kStats;
+        // share by share, four of a lane's places at a time: finding a share takes as
+        // long as adding it
+        const int stride = slices * 128;                  // places keep their row
+        uint16_t *to[4];
+        rows_from(x, lane * 4 % M, to);
 #pragma unroll 1
-        for (int i = threadIdx.x * 4; i < M * D; i += W * 128) {
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t left = bits;
-#pragma unroll 4
-            for (int n = __popc(bits); n; --n) {
-                const int e = __ffs(left) - 1;
-                left &= left - 1;
+        for (int i0 = (warp % slices * 32 + lane) * 4; i0 < M * D; i0 += 4 * stride) {
+            float v[4][4] = {};
+#pragma unroll 1
+            for (uint32_t left = bits; left; left &= left - 1) {
                 // a warp's last item, and behind it the one that another began
-                const float4 u = *reinterpret_cast<const float4 *>(
-                    smem + e / 2 * (kStages * S::kStage) + ((~e & 1) * M * D + i) * 4);
-                const float4 f = *reinterpret_cast<const float4 *>(&worth_of[e][i % M]);
-                v[0] = fmaf(u.x, f.x, v[0]), v[1] = fmaf(u.y, f.y, v[1]);
-                v[2] = fmaf(u.z, f.z, v[2]), v[3] = fmaf(u.w, f.w, v[3]);
+                const int e = __ffs(left) - 1;
+                const float *part = reinterpret_cast<const float *>(
+                                        smem + e / 2 * (kStages * S::kStage)) + (~e & 1) * M * D;
+                const float4 f = *reinterpret_cast<const float4 *>(&worth_of[e][i0 % M]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (i0 + c * stride >= M * D) break;
+                    const float4 u = *reinterpret_cast<const float4 *>(part + i0 + c * stride);
+                    v[c][0] = fmaf(u.x, f.x, v[c][0]), v[c][1] = fmaf(u.y, f.y, v[c][1]);
+                    v[c][2] = fmaf(u.z, f.z, v[c][2]), v[c][3] = fmaf(u.w, f.w, v[c][3]);
+                }
             }
-            if (here)
-                store(x, i, v);
-            else
-                *reinterpret_cast<float4 *>(out + i) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int i = i0 + c * stride;
+                if (i >= M * D) break;
+                if (here)
+                    store(to, i, v[c]);
+                else
+                    *reinterpret_cast<float4 *>(out + i) =
+                        make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+            }
         }
     }
     // -----------------------------------------------------------------------
@@ -993,6 +1016,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                 }
             }
             __syncthreads();
+            uint16_t *to[4];
+            rows_from(x, threadIdx.x * 4 % M, to);
 #pragma unroll 1
             for (int i = threadIdx.x * 4; i < M * D; i += W * 128) {
                 float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1005,7 +1030,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                     v[2] = fmaf(u.z, f.z, v[2]), v[3] = fmaf(u.w, f.w, v[3]);
                 }
                 if (whole)
-                    store(x, i, v);
+                    store(to, i, v);
                 else
                     *reinterpret_cast<float4 *>(part(0) + S::kStats + i) =
                         make_float4(v[0], v[1], v[2], v[3]);

@@ -1,12 +1,15 @@
-"""A routed MoE layer with FP8 weights, for any number of token rows: the
-operators of ops.py as one step of a model, from the previous layer's output
-to this layer's.
+"""A routed MoE layer with FP8 weights, for any number of token rows, and the
+attention before it: the operators of ops.py as one step of a model, from the
+previous layer's output to this layer's.
 
+    norm (+ residual)  ->  queries, keys, values  ->  cache  ->  attention
+                       ->  output product
     norm (+ residual)  ->  router logits  ->  experts of each row
                        ->  shared expert  ->  routed experts, added to it
 
 ``python -m routed_moe_decode_router_gb300.fp8_layer`` runs a layer of the
-decode workload's shape with random weights over one, 64 and 4096 rows.
+decode workload's shape with random weights over one, 64 and 4096 rows, and both
+halves of it over one new token of 1 and 64 sequences and four of 16.
 """
 from __future__ import annotations
 
@@ -98,6 +101,77 @@ class Fp8MoeLayer:
         return out, x if residual is None else n.residual
 
 
+def new_slots(table: torch.Tensor, lengths: torch.Tensor, rows: int, page: int) -> torch.Tensor:
+    """The slots [B, rows] (int32) of the last `rows` tokens of sequences whose
+    pages are table [B, W] and whose lengths, these tokens among them, are lengths
+    [B]; -1 for positions before the first token or behind the table."""
+    pos = lengths[:, None] - rows + torch.arange(rows, device=table.device)
+    at = torch.div(pos, page, rounding_mode="floor")
+    ids = table.gather(1, at.clamp(0, table.shape[1] - 1).long())
+    there = (pos >= 0) & (at < table.shape[1]) & (ids >= 0)
+    return torch.where(there, ids * page + pos % page, -1).to(torch.int32)
+
+
+class Fp8AttentionLayer:
+    """The attention of a layer over a paged cache, and its forward call.
+
+    norm [H] (bf16); qkv: FP8 weights [(heads + 2 kv_heads) dim, H], queries, keys
+    and values in this order; out [H, heads dim] (bf16; its product is PyTorch's).
+    rotate: (q, k, positions) -> (q, k), the position embedding of queries
+    [T, heads, dim] and keys [T, kv_heads, dim], or None.  window and scale as in
+    ops.attend_paged."""
+
+    def __init__(self, norm: torch.Tensor, qkv: Fp8Weights, out: torch.Tensor, heads: int,
+                 kv_heads: int, *, eps: float = 1e-6, rotate=None, window: int = 0,
+                 scale: Optional[float] = None):
+        dim, rest = divmod(qkv.codes.shape[0], heads + 2 * kv_heads)
+        if rest or out.shape[1] != heads * dim:
+            raise ValueError("qkv has %d rows and out %d columns, which are not those of %d and %d "
+                             "heads" % (qkv.codes.shape[0], out.shape[1], heads, kv_heads))
+        self.norm, self.qkv, self.out = norm, qkv, out
+        self.heads, self.kv_heads, self.dim = heads, kv_heads, dim
+        self.eps, self.rotate, self.window, self.scale = eps, rotate, window, scale
+
+    def workspace(self, batch: int, rows: int) -> ops.AttendWorkspace:
+        return ops.AttendWorkspace(batch, rows, self.heads, self.kv_heads, self.dim)
+
+    def forward(self, x: torch.Tensor, cache: ops.KvCache, table: torch.Tensor,
+                lengths: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                ws: Optional[ops.AttendWorkspace] = None):
+        """(out, residual) [B, R, H] bf16 of the last R tokens x of B sequences:
+        their keys and values are written to the cache, and they see what it then
+        holds.  table [B, W] and lengths [B] (the new tokens among them) as in
+        ops.attend_paged."""
+        b, r, h = x.shape
+        flat = None if residual is None else residual.reshape(b * r, h)
+        n = ops.rms_norm(x.reshape(b * r, h), self.norm, eps=self.eps, residual=flat,
+                         quantize=True, keep=False)
+        rows = ops.matmul_fp8(n.q, n.scales, *self.qkv).view(b * r, -1, self.dim)
+        q, k, v = rows.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
+        if self.rotate is not None:
+            pos = lengths[:, None] - r + torch.arange(r, device=x.device)
+            q, k = self.rotate(q, k, pos.clamp(min=0).flatten())
+        slots = new_slots(table, lengths, r, cache.k.shape[2])
+        ops.kv_write(cache, k, v, slots.flatten())
+        a = ops.attend_paged(q.unflatten(0, (b, r)), cache, table, lengths, scale=self.scale,
+                             window=self.window, ws=ws)
+        out = torch.mm(a.view(b * r, -1), self.out.t()).view(b, r, h)
+        return out, x if residual is None else n.residual.view(b, r, h)
+
+
+def random_attention(hidden: int, heads: int, kv_heads: int, dim: int, seed: int = 0,
+                     device="cuda", **kw) -> Fp8AttentionLayer:
+    """An attention layer with weights N(0, 0.02)."""
+    g = torch.Generator(device=device).manual_seed(seed)
+
+    def normal(*shape, std=0.02):
+        return torch.randn(*shape, generator=g, device=device) * std
+
+    return Fp8AttentionLayer((1 + normal(hidden)).to(torch.bfloat16),
+                             quantize_weights(normal((heads + 2 * kv_heads) * dim, hidden)),
+                             normal(hidden, heads * dim).to(torch.bfloat16), heads, kv_heads, **kw)
+
+
 def random_layer(hidden: int, experts: int, inter: int, top_k: int, seed: int = 0,
                  device="cuda", shared_inter: int = 0, shared_gated: bool = True,
                  router_fp8: bool = True, **routing) -> Fp8MoeLayer:
@@ -124,27 +198,50 @@ def random_layer(hidden: int, experts: int, inter: int, top_k: int, seed: int = 
                        router_fp8=router_fp8, bias=bias, **routing)
 
 
+def _timed(run):
+    """(outputs, microseconds) of a call, replayed from a CUDA graph."""
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for _ in range(3):
+        graph.replay()
+    start.record()
+    for _ in range(20):
+        graph.replay()
+    end.record()
+    torch.cuda.synchronize()
+    return out, start.elapsed_time(end) / 20 * 1e3
+
+
 def main():
     layer = random_layer(2048, 128, 768, 8, shared_inter=768)
     for rows in (1, 64, 4096):
         x = torch.randn(rows, 2048, device="cuda").to(torch.bfloat16)
         r = torch.randn(rows, 2048, device="cuda").to(torch.bfloat16)
-        layer.forward(x, r)
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            out, _ = layer.forward(x, r)
-        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-        for _ in range(3):
-            graph.replay()
-        start.record()
-        for _ in range(20):
-            graph.replay()
-        end.record()
-        torch.cuda.synchronize()
+        (out, _), us = _timed(lambda: layer.forward(x, r))
         if ops.device_status() != 0 or not torch.isfinite(out).all():
             raise RuntimeError("the layer of %d rows did not finish" % rows)
-        us = start.elapsed_time(end) / 20 * 1e3
         print("%5d rows: %8.1f us per layer, %10.0f rows/s" % (rows, us, rows / us * 1e6))
+    attention = random_attention(2048, 32, 4, 128)
+    length, page = 4096, 64
+    for batch, rows in ((1, 1), (64, 1), (16, 4)):
+        cache = ops.new_kv_cache(batch * length // page, 4, page, 128)
+        table = torch.randperm(batch * length // page, device="cuda").view(batch, -1).int()
+        lengths = torch.full((batch,), length, dtype=torch.int32, device="cuda")
+        x = torch.randn(batch, rows, 2048, device="cuda").to(torch.bfloat16)
+        r = torch.randn(batch, rows, 2048, device="cuda").to(torch.bfloat16)
+        ws = attention.workspace(batch, rows)
+
+        def step():
+            a, res = attention.forward(x, cache, table, lengths, residual=r, ws=ws)
+            return layer.forward(a.flatten(0, 1), res.flatten(0, 1))
+        (out, _), us = _timed(step)
+        if ops.device_status() != 0 or not torch.isfinite(out).all():
+            raise RuntimeError("the layer of %d sequences did not finish" % batch)
+        print("%5d sequences of %d, %d new tokens each: %8.1f us per layer with its attention"
+              % (batch, length, rows, us))
 
 
 if __name__ == "__main__":
