@@ -174,7 +174,9 @@ MOE_API moe_status moeop_kv_read(const moeop_kv_cache *cache, const int32_t *slo
  * that is one of 16 bits.  Products, softmax statistics and sums are in fp32;
  * probabilities enter the second product as two 16-bit numbers whose sum is
  * within 2^-16 (bf16; 2^-22 fp16, e4m3) of them.  out is rounded once.
- * Scores beyond the range of fp32 give NaN, as they do in a softmax. */
+ * Scores beyond the range of fp32 give NaN, as they do in a softmax; an infinite
+ * value that a row sees gives an infinity or NaN.
+ * The first call on a device looks up what the library keeps per device. */
 typedef struct moeop_attend_config {
     int batch;                   /* 0..2048 */
     int rows;                    /* 1..64 */

@@ -435,7 +435,7 @@ moe_status moeop_attend_paged(const moeop_attend_config *cfg, const moeop_kv_cac
                     c.dtype, cache->type);
     if (c.width < 1 || (int64_t)c.width * cache->page > (1 << 30))
         return fail(MOE_ERR_INVALID_ARG, "width=%d: width * page must be in [1, 2^30]", c.width);
-    if ((int64_t)c.batch * cache->heads * ((int64_t)c.width * cache->page / 16) > INT32_MAX)
+    if ((int64_t)c.batch * cache->heads * ((int64_t)c.width * cache->page / 16 + 2) > INT32_MAX)
         return fail(MOE_ERR_INVALID_ARG, "batch=%d: batch * heads * width * page / 16 must be below "
                     "2^31", c.batch);
     if (c.window < 0)

@@ -215,6 +215,52 @@ def test_attention_long_and_many(held, dtype, dim, heads, group, rows, lengths):
     assert not ws.buf[:1024].any()          # ready for the next call
 
 
+@pytest.mark.parametrize("batch", [32, 33, 1024, 1025, 2048])
+def test_attention_of_many_sequences(batch):
+    lengths = [(37 * i) % 70 for i in range(batch)]
+    lengths[batch // 3] = 3000
+    table, pages = batch_of(lengths, 16)
+    cache = cache_of(pages, 1, 16, 64, F8)
+    q = randn(batch, 1, 3, 64, seed=9).to(BF)
+    check(q, cache, table, lengths)
+
+
+@pytest.mark.parametrize("held,dtype", TYPES)
+@pytest.mark.parametrize("batch,page,window", [(1, 48, 0), (2, 16, 30000), (1, 1024, 0), (20, 64, 0)])
+def test_long_sequences_with_pages_that_are_gone(held, dtype, batch, page, window):
+    """Shares of an item that see nothing, in blocks and in groups of blocks."""
+    lengths = [50000 // (1 + b) + 7 for b in range(batch)]
+    table, pages = batch_of(lengths, page)
+    table[0, 3:table.shape[1] * 2 // 3] = pages + 5
+    table[-1, ::3] = -1
+    cache = cache_of(pages, 2, page, 64, held)
+    q = randn(batch, 3, 4, 64, seed=9).to(dtype)
+    check(q, cache, table, lengths, window=window)
+    table[:] = -1
+    assert not check(q, cache, table, lengths, window=window).any()
+
+
+def test_infinities_and_nan_that_are_seen():
+    """They reach the rows that see them, and those alone.  A weight is two numbers,
+    the second of which may be negative or 0, so an infinity may come out as NaN."""
+    table, pages = batch_of([100, 100], 16)
+    cache = cache_of(pages, 1, 16, 64, BF)
+    q = randn(2, 1, 2, 64, seed=9).to(BF)
+    lengths = torch.tensor([100, 100], dtype=torch.int32, device="cuda")
+    clean = ops.attend_paged(q, cache, table, lengths)
+    cache.v[int(table[0, 1]), 0, 3, 5] = math.inf
+    got = ops.attend_paged(q, cache, table, lengths)
+    assert torch.equal(got[1], clean[1]) and not got[0, 0, :, 5].isfinite().any()
+    assert torch.equal(got[0, 0, :, :5], clean[0, 0, :, :5])
+    assert torch.equal(got[0, 0, :, 6:], clean[0, 0, :, 6:])
+    cache.v[int(table[0, 1]), 0, 3, 5] = 1.0
+    clean = ops.attend_paged(q, cache, table, lengths)
+    bad = q.clone()
+    bad[1, 0, 1, 7] = math.nan
+    got = ops.attend_paged(bad, cache, table, lengths)
+    assert got[1, 0, 1].isnan().all() and torch.equal(got[1, 0, 0], clean[1, 0, 0])
+
+
 @pytest.mark.parametrize("held,dtype", TYPES)
 @pytest.mark.parametrize("window", [0, 20])
 def test_what_a_row_does_not_see_does_not_reach_it(held, dtype, window):
