@@ -164,6 +164,7 @@ struct AttendParams {
     uint32_t *status;
     bool wide;                 // a tile never leaves its page
     bool apart;                // a kernel of its own joins what blocks have of an item
+    int whole;                 // tiles up to which an item is not cut between blocks
 };
 // Query rows (row, head of the group) that a thread block takes together.
 constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 16; }

@@ -71,7 +71,6 @@ struct Shape {
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int smem(int batch) { return 1024 + kRing + (2 * batch + 1) * 4; }
     static constexpr int kSteps = kRow / 32;              // 32 bytes of a row: an MMA's
-    static constexpr int kWhole = 1536 / kTok;
     static_assert(2 * M * D * 4 <= kStages * kStage, "two shares' sums lie in their warp's ring");
     static_assert(kWarps <= 16, "two shares of each warp: a lane for each");
     static_assert(kStage % 1024 == 0 && kSub % 1024 == 0, "the swizzle's period");
@@ -195,7 +194,7 @@ struct Shares {
     }
 };
 // An item of up to `whole` tiles is not cut between blocks: the cut goes to its
-// nearer end.  To join what two blocks have of an item takes some 4 us.
+// nearer end.
 __device__ __forceinline__ int cut(const int *first, int heads, int batch, int tiles, int whole,
                                    int x) {
     if (x <= 0 || x >= tiles) return min(x, tiles);
@@ -279,8 +278,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     else __syncthreads();
     const int tiles = sum * p.heads;
     const Shares shares(tiles, p.by_grid);
-    const int cs = cut(first, p.heads, p.batch, tiles, S::kWhole, shares.begin(blockIdx.x)),
-              ce = cut(first, p.heads, p.batch, tiles, S::kWhole, shares.begin(blockIdx.x + 1));
+    const int cs = cut(first, p.heads, p.batch, tiles, p.whole, shares.begin(blockIdx.x)),
+              ce = cut(first, p.heads, p.batch, tiles, p.whole, shares.begin(blockIdx.x + 1));
     if (cs >= ce) return;
     // equal shares for the block's warps
     const int used = min(W, ce - cs), warp_each = (ce - cs) / W, warp_more = (ce - cs) % W;
@@ -1082,7 +1081,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p) {
     const int start = (__shfl_sync(~0u, run, b) - c) * p.heads + h * c;
     pdl_wait();
     pdl_trigger();
-    if (c <= S::kWhole) return;
+    if (c <= p.whole) return;
     const int c0 = shares.owner(start), parts = shares.owner(start + c - 1) - c0 + 1;
     if (parts == 1) return;
     const int W = S::kWarps, grid = p.by_grid.d;
@@ -1187,9 +1186,14 @@ cudaError_t launch(AttendParams p, cudaStream_t st) {
     const int64_t most = (tiles * p.batch * p.heads + S::kWarps - 1) / S::kWarps;
     const int grid = attend_grid(p.blocks);
     p.by_grid = Divisor((uint32_t)(most < grid ? most : grid));
-    // four blocks or more to an item: the join is a kernel of its own, unless no item
-    // can be that long
-    p.apart = p.batch <= 32 && tiles > S::kWhole && p.batch * p.heads * 4 <= (int)p.by_grid.d;
+    // Where there is a block for every item the blocks share the items out, short ones
+    // too, and a kernel of its own joins them (8 sequences of up to 2000 tokens, 8
+    // heads: 14.5 -> 12.5 us; 32768 tokens of one: 21.3 -> 18.3), unless all sequences
+    // are short (300 tokens of one: 10.0 -> 7.9).  With more items than blocks they
+    // stay whole up to 1536 tokens (33 sequences, window 1024: up to 800 18.2, 1536
+    // 13.5 us).
+    p.apart = p.batch <= 32 && p.batch * p.heads <= grid && tiles > 512 / S::kTok + kEmpty + 1;
+    p.whole = (p.apart ? 256 : 1536) / S::kTok + kEmpty;
     e = launch_early(kernel, dim3(p.by_grid.d, p.blocks), S::kWarps * 32, S::smem(p.batch), 1, st,
                      kmap, vmap, p);
     if (e != cudaSuccess || !p.apart) return e;
