@@ -231,7 +231,7 @@ MOE_API moe_status moeop_verify_draft(const moeop_verify_config *cfg, const int3
 
 /* Synchronise `stream`, read the current device's status word of these
  * operators into *code (MOE_DEV_*) and clear it.  MOE_DEV_WAIT_TIMEOUT: an
- * on-chip wait exceeded its bound and a product is incomplete.  Returns
+ * on-chip wait exceeded its bound and a product or attention is incomplete.  Returns
  * MOE_ERR_DEVICE_STATUS when the code is non-zero. */
 MOE_API moe_status moeop_read_device_status(int *code, void *stream);
 

@@ -8,7 +8,12 @@
 // elements of each half of a head's row, of the key and of the value: four
 // loads under way, none of which waits for the slot, and accesses of 8, 16 or 32
 // bytes beside those of the next lane.  A row's amax is a few shuffles among its
-// dim / 16 lanes.
+// dim / 16 lanes.  Quotients are computed two at a time (packed fp32: 13.3 -> 11.8
+// million instructions for 16383 tokens, 21 -> 18 us).
+//
+// One GB300: 16383 tokens, 8 heads of 128, bf16 to e4m3 18 us in a stream of calls
+// (5.6 TB/s), 15.7 with the inputs in L2; 65536 read back 61 us (6.6 TB/s); 61 tokens
+// 1.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

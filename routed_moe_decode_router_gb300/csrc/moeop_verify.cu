@@ -18,6 +18,10 @@
 // exact in any order.  64-bit floating point would do too, but an SM adds two a
 // cycle; whole numbers come out of fp32 additions of a constant whose last bit
 // is the step wanted (its sum's lower bits are the number), two at a time.
+//
+// One GB300: 1 sequence, 3 drafts, 32768 ids 5.3 us (launch, draft, its probability,
+// the row, the clusters' meeting, the id); 64 sequences, 131072 ids 21 us (3.2 TB/s),
+// 16.5 with the rows in L2; with a 64-bit sum per id 31.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
