@@ -165,15 +165,19 @@ struct AttendParams {
     bool wide;                 // a tile never leaves its page
     bool apart;                // a kernel of its own joins what blocks have of an item
     int whole;                 // tiles up to which an item is not cut between blocks
+    // it joins what warps have of an item: warps take shares of the whole work, in turn
+    // from block to block, and blocks join nothing
+    bool flat;
+    Divisor by_warps;          // warps of the grid
 };
 // Query rows (row, head of the group) that a thread block takes together.
 constexpr int attend_block(int dim, int m) { return dim == 256 || m <= 8 ? 8 : 16; }
 // Thread blocks for each block of query rows: together one for every SM.
 constexpr int kAttendSms = 152, kAttendCounters = 3 * 256, kAttendMaxBatch = 2048;
 constexpr int attend_grid(int blocks) { return blocks < kAttendSms ? kAttendSms / blocks : 1; }
-// Workspace of moeop_attend_paged: the counters, in every shape the same, then a
-// partial sum for each warp (up to 8 in a thread block) and two for each thread
-// block: three numbers for a row, and the row.
+// Workspace of moeop_attend_paged: the counters, in every shape the same, then two
+// partial sums for each warp (up to 8 in a thread block), or one for each warp and
+// two for each thread block: three numbers for a row, and the row.
 struct AttendWs {
     size_t parts, total;
     static AttendWs make(int m, int dim) {
@@ -181,7 +185,7 @@ struct AttendWs {
         const size_t part = (size_t)block * (3 + dim) * 4;
         AttendWs w{};
         w.parts = kAttendCounters * 4;
-        w.total = w.parts + part * blocks * attend_grid(blocks) * (8 + 2);
+        w.total = w.parts + part * blocks * attend_grid(blocks) * (2 * 8);
         return w;
     }
 };

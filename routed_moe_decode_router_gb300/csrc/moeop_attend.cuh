@@ -39,7 +39,7 @@
 // One GB300, calls in a stream: 96 sequences of up to 16384 tokens, 64/8 heads of 128,
 // e4m3 256 us (6.6 TB/s); one of 131071, 16/2 of 256, fp16 54 us (5.0 TB/s); 9 of up to
 // 6007, 4 rows, 64/8 of 128, bf16 37 us (two passes of 16 query rows); one of 901, e4m3
-// 10 us, 8000 cycles of which are waits for lengths, table, tiles, one after the other.
+// 8.5 us, 6000 cycles of which are waits for lengths, table, tiles, one after the other.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -284,14 +284,21 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     if (few) __syncwarp();
     else __syncthreads();
     const int tiles = sum * p.heads;
-    const Shares shares(tiles, p.by_grid);
-    const int cs = cut(first, p.heads, p.batch, tiles, p.whole, shares.begin(blockIdx.x)),
-              ce = cut(first, p.heads, p.batch, tiles, p.whole, shares.begin(blockIdx.x + 1));
-    if (cs >= ce) return;
-    // equal shares for the block's warps
-    const int used = min(W, ce - cs), warp_each = (ce - cs) / W, warp_more = (ce - cs) % W;
-    auto warp_begin = [&](int w) { return cs + w * warp_each + min(w, warp_more); };
-    const int begin = warp_begin(warp), end = warp_begin(warp + 1);
+    const Shares shares(tiles, p.flat ? p.by_warps : p.by_grid);
+    const int worker = warp * gridDim.x + blockIdx.x;          // of a flat grid
+    int begin, end, cs = 0, ce = 0;
+    if (p.flat) {
+        begin = shares.begin(worker), end = shares.begin(worker + 1);
+    } else {
+        cs = cut(first, p.heads, p.batch, tiles, p.whole, shares.begin(blockIdx.x));
+        ce = cut(first, p.heads, p.batch, tiles, p.whole, shares.begin(blockIdx.x + 1));
+        if (cs >= ce) return;
+        // equal shares for the block's warps
+        const int each = (ce - cs) / W, more = (ce - cs) % W;
+        begin = cs + warp * each + min(warp, more);
+        end = begin + each + (warp < more ? 1 : 0);
+    }
+    const int used = min(W, ce - cs);
 
     char *const ring = smem + warp * (kStages * S::kStage);
     const uint32_t ring_addr = smem_u32(ring);
@@ -794,9 +801,14 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             } else {
                 // the last item's sums go to the ring, which is empty then
                 const bool last = was.start + s1 == end;
-                const int share = 2 * warp + (last ? 1 : 0);
+                float *of_rows = &stats[2 * warp + (last ? 1 : 0)][0][0];
                 float *part = last ? reinterpret_cast<float *>(ring)
                                    : heads_at + (int64_t)warp * S::kPart;
+                if (p.flat) {
+                    of_rows = p.parts + (((int64_t)mb * gridDim.x * W + worker) * 2 + (last ? 1 : 0)) *
+                                            S::kPart;
+                    part = of_rows + S::kStats;
+                }
                 has |= last ? 2 : 1;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
@@ -804,9 +816,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const int m = j * 8 + 2 * t + c;
-                            stats[share][0][m] = top[j][c];
-                            stats[share][1][m] = sums[j][c];
-                            stats[share][2][m] = F8 ? otop[j][c] : top[j][c];
+                            of_rows[m] = top[j][c];
+                            of_rows[M + m] = sums[j][c];
+                            of_rows[2 * M + m] = F8 ? otop[j][c] : top[j][c];
                         }
                     }
 #pragma unroll
@@ -822,7 +834,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         }
         if (lane == 0) lasts[warp] = it;
         // what the warp has of the item it did not begin follows into the ring
-        if (has & 1) {
+        if ((has & 1) && !p.flat) {
             const float *from = heads_at + (int64_t)warp * S::kPart;
             __syncwarp();
 #pragma unroll 1
@@ -831,6 +843,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             copies_wait();
         }
     }
+    if (p.flat) return;
     if (lane == 0) shares_of[warp] = has;
     // The next kernel may come (calls in a row, 9 x 6007: 44 us, so 41); the one that
     // joins reads the lengths before it waits, and would only take room (32768 tokens
@@ -1083,7 +1096,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p) {
         const int left = __shfl_up_sync(~0u, run, o);
         if (lane >= o) run += left;
     }
-    const Shares shares(__shfl_sync(~0u, run, 31) * p.heads, p.by_grid);
+    const Shares shares(__shfl_sync(~0u, run, 31) * p.heads, p.flat ? p.by_warps : p.by_grid);
     c = __shfl_sync(~0u, c, b);
     const int start = (__shfl_sync(~0u, run, b) - c) * p.heads + h * c;
     pdl_wait();
@@ -1092,10 +1105,16 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p) {
     const int c0 = shares.owner(start), parts = shares.owner(start + c - 1) - c0 + 1;
     if (parts == 1) return;
     const int W = S::kWarps, grid = p.by_grid.d;
-    const float *const blocks_at = p.parts + ((int64_t)mb * grid * (W + 2) + (int64_t)grid * W) * S::kPart;
+    const bool goes_on = shares.begin(c0 + parts) > start + c;     // its last owner does
+    const float *const parts_at =
+        p.parts + (p.flat ? (int64_t)mb * grid * W * 2
+                          : (int64_t)mb * grid * (W + 2) + (int64_t)grid * W) * S::kPart;
+    // a warp's second sum is that of its last item, a block's of one that begins in it
     auto part = [&](int i) {
-        return blocks_at + (2 * (c0 + i) + (i == 0 ? 1 : 0)) * (int64_t)S::kPart;
+        const bool second = p.flat ? i < parts - 1 || !goes_on : i == 0;
+        return parts_at + (2 * (c0 + i) + (second ? 1 : 0)) * (int64_t)S::kPart;
     };
+    static_assert(140 <= kAttendSms, "an item's warps, and its blocks, fit");
     const int mine = threadIdx.x % kEach * 4, group = threadIdx.x / kEach;
     const int at = blockIdx.z * 32 * M + mine;          // number of a partial sum
     float4 u[8];
@@ -1190,17 +1209,22 @@ cudaError_t launch(AttendParams p, cudaStream_t st) {
     if (p.window && (p.window + p.rows) / S::kTok + 2 < tiles)
         tiles = (p.window + p.rows) / S::kTok + 2;
     tiles += kEmpty;
-    const int64_t most = (tiles * p.batch * p.heads + S::kWarps - 1) / S::kWarps;
     const int grid = attend_grid(p.blocks);
-    p.by_grid = Divisor((uint32_t)(most < grid ? most : grid));
-    // Where there is a block for every item the blocks share the items out, short ones
+    // Where there is a block for every item, the blocks share the items out, short ones
     // too, and a kernel of its own joins them (8 sequences of up to 2000 tokens, 8
-    // heads: 14.5 -> 12.5 us; 32768 tokens of one: 21.3 -> 18.3), unless all sequences
-    // are short (300 tokens of one: 10.0 -> 7.9).  With more items than blocks they
-    // stay whole up to 1536 tokens (33 sequences, window 1024: up to 800 18.2, 1536
-    // 13.5 us).
+    // heads: 14.5 -> 12.5 us; 32768 tokens of one: 21.3 -> 18.4); where all sequences are
+    // of up to 140 tiles (what that kernel can hold of an item) it joins the warps' sums,
+    // and warps may be spread over all SMs (901 tokens of one: 10.2 -> 8.5; 4 of up to
+    // 901: 10.2 -> 9.0); up to 512 tokens one block takes an item (300 tokens: 7.9, with
+    // the kernel that joins 7.8).  With more items than blocks they stay whole up to 1536
+    // tokens (33 sequences, window 1024: up to 800 18.2, 1536 13.5 us).
     p.apart = p.batch <= 32 && p.batch * p.heads <= grid && tiles > 512 / S::kTok + kEmpty + 1;
-    p.whole = (p.apart ? 256 : 1536) / S::kTok + kEmpty;
+    p.flat = p.apart && tiles <= 140;
+    p.whole = p.flat ? 0 : (p.apart ? 256 : 1536) / S::kTok + kEmpty;
+    const int64_t all = tiles * p.batch * p.heads;
+    const int64_t most = p.flat ? all : (all + S::kWarps - 1) / S::kWarps;
+    p.by_grid = Divisor((uint32_t)(most < grid ? most : grid));
+    p.by_warps = Divisor(p.by_grid.d * S::kWarps);
     e = launch_early(kernel, dim3(p.by_grid.d, p.blocks), S::kWarps * 32, S::smem(p.batch), 1, st,
                      kmap, vmap, p);
     if (e != cudaSuccess || !p.apart) return e;
