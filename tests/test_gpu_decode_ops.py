@@ -240,6 +240,30 @@ def test_long_sequences_with_pages_that_are_gone(held, dtype, batch, page, windo
     assert not check(q, cache, table, lengths, window=window).any()
 
 
+@pytest.mark.parametrize("held,dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lengths,heads,group,rows,window", [
+    ([1983], 1, 1, 1, 0), ([1100, 30, 0, 2000], 4, 3, 2, 0), ([600] * 3, 8, 4, 1, 0),
+    ([4000, 513], 2, 2, 5, 700), ([2100, 2, 1], 1, 16, 2, 0)])
+def test_attention_of_few_sequences_spread_over_all_blocks(held, dtype, dim, lengths, heads, group,
+                                                           rows, window):
+    table, pages = batch_of(lengths, 32)
+    cache = cache_of(pages, heads, 32, dim, held)
+    q = randn(len(lengths), rows, group * heads, dim, seed=9).to(dtype)
+    ws = ops.AttendWorkspace(len(lengths), rows, group * heads, heads, dim)
+    got = check(q, cache, table, lengths, ws=ws, window=window)
+    table[0, 5:9] = -1
+    check(q, cache, table, lengths, ws=ws, window=window)
+    lengths = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ops.attend_paged(q, cache, table, lengths, ws=ws, window=window)
+    lengths.sub_(1).clamp_(min=0)
+    graph.replay()
+    want, bound = D.attend(q, cache, table, lengths, window=window)
+    assert ((out.double() - want).abs() <= bound).all() and out.shape == got.shape
+
+
 def test_infinities_and_nan_that_are_seen():
     """They reach the rows that see them, and those alone.  A weight is two numbers,
     the second of which may be negative or 0, so an infinity may come out as NaN."""
