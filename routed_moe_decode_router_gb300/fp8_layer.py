@@ -104,12 +104,14 @@ class Fp8MoeLayer:
 def new_slots(table: torch.Tensor, lengths: torch.Tensor, rows: int, page: int) -> torch.Tensor:
     """The slots [B, rows] (int32) of the last `rows` tokens of sequences whose
     pages are table [B, W] and whose lengths, these tokens among them, are lengths
-    [B]; -1 for positions before the first token or behind the table."""
+    [B]; -1 for positions before the first token or behind the table, and for page
+    numbers that no cache has."""
     pos = lengths[:, None] - rows + torch.arange(rows, device=table.device)
     at = torch.div(pos, page, rounding_mode="floor")
-    ids = table.gather(1, at.clamp(0, table.shape[1] - 1).long())
-    there = (pos >= 0) & (at < table.shape[1]) & (ids >= 0)
-    return torch.where(there, ids * page + pos % page, -1).to(torch.int32)
+    ids = table.gather(1, at.clamp(0, table.shape[1] - 1).long()).long()
+    slots = ids * page + pos % page
+    there = (pos >= 0) & (at < table.shape[1]) & (ids >= 0) & (slots < 1 << 31)
+    return torch.where(there, slots, -1).to(torch.int32)
 
 
 class Fp8AttentionLayer:

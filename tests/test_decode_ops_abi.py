@@ -10,7 +10,7 @@ import torch
 
 from routed_moe_decode_router_gb300 import build as B
 from routed_moe_decode_router_gb300 import native as N
-from routed_moe_decode_router_gb300 import ops
+from routed_moe_decode_router_gb300 import fp8_layer, ops
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 28      # a well-aligned address that no refused call may touch
@@ -216,3 +216,13 @@ def test_python_refuses_host_tensors_before_the_library():
         ops.kv_read(ops.KvCache(k, k), i)
     with pytest.raises(ValueError, match="dtype"):
         ops.kv_read(host, i, dtype=torch.int8)
+
+
+def test_slots_of_page_numbers_that_no_cache_has():
+    # 2^28 * 16 is 0 in 32 bits: a token of no page must not land in page 0
+    big = 1 << 28
+    table = torch.tensor([[big], [(1 << 31) - 1], [-1], [(1 << 27) - 1]], dtype=torch.int32)
+    lengths = torch.full((4,), 3, dtype=torch.int32)
+    got = fp8_layer.new_slots(table, lengths, 2, 16)
+    assert got.dtype == torch.int32
+    assert got.tolist() == [[-1, -1]] * 3 + [[(1 << 31) - 15, (1 << 31) - 14]]
