@@ -183,7 +183,7 @@ typedef struct moeop_attend_config {
     int q_heads;                 /* a multiple of the cache's heads; rows * group <= 256 */
     int width;                   /* pages in a row of the table, >= 1 */
     int window;                  /* 0 = none */
-    float scale;                 /* finite */
+    float scale;                 /* below 2^127 in magnitude */
     int dtype;                   /* of q and out */
 } moeop_attend_config;
 

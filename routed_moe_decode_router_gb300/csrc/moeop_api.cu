@@ -440,7 +440,8 @@ moe_status moeop_attend_paged(const moeop_attend_config *cfg, const moeop_kv_cac
                     "2^31", c.batch);
     if (c.window < 0)
         return fail(MOE_ERR_INVALID_ARG, "window=%d: must not be negative", c.window);
-    if (!std::isfinite(c.scale)) return fail(MOE_ERR_INVALID_ARG, "scale is not finite");
+    if (!(std::fabs(c.scale) < 0x1p127f))   // times log2(e) it is a finite number
+        return fail(MOE_ERR_INVALID_ARG, "scale is not finite, or 2^127 or more");
     if (c.batch == 0) return ok();
     const int64_t row = (int64_t)c.q_heads * cache->dim;
     if (bad(q, 16) || bad(out, 16))

@@ -226,3 +226,8 @@ def test_slots_of_page_numbers_that_no_cache_has():
     got = fp8_layer.new_slots(table, lengths, 2, 16)
     assert got.dtype == torch.int32
     assert got.tolist() == [[-1, -1]] * 3 + [[(1 << 31) - 15, (1 << 31) - 14]]
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, -3e38])
+def test_scales_that_no_product_with_them_is_finite(scale):
+    refused(N.moeop_attend_paged, config(scale=scale), cache(), *attend_args(), text="scale")
