@@ -381,14 +381,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                 row[u] = li.h * p.page + lplace + 16 * u - (next ? p.page : 0);
                 if (!live || (unsigned)id[u] >= (unsigned)p.pages) id[u] = -1;
                 else in |= 1u << u;
-                if (lane == u) places[warp][stage_in][u] = make_int2(id[u], row[u]);
+                if (F8 && lane == u) places[warp][stage_in][u] = make_int2(id[u], row[u]);
             }
             valid = valid << kSubs | in;
             if (in) {
-                const uint32_t dst = uniform(ring_addr + stage_in * S::kStage);
+                const uint32_t dst = ring_addr + stage_in * S::kStage;
                 uint64_t *bar = &bars[warp][stage_in];
-#pragma unroll
-                for (int u = 0; u < kSubs; ++u) id[u] = uniform(id[u]), row[u] = uniform(row[u]);
                 if (elect_one()) {
                     mbar_arrive_expect_tx(bar, __popc(in) * 2 * S::kSub);
                     if (p.wide) {
