@@ -20,7 +20,7 @@
 // is the step wanted (its sum's lower bits are the number), two at a time.
 //
 // One GB300: 1 sequence, 3 drafts, 32768 ids 5.3 us (launch, draft, its probability,
-// the row, the clusters' meeting, the id); 64 sequences, 131072 ids 21 us (3.2 TB/s),
+// the row, the clusters' meeting, the id); 64 sequences, 131072 ids 20.4 us (3.3 TB/s),
 // 15.5 with the rows in L2; with a 64-bit sum per id 31.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -55,8 +55,8 @@ __device__ __forceinline__ uint64_t both(float a, float b) {
 __device__ __forceinline__ int low(uint64_t v) { return (int)(uint32_t)v; }
 __device__ __forceinline__ int high(uint64_t v) { return (int)(v >> 32); }
 
-// What weights count so far: hi 2^-22 + lo 2^-44.  A lane's share is at most 128 of
-// them (2^19 ids, 8 blocks of 512 lanes), and both stay below 2^30.
+// What weights count so far: hi 2^-22 + lo 2^-44.  A lane's share is at most 260 of
+// them (2^19 ids, 8 blocks of 256 lanes, whole fours), and both stay below 2^31.
 struct Count {
     int hi = 0, lo = 0;
     // The weight of an id: p, or what p has more than q.  A number w in [0, 1] is

@@ -649,3 +649,69 @@ def test_cache_refusals():
         ops.kv_read(ops.new_kv_cache(3, 2, 16, 96), slots)
     with pytest.raises(ValueError, match="dtype"):
         ops.kv_read(cache, slots, dtype=torch.float64)
+
+
+# ---------------------------------------------------------------------------
+# The ends of what calls may ask for
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("held,dtype", [(F8, BF), (HF, HF)])
+@pytest.mark.parametrize("heads,group,rows,dim,lengths", [
+    (1024, 1, 1, 64, [300, 33]), (1, 256, 1, 64, [1000]), (1, 256, 1, 128, [40, 900]),
+    (1, 256, 1, 256, [700, 0, 20]), (3, 4, 64, 128, [63, 600])])
+def test_attention_of_most_heads_and_rows(held, dtype, heads, group, rows, dim, lengths):
+    table, pages = batch_of(lengths, 16)
+    cache = cache_of(pages, heads, 16, dim, held)
+    q = randn(len(lengths), rows, group * heads, dim, seed=9).to(dtype)
+    check(q, cache, table, lengths)
+    check(q, cache, table, lengths, window=50)
+
+
+def test_two_graphs_share_a_workspace():
+    cache = cache_of(300, 2, 16, 128, F8)
+    ws = ops.AttendWorkspace(8, 4, 16, 2, 128)
+    calls = []
+    for rows, lengths in ((1, [2500]), (4, [900, 3, 0, 40, 1000, 7, 64, 65])):
+        table, _ = batch_of(lengths, 16, seed=rows)
+        q = randn(len(lengths), rows, 16, 128, seed=rows).to(BF)
+        n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        want = check(q, cache, table, lengths)
+        ops.attend_paged(q, cache, table, n, ws=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = ops.attend_paged(q, cache, table, n, ws=ws)
+        calls.append((graph, out, want, q, table, n))      # a graph reads where they lie
+    for _ in range(3):
+        for graph, out, want, *_ in calls:
+            out.fill_(7)
+            graph.replay()
+            assert torch.equal(out, want)
+
+
+def test_verify_counts_the_largest_sums():
+    """2^19 weights of 1, by clusters of 256 threads as well as of 512."""
+    vocab = 1 << 19
+    for batch in (38, 39):
+        target = torch.ones(batch, 1, vocab, device="cuda")
+        u = torch.rand(batch, generator=gen(3), device="cuda")
+        u[0], u[1] = 0.0, 1 - 2.0 ** -24
+        none = torch.empty(batch, 0, device="cuda")
+        r = ops.verify_draft(none.int(), target, none, u)
+        assert torch.equal(r.tokens[:, 0].double(), torch.floor(u.double() * vocab))
+        target[:, :, 7::8] = 0         # rows of another sum, and places that none falls to
+        r = ops.verify_draft(none.int(), target, none, u)
+        at = torch.floor(u.double() * (vocab // 8 * 7))
+        assert torch.equal(r.tokens[:, 0].double(), torch.floor(at / 7) + at)
+
+
+def test_verify_of_the_largest_batch():
+    batch, vocab = 65535, 5
+    want = torch.randint(0, vocab, (batch, 2), generator=gen(1), device="cuda")
+    target = torch.nn.functional.one_hot(want, vocab).float()
+    draft = torch.randint(0, vocab, (batch, 1), generator=gen(2), device="cuda").int()
+    u = torch.rand(batch, 1, generator=gen(3), device="cuda")
+    r = ops.verify_draft(draft, target, u, u[:, 0].contiguous())
+    good = draft[:, 0] == want[:, 0]
+    assert torch.equal(r.accepted, good.int())
+    assert torch.equal(r.tokens[:, 0], want[:, 0].int())
+    assert torch.equal(r.tokens[:, 1], torch.where(good, want[:, 1], -1).int())
