@@ -776,8 +776,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                     for (int c = 0; c < 2; ++c) {
                         const int m = mb * M + j * 8 + 2 * t + c;
                         if (m >= m_all) continue;
-                        const float l = sums[j][c];
-                        const float f = l == 0.f ? 0.f : inverse(F8 ? l * lift[j][c] : l);
+                        // (not 1 / (l lift): that ends where values are below 2^-100)
+                        const float f = worth<F8>(sums[j][c], top[j][c], otop[j][c]);
                         const int r = p.by_group.over(m);
                         uint16_t *row = static_cast<uint16_t *>(p.out) +
                                         (((int64_t)was.b * p.rows + r) * p.heads + was.h) *
