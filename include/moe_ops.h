@@ -173,7 +173,9 @@ MOE_API moe_status moeop_kv_read(const moeop_kv_cache *cache, const int32_t *slo
  * same, contiguous, both of type dtype: bf16 or fp16, the cache's own type where
  * that is one of 16 bits.  Products, softmax statistics and sums are in fp32;
  * probabilities enter the second product as two 16-bit numbers whose sum is
- * within 2^-16 (bf16; 2^-22 fp16, e4m3) of them.  out is rounded once.
+ * within 2^-16 of them (bf16), or within 2^-22 of them or 2^-44 of the row's
+ * largest (fp16; e4m3: of the probability times the value's scale).  out is
+ * rounded once.
  * Scores beyond the range of fp32 give NaN, as they do in a softmax; an infinite
  * value that a row sees gives an infinity or NaN.
  * The first call on a device looks up what the library keeps per device. */

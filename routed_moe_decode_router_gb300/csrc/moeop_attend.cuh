@@ -28,7 +28,10 @@
 //   of their own, of s_j + log vs_j, and keep the range of f16 whatever the scales.
 //   (mma.sync on e4m3 itself, Q in two e4m3 numbers, takes 80 instructions a tile more.)
 // - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo (one f16
-//   number for e4m3 would be 2^-11 off, and saves no time).
+//   number for e4m3 would be 2^-11 off, and saves no time).  f16 ends at 2^-24, and a
+//   long row's weights may all be below that beside its largest, so there they count
+//   from 2^15 down, and lo is 2^12 times what hi left, summed apart and added at 2^-12:
+//   hi + lo is within 2^-22 of the weight, or 2^-44 of the row's largest.
 // - Maxima are raised only where a score exceeds them by 2^8, so that most tiles
 //   need one vote and no reduction.
 // - Join.  A warp's share of an item goes to shared memory (its last item) or to
@@ -57,6 +60,8 @@ namespace op {
 namespace attend {
 
 constexpr float kSlack = 8.f;    // what a score may exceed the running maximum by (log2)
+// f16 weights: at most 2^(kSlack + kRoom), hi off by 2^3 there, and 2^3 kLow = 2^15
+constexpr float kRoom = 7.f, kLow = 4096.f;
 
 // TYPE of the cache, D: dim, NT: groups of 8 query rows.
 // A tile is kTok tokens, 8 KB of keys and values where it can be; warps x stages of
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     attend_kernel(const __grid_constant__ TensorMap kmap, const __grid_constant__ TensorMap vmap,
                   const AttendParams p) {
     using S = Shape<TYPE, D, NT>;
-    constexpr bool F8 = S::F8;
+    constexpr bool F8 = S::F8, kHalf = TYPE != MOEOP_BF16;    // weights in f16
     constexpr int W = S::kWarps, M = S::M, kStages = S::kStages, kSteps = S::kSteps;
     constexpr int kTok = S::kTok, kSubs = S::kSubs;
     extern __shared__ char raw[];
@@ -634,7 +639,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                         float w[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const float from = top[j][c % 2] == -INFINITY ? 0.f : top[j][c % 2];
+                            const float from = top[j][c % 2] == -INFINITY ? 0.f
+                                               : kHalf ? top[j][c % 2] - kRoom : top[j][c % 2];
                             w[c] = ex2(x2[u][j][c] - from);
                             sums[j][c % 2] += w[c];
                             // a token that is not seen weighs 0 whatever its scale holds
@@ -648,43 +654,60 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                             const uint32_t hi = pair<TYPE>(w[2 * r], w[2 * r + 1]);
                             ph[u][j][r] = transposed(hi);
                             const float2 h = unpair<TYPE>(hi);
-                            pl[u][j][r] =
-                                transposed(pair<TYPE>(w[2 * r] - h.x, w[2 * r + 1] - h.y));
+                            float l0 = w[2 * r] - h.x, l1 = w[2 * r + 1] - h.y;
+                            if (kHalf) l0 *= kLow, l1 *= kLow;
+                            pl[u][j][r] = transposed(pair<TYPE>(l0, l1));
                         }
                     }
 
                 // sums of the values: use(i, fragment of 16 d's and the 16 tokens)
+                auto values_at = [&](int u, int k, auto use) {
+                    uint32_t v[4];
+                    load_matrices<true>(v, (at + off_v + u * S::kSub + k / 4 * 2048) ^
+                                               (k % 4 * 32));
+                    if constexpr (F8) {
+                        // pairs of d's of two tokens -> pairs of tokens of two d's
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a = __byte_perm(v[2 * h], 0, 0x3120);
+                            const uint32_t b = __byte_perm(v[2 * h + 1], 0, 0x3120);
+                            const uint32_t f[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16),
+                                                   e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16)};
+                            use(2 * k + h, f);
+                        }
+                    } else {
+                        use(k, v);
+                    }
+                };
                 auto values = [&](int u, auto use) {
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        uint32_t v[4];
-                        load_matrices<true>(v, (at + off_v + u * S::kSub + k / 4 * 2048) ^
-                                                   (k % 4 * 32));
-                        if constexpr (F8) {
-                            // pairs of d's of two tokens -> pairs of tokens of two d's
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t a = __byte_perm(v[2 * h], 0, 0x3120);
-                                const uint32_t b = __byte_perm(v[2 * h + 1], 0, 0x3120);
-                                const uint32_t f[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16),
-                                                       e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16)};
-                                use(2 * k + h, f);
-                            }
-                        } else {
-                            use(k, v);
-                        }
-                    }
+                    for (int k = 0; k < kSteps; ++k) values_at(u, k, use);
                 };
                 if (!partly) {
 #pragma unroll
-                    for (int u = 0; u < kSubs; ++u)
-                        values(u, [&](int i, const uint32_t (&f)[4]) {
+                    for (int k = 0; k < kSteps; ++k) {
+                        constexpr int kEach = D / 16 / kSteps;      // d fragments of a step
+                        float low[kEach][NT][4] = {};
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                mma<TYPE>(o[i][j], f, ph[u][j][0], ph[u][j][1]);
-                                mma<TYPE>(o[i][j], f, pl[u][j][0], pl[u][j][1]);
-                            }
-                        });
+                        for (int u = 0; u < kSubs; ++u)
+                            values_at(u, k, [&](int i, const uint32_t (&f)[4]) {
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) {
+                                    mma<TYPE>(o[i][j], f, ph[u][j][0], ph[u][j][1]);
+                                    mma<TYPE>(kHalf ? low[i % kEach][j] : o[i][j], f, pl[u][j][0],
+                                              pl[u][j][1]);
+                                }
+                            });
+                        if (!kHalf) continue;
+#pragma unroll
+                        for (int h = 0; h < kEach; ++h)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    o[k * kEach + h][j][c] =
+                                        fmaf(low[h][j][c], 1.f / kLow, o[k * kEach + h][j][c]);
+                    }
                 } else {
                     // Values that no row sees are taken out: 0 times what lies there
                     // may be NaN.  Where a value that some rows see and others do not
@@ -738,12 +761,14 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                                                        f[2] & keep[1], f[3] & keep[1]};
 #pragma unroll
                                 for (int j = 0; j < NT; ++j) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                    float d[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
                                     mma<TYPE>(d, a, p0[j][0], p0[j][1]);
-                                    mma<TYPE>(d, a, p1[j][0], p1[j][1]);
+                                    mma<TYPE>(kHalf ? low : d, a, p1[j][0], p1[j][1]);
 #pragma unroll
-                                    for (int c = 0; c < 4; ++c)
+                                    for (int c = 0; c < 4; ++c) {
+                                        if (kHalf) d[c] = fmaf(low[c], 1.f / kLow, d[c]);
                                         if (!each || pos[j][c % 2] == last) o[i][j][c] += d[c];
+                                    }
                                 }
                             });
                         }
