@@ -25,7 +25,7 @@
 //   is.)  Fragments come by ldmatrix from the swizzled tiles, V transposed on the way.
 // - e4m3 is widened to f16, exactly.  A key's scale multiplies its score, a value's
 //   its weight: weights are exp(s_j - m) vs_j, so the sums O have a running maximum
-//   of their own, of s_j + log vs_j, and keep the range of f16 whatever the scales.
+//   of their own, of s_j + log |vs_j|, and keep the range of f16 whatever the scales.
 //   (mma.sync on e4m3 itself, Q in two e4m3 numbers, takes 80 instructions a tile more.)
 // - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo (one f16
 //   number for e4m3 would be 2^-11 off, and saves no time).  f16 ends at 2^-24, and a
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                         if (F8) {
                             ks = __shfl_sync(~0u, ks_now, 16 * u + 8 * r + g);
                             vs[u][r] = __shfl_sync(~0u, vs_now, 16 * u + 8 * r + g);
-                            lv[u][r] = fmaxf(lg2(vs[u][r]), -120.f);
+                            lv[u][r] = fmaxf(lg2(fabsf(vs[u][r])), -120.f);
                         }
 #pragma unroll
                         for (int j = 0; j < NT; ++j)

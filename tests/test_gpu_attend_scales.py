@@ -51,3 +51,19 @@ def test_values_near_the_least_numbers(lengths, dim, size):
     want, bound = D.attend(q, cache, table, n)
     got = ops.attend_paged(q, cache, table, n).double()
     assert want.abs().mean() > 2.0 ** -120 and ((got - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("lengths", LENGTHS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_scales_of_either_sign(lengths, dim, dtype):
+    """A value is code * scale, whatever the scale's sign."""
+    cache, table, n, g = made(lengths, 2, dim, seed=1)
+    q = torch.randn(len(lengths), 1, 8, dim, generator=g, device="cuda").to(dtype)
+    for s in (cache.k_scales, cache.v_scales):
+        s.mul_(torch.where(torch.rand(s.shape, generator=g, device="cuda") < 0.4, -1.0, 1.0))
+    want, _ = D.attend(q, cache, table, n)
+    # the bound counts magnitudes, and half a step of its own output
+    _, bound = D.attend(q, cache._replace(v_scales=cache.v_scales.abs()), table, n)
+    got = ops.attend_paged(q, cache, table, n).double()
+    assert ((got - want).abs() <= bound + want.abs() * half_step(dtype) * 1.01).all()
