@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) verify_kernel(const VerifyP
             const float q = p.draft_probs
                                 ? __ldg(p.draft_probs + ((size_t)b * n + lane) * p.c.draft_stride + x)
                                 : 1.f;
-            good = (double)u * (double)q < (double)t;
+            // from 0 to 1, NaN 0, as in the draw
+            good = (double)u * (double)__saturatef(q) < (double)__saturatef(t);
         }
     }
     const int accepted = __ffs(__ballot_sync(~0u, !good)) - 1;  // lane 31 has no draft
