@@ -77,6 +77,18 @@ struct Count {
     }
 };
 
+// u * total of a u in [0, 1), rounded down, exactly: a whole sum exceeds u * total
+// where it exceeds this.  (In 64-bit floating point the product of 24 and 44 bits or
+// more may be rounded up to a whole number, and the next id would be drawn.)
+__device__ __forceinline__ uint64_t share_of(float u, uint64_t total) {
+    const uint32_t bits = __float_as_uint(fabsf(u)), e = bits >> 23;   // (-0: 0)
+    const uint64_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);     // u = m 2^-shift
+    const uint32_t shift = 150 - (e ? e : 1);                         // 24 .. 149
+    const uint64_t lo = m * total, hi = __umul64hi(m, total);         // hi < 2^24
+    if (shift < 64) return hi << (64 - shift) | lo >> shift;
+    return shift < 128 ? hi >> (shift - 64) : 0;
+}
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -184,10 +196,8 @@ __device__ __forceinline__ void draw(const VerifyParams &p, const Row &row, bool
     if (!total && rank == 0 && threadIdx.x == 0) *out = -1;
     before += warp_sum(lane < warp ? warp_total[lane] : 0);
     const uint64_t own = warp_total[warp];
-    // u * total < total, rounded down: a whole sum exceeds u * total where it
-    // exceeds this.  The product is rounded at 2^-53 of itself.
     const float u = fminf(fmaxf(__ldg(p.sample_u + b), 0.f), 1.f - 0x1p-24f);
-    const uint64_t target = (uint64_t)((double)u * (double)total);
+    const uint64_t target = share_of(u, total);
     if (target >= before && target < before + own) {
         const int id = rest ? find<true>(row, i0, i1, target - before, lane)
                             : find<false>(row, i0, i1, target - before, lane);
