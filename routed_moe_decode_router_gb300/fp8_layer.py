@@ -148,7 +148,7 @@ class Fp8AttentionLayer:
         flat = None if residual is None else residual.reshape(b * r, h)
         n = ops.rms_norm(x.reshape(b * r, h), self.norm, eps=self.eps, residual=flat,
                          quantize=True, keep=False)
-        rows = ops.matmul_fp8(n.q, n.scales, *self.qkv).view(b * r, -1, self.dim)
+        rows = ops.matmul_fp8(n.q, n.scales, *self.qkv).unflatten(1, (-1, self.dim))
         q, k, v = rows.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
         if self.rotate is not None:
             pos = lengths[:, None] - r + torch.arange(r, device=x.device)
@@ -157,7 +157,7 @@ class Fp8AttentionLayer:
         ops.kv_write(cache, k, v, slots.flatten())
         a = ops.attend_paged(q.unflatten(0, (b, r)), cache, table, lengths, scale=self.scale,
                              window=self.window, ws=ws)
-        out = torch.mm(a.view(b * r, -1), self.out.t()).view(b, r, h)
+        out = torch.mm(a.view(b * r, self.heads * self.dim), self.out.t()).view(b, r, h)
         return out, x if residual is None else n.residual.view(b, r, h)
 
 
