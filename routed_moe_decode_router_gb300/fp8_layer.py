@@ -101,16 +101,20 @@ class Fp8MoeLayer:
         return out, x if residual is None else n.residual
 
 
-def new_slots(table: torch.Tensor, lengths: torch.Tensor, rows: int, page: int) -> torch.Tensor:
+def new_slots(table: torch.Tensor, lengths: torch.Tensor, rows: int, page: int,
+              counts: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The slots [B, rows] (int32) of the last `rows` tokens of sequences whose
     pages are table [B, W] and whose lengths, these tokens among them, are lengths
-    [B]; -1 for positions before the first token or behind the table, and for page
-    numbers that no cache has."""
+    [B]; -1 for positions before the first token or behind the table, for page
+    numbers that no cache has, and with counts [B] for all but the last counts[b]
+    tokens."""
     pos = lengths[:, None] - rows + torch.arange(rows, device=table.device)
     at = torch.div(pos, page, rounding_mode="floor")
     ids = table.gather(1, at.clamp(0, table.shape[1] - 1).long()).long()
     slots = ids * page + pos % page
     there = (pos >= 0) & (at < table.shape[1]) & (ids >= 0) & (slots < 1 << 31)
+    if counts is not None:
+        there &= pos >= (lengths - counts)[:, None]
     return torch.where(there, slots, -1).to(torch.int32)
 
 
@@ -139,11 +143,15 @@ class Fp8AttentionLayer:
 
     def forward(self, x: torch.Tensor, cache: ops.KvCache, table: torch.Tensor,
                 lengths: torch.Tensor, residual: Optional[torch.Tensor] = None,
-                ws: Optional[ops.AttendWorkspace] = None):
+                ws: Optional[ops.AttendWorkspace] = None, counts: Optional[torch.Tensor] = None):
         """(out, residual) [B, R, H] bf16 of the last R tokens x of B sequences:
         their keys and values are written to the cache, and they see what it then
         holds.  table [B, W] and lengths [B] (the new tokens among them) as in
-        ops.attend_paged."""
+        ops.attend_paged.  counts [B]: how many of its R rows a sequence's new tokens
+        are, the last ones; without it all are, and overwrite what the cache has at
+        their positions.  The other rows are not written, and what comes out for
+        them is of no token.  Lengths are within the table: tokens behind it are not
+        written, and their rows see what the last of it do."""
         b, r, h = x.shape
         flat = None if residual is None else residual.reshape(b * r, h)
         n = ops.rms_norm(x.reshape(b * r, h), self.norm, eps=self.eps, residual=flat,
@@ -153,7 +161,7 @@ class Fp8AttentionLayer:
         if self.rotate is not None:
             pos = lengths[:, None] - r + torch.arange(r, device=x.device)
             q, k = self.rotate(q, k, pos.clamp(min=0).flatten())
-        slots = new_slots(table, lengths, r, cache.k.shape[2])
+        slots = new_slots(table, lengths, r, cache.k.shape[2], counts)
         ops.kv_write(cache, k, v, slots.flatten())
         a = ops.attend_paged(q.unflatten(0, (b, r)), cache, table, lengths, scale=self.scale,
                              window=self.window, ws=ws)
