@@ -96,7 +96,7 @@ moe_status check_cache(const moeop_kv_cache *c) {
     if (bad(c->k, 16) || bad(c->v, 16))
         return fail(MOE_ERR_INVALID_ARG, "the cache's k and v must be 16-byte aligned and not NULL");
     for (const int64_t stride : {c->k_stride, c->v_stride})
-        if (stride < places * c->dim || stride * es % 16 || stride * es >= (1LL << 40))
+        if (stride < places * c->dim || stride >= (1LL << 40) / es || stride * es % 16)
             return fail(MOE_ERR_INVALID_ARG,
                         "the cache's strides must be at least heads * page * dim and multiples of "
                         "16 bytes");
@@ -365,7 +365,7 @@ moe_status moeop_kv_write(const moeop_kv_cache *cache, const void *k, int64_t k_
         return fail(MOE_ERR_INVALID_ARG,
                     "k and v must be 16-byte aligned, slots 4-byte, none of them NULL");
     for (const int64_t stride : {k_stride, v_stride})
-        if (tokens > 1 && (stride < row || stride * es % 16 || stride >= (1LL << 40)))
+        if (tokens > 1 && (stride < row || stride >= (1LL << 40) || stride * es % 16))
             return fail(MOE_ERR_INVALID_ARG,
                         "the row strides must be at least heads * dim and multiples of 16 bytes");
     Range r[4];
