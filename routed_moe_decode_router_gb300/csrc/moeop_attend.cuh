@@ -148,6 +148,14 @@ __device__ __forceinline__ float inverse(float x) {    // within 2^-23
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// mbar_wait of all lanes together: none goes on where another gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(~0u, mbar_try_wait(bar, parity)))
+        if (__any_sync(~0u, clock64() - t0 > kWaitLimitCycles)) return false;
+    return true;
+}
 // exp2(a - b), 0 where a is -inf.
 __device__ __forceinline__ float ratio(float a, float b) {
     return a == -INFINITY ? 0.f : ex2(a - b);
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
         int page0 = 0, ids = -1;                   // lane i: the number of page page0 + i
         // which groups of the tiles under way are in the cache: the last loaded lowest
         uint32_t valid = 0;
-        bool lost = false;                         // a wait ran out
+        bool lost = false;                         // a wait ran out: no more loads
         auto pages = [&]() {                       // a tile ahead of their use
             page0 = lpage;
             ids = page0 + lane < p.width
@@ -514,7 +522,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                 scales(stage);
                 const uint32_t there = valid >> (kSubs * (kStages - 1)) & ((1u << kSubs) - 1);
                 if (!there) continue;
-                if (!mbar_wait(&bars[warp][now], phases >> now & 1)) {
+                if (!warp_wait(&bars[warp][now], phases >> now & 1)) {
                     lost = true;
                     if (lane == 0) atomicExch(p.status, (uint32_t)MOE_DEV_WAIT_TIMEOUT);
                 }
@@ -776,6 +784,10 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                 }
                 __syncwarp();                  // the stage may be filled again
             }
+
+            // no copy may still be on its way when the ring is used for sums, or left
+            if (lost)
+                for (int i = 0; i < kStages; ++i) warp_wait(&bars[warp][i], ~phases >> i & 1);
 
             // the sums of the rows' weights over the lanes
 #pragma unroll
