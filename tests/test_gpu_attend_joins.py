@@ -122,3 +122,52 @@ def test_a_workspace_from_call_to_call(held, dtype, dim, heads, group):
         assert not ws.buf[:COUNTERS].any()
         c.check(longest, 1, group, dtype, ws=ws)
         assert not ws.buf[:COUNTERS].any()
+
+
+def counts_of_a_page(cache, page, dim):
+    """Channel d of the value at place i of every page: 1 where i % dim == d."""
+    one = torch.nn.functional.one_hot(torch.arange(page, device="cuda") % dim, dim)
+    cache.v.copy_(one.to(cache.v.dtype).expand(cache.v.shape))
+
+
+@pytest.mark.parametrize("held,dtype", [(F8, BF), (HF, HF)])
+@pytest.mark.parametrize("length,window", [
+    (1 << 30, 0), ((1 << 30) - 100, 0), (1 << 30, 1000), (1 << 30, (1 << 30) - 7), ((1 << 29) + 33, 1 << 20)])
+def test_the_longest_sequences(held, dtype, length, window):
+    """2^30 tokens, on pages that come again and again."""
+    page, dim = 1024, 64
+    cache = ops.new_kv_cache(3, 1, page, dim, held)
+    counts_of_a_page(cache, page, dim)
+    if held == F8:
+        cache.k_scales.fill_(1)
+        cache.v_scales.fill_(1)
+    table = (torch.arange((1 << 30) // page, device="cuda").int() % 3)[None]
+    q = torch.ones(1, 2, 2, dim, dtype=dtype, device="cuda")
+    got = ops.attend_paged(q, cache, table, torch.tensor([length], dtype=torch.int32, device="cuda"),
+                           window=window).double()
+    for r in range(2):
+        last = length - 2 + r
+        lo = max(0, last - window + 1) if window else 0
+        d = torch.arange(dim, device="cuda")
+
+        def below(n):       # tokens of each channel below n: pages are whole rounds of dim
+            return n // dim + (d < n % dim).long()
+        want = (below(last + 1) - below(lo)).double() / (last + 1 - lo)
+        # a warp's share is exact (below 2^24 of them); 1216 shares, and the output
+        assert ((got[0, r] - want).abs() <= want * (half_step(dtype) * 1.01 + 1300 * 2.0 ** -24)).all()
+
+
+def test_the_most_sequences_and_heads():
+    """2048 sequences of 1024 heads: two million items of a few tokens, some of none."""
+    batch, heads, page, dim = 2048, 1024, 16, 64
+    cache = ops.new_kv_cache(3, heads, page, dim, BF)
+    counts_of_a_page(cache, page, dim)
+    sign = torch.where(torch.arange(heads, device="cuda") % 3 == 0, -1.0, 1.0)
+    cache.v.mul_(sign.to(BF)[:, None, None])
+    table = torch.randint(0, 3, (batch, 2), device="cuda").int()
+    n = torch.arange(batch, device="cuda").int() % 33
+    got = ops.attend_paged(torch.ones(batch, heads, dim, dtype=BF, device="cuda"), cache, table, n)
+    d = torch.arange(dim, device="cuda")
+    count = (d < n[:, None].clamp(max=16)).int() + (d < (n[:, None] - 16)).int()
+    want = (count.double() / n[:, None].clamp(min=1)).unsqueeze(1) * sign.double()[:, None]
+    assert ((got.double() - want).abs() <= want.abs() * (half_step(BF) * 1.01 + 2.0 ** -20)).all()
