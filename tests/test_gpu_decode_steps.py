@@ -129,3 +129,43 @@ def test_rows_of_a_verify_step_are_steps_of_one_token(dtype):
         one = ops.attend_paged(q[:, r], m.cache, m.table, n)
         assert ((one.double() - want[:, 0]).abs() <= bound[:, 0]).all()
         assert ((together[:, r].double() - want[:, 0]).abs() <= bound[:, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [F8, BF])
+@pytest.mark.parametrize("batch,length,window", [(1, 40, 0), (4, 300, 0), (3, 1000, 0), (40, 700, 0), (2, 5000, 90)])
+def test_each_call_sees_what_the_one_before_it_wrote(dtype, batch, length, window):
+    """Calls that start while the one before still runs: the same slots written, read
+    and attended to in turn, with other values each time, from one graph."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    steps, heads = 12, 4
+    width = length // PAGE + 1
+    cache = ops.new_kv_cache(batch * width, heads, PAGE, 128, dtype)
+    table = torch.randperm(batch * width, generator=g, device="cuda").view(batch, width).int()
+    lengths = torch.full((batch,), length, dtype=torch.int32, device="cuda")
+    every = fp8_layer.new_slots(table, lengths, length, PAGE).flatten()
+    last = fp8_layer.new_slots(table, lengths, 2, PAGE).flatten()
+    q = torch.randn(batch, 2, 8, 128, generator=g, device="cuda").to(BF)
+    rows = [torch.randn(2, len(s), heads, 128, generator=g, device="cuda").to(BF)
+            for s in (every, last) * steps]
+    ws = ops.AttendWorkspace(batch, 2, 8, heads, 128)
+
+    def run(wait):
+        out = []
+        for i in range(steps):
+            for j, slots in enumerate((every, last)):
+                ops.kv_write(cache, *rows[2 * i + j], slots)
+                wait()
+                for call in (lambda: ops.attend_paged(q, cache, table, lengths, window=window, ws=ws),
+                             lambda: torch.stack(ops.kv_read(cache, last))):
+                    out.append(call())
+                    wait()
+        return out
+    want = run(torch.cuda.synchronize)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(lambda: None)
+    for _ in range(5):
+        for t in got:
+            t.fill_(7)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
