@@ -5,7 +5,7 @@ import torch
 
 from routed_moe_decode_router_gb300 import ops
 from tests import decode_ref as D
-from tests.ops_ref import half_step
+from tests.ops_ref import F8, half_step
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -67,3 +67,22 @@ def test_scales_of_either_sign(lengths, dim, dtype):
     _, bound = D.attend(q, cache._replace(v_scales=cache.v_scales.abs()), table, n)
     got = ops.attend_paged(q, cache, table, n).double()
     assert ((got - want).abs() <= bound + want.abs() * half_step(dtype) * 1.01).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, torch.float32])
+def test_written_rows_with_nan_and_infinities(dtype):
+    """A NaN leaves its row's scale to the others; an infinity makes all of its row NaN."""
+    cache = ops.new_kv_cache(1, 2, 16, 64)
+    x = torch.randn(3, 2, 64, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dtype)
+    clean = x.clone()
+    x[0, 1, 5], x[1, 0, 63] = float("nan"), -float("inf")
+    clean[0, 1, 5] = 0
+    # (divided in 64 bits: PyTorch's GPU division by a number is a product with its inverse)
+    scales = (clean.double().abs().amax(-1) / 448).float()
+    want = (clean.double() / scales.double().unsqueeze(-1)).float().to(F8).float() * scales.unsqueeze(-1)
+    want[0, 1, 5], want[1, 0] = float("nan"), float("nan")
+    slots = torch.arange(3, dtype=torch.int32, device="cuda")
+    ops.kv_write(cache, x, x, slots)
+    for got in ops.kv_read(cache, slots, dtype=torch.float32):
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))
