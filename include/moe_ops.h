@@ -143,8 +143,10 @@ typedef struct moeop_kv_cache {
 
 /* Write the keys and values of `tokens` tokens, [tokens][heads][dim] with row
  * strides in elements, to their slots.  e4m3: scale = max(largest magnitude of
- * the dim, 1e-30) / 448, code = e4m3(value / scale), from any dtype; a cache of
- * 16 bits takes rows of its own type and keeps them as they are.  A slot outside
+ * the dim, 1e-30) / 448, code = e4m3(value / scale), from any dtype (a NaN is
+ * the code of NaN and leaves the scale to the others; an infinity makes all of
+ * its row NaN); a cache of 16 bits takes rows of its own type and keeps them as
+ * they are.  A slot outside
  * the cache is passed over.  The slots of a call are distinct: what a slot given
  * twice holds afterwards is not defined (the others are not touched by it).
  * k, v and their strides 16-byte aligned. */

@@ -12,8 +12,8 @@
 // million instructions for 16383 tokens, 21 -> 18 us).
 //
 // One GB300: 16383 tokens, 8 heads of 128, bf16 to e4m3 18 us in a stream of calls
-// (5.6 TB/s), 15.7 with the inputs in L2; 65536 read back 61 us (6.6 TB/s); 61 tokens
-// 1.8 us.
+// (5.6 TB/s), 15.7 with the inputs in L2; 65536 read back 61 us (6.6 TB/s), in fp32 120
+// (5.6), a bf16 cache's 80 (6.7), those in fp32 128 (6.3); 61 tokens 1.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -147,6 +147,7 @@ struct Place {
     }
 };
 
+// (A NaN does not count in amax: it becomes the code of NaN beside what the others are.)
 template <int CACHE, int IN>
 __global__ void __launch_bounds__(256, IN == MOEOP_FP32 ? 4 : 5) write_kernel(const CacheParams p) {
     using T = typename TypeOf<IN>::T;

@@ -19,9 +19,9 @@
 // cycle; whole numbers come out of fp32 additions of a constant whose last bit
 // is the step wanted (its sum's lower bits are the number), two at a time.
 //
-// One GB300: 1 sequence, 3 drafts, 32768 ids 5.3 us (launch, draft, its probability,
-// the row, the clusters' meeting, the id); 64 sequences, 131072 ids 20.4 us (3.3 TB/s),
-// 15.5 with the rows in L2; with a 64-bit sum per id 31.
+// One GB300: 1 sequence, 3 drafts, 32768 ids 5.0 us (launch, draft, its probability,
+// the row, the clusters' meeting, the id); 64 sequences, 131072 ids 20.3 us (3.3 TB/s),
+// 15.7 with the rows in L2; with a 64-bit sum per id 31.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -179,7 +179,8 @@ def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     """Write the keys and values [T, heads, dim] of T tokens to their slots
     (int32 [T]; one outside the cache, as -1, is passed over).  An e4m3 cache
     takes bf16, fp16 or fp32 and quantises: scale = max(amax of the dim, 1e-30) /
-    448; a cache of 16 bits takes its own type.  Tokens may be strided.  The slots
+    448 (a NaN leaves it to the others; an infinity makes its row NaN); a cache of
+    16 bits takes its own type.  Tokens may be strided.  The slots
     of a call are distinct: a slot given twice holds nothing defined."""
     if stream is not None:
         with torch.cuda.stream(stream):
