@@ -26,6 +26,8 @@
 // - e4m3 is widened to f16, exactly.  A key's scale multiplies its score, a value's
 //   its weight: weights are exp(s_j - m) vs_j, so the sums O have a running maximum
 //   of their own, of s_j + log |vs_j|, and keep the range of f16 whatever the scales.
+//   It is held as what it exceeds m by, and thresholds are on differences of scores:
+//   a sum of a score of 2^24 and a logarithm would be off by more than f16 has room.
 //   (mma.sync on e4m3 itself, Q in two e4m3 numbers, takes 80 instructions a tile more.)
 // - P is turned by movmatrix.  It enters as two 16-bit numbers, hi + lo (one f16
 //   number for e4m3 would be 2^-11 off, and saves no time).  f16 ends at 2^-24, and a
@@ -65,6 +67,7 @@ namespace attend {
 constexpr float kSlack = 8.f;    // what a score may exceed the running maximum by (log2)
 // f16 weights: at most 2^(kSlack + kRoom), hi off by 2^3 there, and 2^3 kLow = 2^15
 constexpr float kRoom = 7.f, kLow = 4096.f;
+static_assert(kRoom == 7.f, "2^-kRoom in worth()");
 
 // TYPE of the cache, D: dim, NT: groups of 8 query rows.
 // A tile is kTok tokens, 8 KB of keys and values where it can be; warps x stages of
@@ -81,7 +84,8 @@ struct Shape {
     static constexpr int kWarps = kRow == 512 ? 4 : 8;
     static constexpr int kStages = kRow == 64 ? 6 : 3;
     static constexpr int M = 8 * NT;
-    // a partial sum: m, l and the sums' own maximum of each row, then O^T
+    // a partial sum: m, l and what the sums' own maximum is above m (0 without e4m3) of
+    // each row, then O^T
     static constexpr int kStats = 3 * M, kPart = kStats + M * D;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int smem(int batch) { return 1024 + kRing + (2 * batch + 1) * 4; }
@@ -164,11 +168,12 @@ __device__ __forceinline__ float ratio(float a, float b) {
     return a == -INFINITY ? 0.f : ex2(a - b);
 }
 
-// What sums are worth in the end: 2^(otop - top) / l.
+// What sums are worth in the end: 2^above / l, with e4m3 (whose weights alone have the
+// factor 2^kRoom; above is -120 and more).
 template <bool F8>
-__device__ __forceinline__ float worth(float l, float top, float otop) {
+__device__ __forceinline__ float worth(float l, float above) {
     if (l == 0.f) return 0.f;
-    return (F8 && top != -INFINITY && otop != -INFINITY ? ex2(otop - top) : 1.f) * inverse(l);
+    return F8 && above != -INFINITY ? ex2(above) * (inverse(l) * 0x1p-7f) : inverse(l);
 }
 
 // An item begins with kEmpty tiles of nothing: what a warp does once for an item takes
@@ -504,12 +509,13 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             }
 
             float o[D / 16][NT][4];
-            float top[NT][2], sums[NT][2], otop[NT][2], lift[NT][2];
+            // m, l, with e4m3 what the sums' own maximum is above m, 2^(kRoom - that)
+            float top[NT][2], sums[NT][2], above[NT][2], lift[NT][2];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    top[j][c] = otop[j][c] = -INFINITY, sums[j][c] = 0.f, lift[j][c] = 1.f;
+                    top[j][c] = above[j][c] = -INFINITY, sums[j][c] = 0.f, lift[j][c] = 1.f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -605,36 +611,46 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            up |= x2[u][j][c] > top[j][c % 2] + kSlack;
-                            if (F8) up |= x2[u][j][c] + lv[u][c / 2] > otop[j][c % 2] + kSlack;
+                            const float m = top[j][c % 2];
+                            if (F8)
+                                up |= x2[u][j][c] - m >
+                                      fminf(kSlack, above[j][c % 2] + kSlack - lv[u][c / 2]);
+                            else      // (rounded down: a weight in f16 has no room above)
+                                up |= x2[u][j][c] > (kHalf ? __fadd_rd(m, kSlack) : m + kSlack);
                         }
                 if (__any_sync(~0u, up)) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float a = -INFINITY, b = -INFINITY;
+                            float a = -INFINITY;
 #pragma unroll
-                            for (int u = 0; u < kSubs; ++u) {
+                            for (int u = 0; u < kSubs; ++u)
                                 a = fmaxf(a, fmaxf(x2[u][j][c], x2[u][j][c + 2]));
-                                b = fmaxf(b, fmaxf(x2[u][j][c] + lv[u][0], x2[u][j][c + 2] + lv[u][1]));
-                            }
 #pragma unroll
-                            for (int d = 4; d < 32; d *= 2) {
+                            for (int d = 4; d < 32; d *= 2)
                                 a = fmaxf(a, __shfl_xor_sync(~0u, a, d));
-                                if (F8) b = fmaxf(b, __shfl_xor_sync(~0u, b, d));
-                            }
                             a = fmaxf(a, top[j][c]);
                             const float fade = ratio(top[j][c], a);
                             sums[j][c] *= fade;
-                            top[j][c] = a;
                             float ofade = fade;
                             if (F8) {
-                                b = fmaxf(b, otop[j][c]);
-                                ofade = ratio(otop[j][c], b);
-                                otop[j][c] = b;
-                                lift[j][c] = a == -INFINITY || b == -INFINITY ? 1.f : ex2(a - b);
+                                const float from = a == -INFINITY ? 0.f : a;
+                                float b = -INFINITY;
+#pragma unroll
+                                for (int u = 0; u < kSubs; ++u)
+                                    b = fmaxf(b, fmaxf(x2[u][j][c] - from + lv[u][0],
+                                                       x2[u][j][c + 2] - from + lv[u][1]));
+#pragma unroll
+                                for (int d = 4; d < 32; d *= 2)
+                                    b = fmaxf(b, __shfl_xor_sync(~0u, b, d));
+                                const float old = above[j][c] + (top[j][c] - from);
+                                b = fmaxf(b, old);
+                                ofade = ratio(old, b);
+                                above[j][c] = b;
+                                lift[j][c] = b == -INFINITY ? 1.f : ex2(kRoom - b);
                             }
+                            top[j][c] = a;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i)
                                 o[i][j][c] *= ofade, o[i][j][c + 2] *= ofade;
@@ -650,9 +666,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                         float w[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const float from = top[j][c % 2] == -INFINITY ? 0.f
-                                               : kHalf ? top[j][c % 2] - kRoom : top[j][c % 2];
-                            w[c] = ex2(x2[u][j][c] - from);
+                            const float from = top[j][c % 2] == -INFINITY ? 0.f : top[j][c % 2];
+                            const float x = x2[u][j][c] - from;
+                            w[c] = ex2(kHalf && !F8 ? x + kRoom : x);
                             sums[j][c % 2] += w[c];
                             // a token that is not seen weighs 0 whatever its scale holds
                             if (F8)
@@ -817,7 +833,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                         const int m = mb * M + j * 8 + 2 * t + c;
                         if (m >= m_all) continue;
                         // (not 1 / (l lift): that ends where values are below 2^-100)
-                        const float f = worth<F8>(sums[j][c], top[j][c], otop[j][c]);
+                        const float f = worth<F8>(sums[j][c], above[j][c]);
                         const int r = p.by_group.over(m);
                         uint16_t *row = static_cast<uint16_t *>(p.out) +
                                         (((int64_t)was.b * p.rows + r) * p.heads + was.h) *
@@ -856,7 +872,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
                             const int m = j * 8 + 2 * t + c;
                             of_rows[m] = top[j][c];
                             of_rows[M + m] = sums[j][c];
-                            of_rows[2 * M + m] = F8 ? otop[j][c] : top[j][c];
+                            of_rows[2 * M + m] = F8 ? above[j][c] : 0.f;
                         }
                     }
 #pragma unroll
@@ -932,24 +948,25 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
     // what each share's rows are worth: to the common maximum, or in the end
 #pragma unroll 1
     for (int m = warp; m < M; m += W) {
-        const float top = there ? stats[lane][0][m] : -INFINITY, l = there ? stats[lane][1][m] : 0.f,
-                    otop = there ? stats[lane][2][m] : -INFINITY;
-        float tall = top, oall = otop;
+        const float top = there ? stats[lane][0][m] : -INFINITY, l = there ? stats[lane][1][m] : 0.f;
+        float tall = top;
 #pragma unroll
         for (int d = 1; d < 2 * W; d *= 2) {          // to the end of the item's shares
-            const float a = __shfl_down_sync(~0u, tall, d), b = __shfl_down_sync(~0u, oall, d);
-            if (lane + d <= to) tall = fmaxf(tall, a), oall = fmaxf(oall, b);
+            const float a = __shfl_down_sync(~0u, tall, d);
+            if (lane + d <= to) tall = fmaxf(tall, a);
         }
-        tall = __shfl_sync(~0u, tall, from), oall = __shfl_sync(~0u, oall, from);
-        float sum_l = there ? l * ex2(top - finite(tall)) : 0.f;
+        tall = __shfl_sync(~0u, tall, from);
+        // what the sums' own maxima are above the common one
+        const float below = top - finite(tall), otop = there ? below + stats[lane][2][m] : -INFINITY;
+        float oall = otop, sum_l = there ? l * ex2(below) : 0.f;
 #pragma unroll
         for (int d = 1; d < 2 * W; d *= 2) {
-            const float a = __shfl_down_sync(~0u, sum_l, d);
-            if (lane + d <= to) sum_l += a;
+            const float a = __shfl_down_sync(~0u, sum_l, d), b = __shfl_down_sync(~0u, oall, d);
+            if (lane + d <= to) sum_l += a, oall = fmaxf(oall, b);
         }
-        sum_l = __shfl_sync(~0u, sum_l, from);
+        sum_l = __shfl_sync(~0u, sum_l, from), oall = __shfl_sync(~0u, oall, from);
         const float f = ex2(otop - finite(oall));
-        if (there) worth_of[lane][m] = inside ? f * worth<F8>(sum_l, tall, oall) : f;
+        if (there) worth_of[lane][m] = inside ? f * worth<F8>(sum_l, oall) : f;
         if (there && !inside && lane == from + __ffs(those) - 1) {
             float *out = blocks_out + (mine.start >= cs ? S::kPart : 0);
             out[m] = tall, out[M + m] = sum_l, out[2 * M + m] = oall;
@@ -1061,19 +1078,21 @@ __global__ void __launch_bounds__(Shape<TYPE, D, NT>::kWarps * 32, 1)
             for (int m = warp; m < M; m += W) {
                 const float *s = all + lane * S::kStats;
                 const bool in = lane < parts;
-                const float top = in ? s[m] : -INFINITY, otop = in ? s[2 * M + m] : -INFINITY;
-                float tall = top, oall = otop;
+                const float top = in ? s[m] : -INFINITY;
+                float tall = top;
+#pragma unroll
+                for (int d = kJoin / 2; d; d >>= 1)
+                    tall = fmaxf(tall, __shfl_xor_sync(~0u, tall, d));
+                const float below = top - finite(tall), otop = in ? below + s[2 * M + m] : -INFINITY;
+                float oall = otop, l = in ? s[M + m] * ex2(below) : 0.f;
 #pragma unroll
                 for (int d = kJoin / 2; d; d >>= 1) {
-                    tall = fmaxf(tall, __shfl_xor_sync(~0u, tall, d));
+                    l += __shfl_xor_sync(~0u, l, d);
                     oall = fmaxf(oall, __shfl_xor_sync(~0u, oall, d));
                 }
-                float l = in ? s[M + m] * ex2(top - finite(tall)) : 0.f;
-#pragma unroll
-                for (int d = kJoin / 2; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
                 if (in) {
                     const float f = ex2(otop - finite(oall));
-                    worth_of[lane][m] = whole ? f * worth<F8>(l, tall, oall) : f;
+                    worth_of[lane][m] = whole ? f * worth<F8>(l, oall) : f;
                 }
                 if (lane == 0 && !whole) {
                     float *out = part(0);
@@ -1165,23 +1184,24 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p) {
     __syncthreads();
     for (int m = warp; m < M; m += 8) {
         float top = -INFINITY, otop = -INFINITY, l = 0.f;
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, all[i * kStats + m]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        const float tref = top == -INFINITY ? 0.f : top;
+        // what the sums' own maxima are above the common one
         for (int i = lane; i < parts; i += 32) {
-            top = fmaxf(top, all[i * kStats + m]);
-            otop = fmaxf(otop, all[i * kStats + 2 * M + m]);
+            float *s = all + i * kStats;
+            const float below = s[m] - tref;
+            l = fmaf(s[M + m], ex2(below), l);
+            s[2 * M + m] += below;
+            otop = fmaxf(otop, s[2 * M + m]);
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            l += __shfl_xor_sync(~0u, l, d);
             otop = fmaxf(otop, __shfl_xor_sync(~0u, otop, d));
         }
-        const float tref = top == -INFINITY ? 0.f : top, oref = otop == -INFINITY ? 0.f : otop;
-        for (int i = lane; i < parts; i += 32) {
-            const float *s = all + i * kStats;
-            l = fmaf(s[M + m], ex2(s[m] - tref), l);
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-        const float w = worth<F8>(l, top, otop);
+        const float w = worth<F8>(l, otop), oref = otop == -INFINITY ? 0.f : otop;
         for (int i = lane; i < parts; i += 32) {
             float *s = all + i * kStats;
             s[m] = ex2(s[2 * M + m] - oref) * w;
