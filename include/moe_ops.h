@@ -146,10 +146,9 @@ typedef struct moeop_kv_cache {
  * the dim, 1e-30) / 448, code = e4m3(value / scale), from any dtype (a NaN is
  * the code of NaN and leaves the scale to the others; an infinity makes all of
  * its row NaN); a cache of 16 bits takes rows of its own type and keeps them as
- * they are.  A slot outside
- * the cache is passed over.  The slots of a call are distinct: what a slot given
- * twice holds afterwards is not defined (the others are not touched by it).
- * k, v and their strides 16-byte aligned. */
+ * they are.  A slot outside the cache is passed over.  The slots of a call are
+ * distinct: what a slot given twice holds afterwards is not defined (the others
+ * are not touched by it).  k, v and their strides 16-byte aligned. */
 MOE_API moe_status moeop_kv_write(const moeop_kv_cache *cache, const void *k, int64_t k_stride,
                                   const void *v, int64_t v_stride, int dtype,
                                   const int32_t *slots, int tokens, void *stream);

@@ -114,6 +114,8 @@ def new_slots(table: torch.Tensor, lengths: torch.Tensor, rows: int, page: int,
     slots = ids * page + pos % page
     there = (pos >= 0) & (at < table.shape[1]) & (ids >= 0) & (slots < 1 << 31)
     if counts is not None:
+        if counts.shape != lengths.shape:
+            raise ValueError("counts has shape %s, expected %s" % (tuple(counts.shape), tuple(lengths.shape)))
         there &= pos >= (lengths - counts)[:, None]
     return torch.where(there, slots, -1).to(torch.int32)
 
